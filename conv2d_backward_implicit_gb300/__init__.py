@@ -1,6 +1,7 @@
 """GB300-native conv2d input gradient (dgrad) as an implicit GEMM, with the
-strided forward convolution, the fused RMSNorm + matmul and the attention
-gradient with respect to V beside it.
+strided forward convolution, the fused RMSNorm + matmul, the attention gradient
+with respect to V, causal attention over packed sequences (forward and
+backward) and the gated residual RMSNorm (forward and backward) beside it.
 
 The compute path is the C-ABI library ``libconv2d_grad_input.so`` built from
 ``csrc/`` for sm_103a; :mod:`.binding` marshals arguments to it.  Importing
@@ -19,4 +20,8 @@ from .binding import (  # noqa: F401
     RmsParams, rmsnorm_matmul, rmsnorm_matmul_check_errors, rmsnorm_matmul_select_kernel,
     rmsnorm_matmul_set_kernel,
     MhaParams, mha_grad_v, mha_grad_v_check_errors, mha_grad_v_select_kernel, mha_grad_v_set_kernel,
+    MhaPackedParams, mha_packed_backward, mha_packed_backward_select_kernel, mha_packed_check_errors,
+    mha_packed_forward, mha_packed_forward_select_kernel, mha_packed_set_kernel, mha_packed_workspace_size,
+    RESIDUAL_GATE_CHANNEL, RESIDUAL_GATE_ELEMENT, RESIDUAL_GATE_NONE, ResidualRmsnormParams,
+    residual_rmsnorm_backward, residual_rmsnorm_forward, residual_rmsnorm_workspace_size,
 )

@@ -1,5 +1,6 @@
-"""ctypes binding for the C ABI in include/conv2d_grad_input.h, include/rmsnorm_matmul.h
-and include/mha_grad_v.h (argument marshalling only).
+"""ctypes binding for the C ABI in include/conv2d_grad_input.h, include/rmsnorm_matmul.h,
+include/mha_grad_v.h, include/mha_packed.h and include/residual_rmsnorm.h (argument
+marshalling only).
 
 Every function here has the name of the C entry point it calls, accepts torch
 tensors (or raw integer addresses) for the buffers, and raises
@@ -49,6 +50,22 @@ MHA_FIELDS = ("q_seq", "kv_seq", "num_heads", "num_kv_heads", "head_dim", "windo
 class MhaParams(ctypes.Structure):
     """mha_grad_v_params: six uint32 fields in the header's order."""
     _fields_ = [(name, ctypes.c_uint32) for name in MHA_FIELDS]
+
+
+class MhaPackedParams(ctypes.Structure):
+    """mha_packed_params: nine uint32 fields in the header's order (strides in elements, 0: dense)."""
+    _fields_ = [(name, ctypes.c_uint32) for name in
+                ("tokens", "num_seqs", "num_heads", "num_kv_heads", "head_dim", "window_size", "q_stride",
+                 "k_stride", "v_stride")]
+
+
+RESIDUAL_GATE_NONE, RESIDUAL_GATE_CHANNEL, RESIDUAL_GATE_ELEMENT = 0, 1, 2
+
+
+class ResidualRmsnormParams(ctypes.Structure):
+    """residual_rmsnorm_params: m, n, gate_kind (uint32), eps and scale (float)."""
+    _fields_ = [("m", ctypes.c_uint32), ("n", ctypes.c_uint32), ("gate_kind", ctypes.c_uint32),
+                ("eps", ctypes.c_float), ("scale", ctypes.c_float)]
 
 
 class DgradError(RuntimeError):
@@ -130,6 +147,28 @@ def library() -> ctypes.CDLL:
             lib.mha_grad_v_set_kernel.restype = I
             lib.mha_grad_v_check_errors.argtypes = [P]
             lib.mha_grad_v_check_errors.restype = I
+            KP = ctypes.POINTER(MhaPackedParams)
+            lib.mha_packed_forward.argtypes = [P] * 6 + [KP, I, P]
+            lib.mha_packed_forward.restype = I
+            lib.mha_packed_workspace_size.argtypes = [KP, I]
+            lib.mha_packed_workspace_size.restype = S
+            lib.mha_packed_backward.argtypes = [P] * 11 + [S, KP, I, P]
+            lib.mha_packed_backward.restype = I
+            lib.mha_packed_forward_select_kernel.argtypes = [P] * 4 + [KP, I]
+            lib.mha_packed_forward_select_kernel.restype = I
+            lib.mha_packed_backward_select_kernel.argtypes = [P] * 8 + [KP, I]
+            lib.mha_packed_backward_select_kernel.restype = I
+            lib.mha_packed_set_kernel.argtypes = [I]
+            lib.mha_packed_set_kernel.restype = I
+            lib.mha_packed_check_errors.argtypes = [P]
+            lib.mha_packed_check_errors.restype = I
+            NP = ctypes.POINTER(ResidualRmsnormParams)
+            lib.residual_rmsnorm_forward.argtypes = [P] * 8 + [NP, I, P]
+            lib.residual_rmsnorm_forward.restype = I
+            lib.residual_rmsnorm_workspace_size.argtypes = [NP, I]
+            lib.residual_rmsnorm_workspace_size.restype = S
+            lib.residual_rmsnorm_backward.argtypes = [P] * 14 + [S, NP, I, P]
+            lib.residual_rmsnorm_backward.restype = I
             _lib = lib
     return _lib
 
@@ -357,3 +396,136 @@ def mha_grad_v_set_kernel(kernel: int) -> int:
 def mha_grad_v_check_errors(stream=None) -> int:
     """Returns the status (0, DGRAD_ERR_TIMEOUT = 6 or DGRAD_ERR_CUDA = 5) without raising."""
     return int(library().mha_grad_v_check_errors(_stream(stream)))
+
+
+def _dense(dtype: str | None, *buffers):
+    """Addresses of dense buffers given as (x, name, elements) or (x, name, elements, dtype): the checks of
+    _addr, with one comparison per property for a torch tensor that passes them."""
+    import torch
+    device, out = -1, []
+    for x, name, numel, *own in buffers:
+        t = own[0] if own else dtype
+        if isinstance(x, torch.Tensor) and x.is_cuda:
+            if device < 0:
+                device = torch.cuda.current_device()
+            if (x.get_device() == device and x.numel() == numel and x.is_contiguous()
+                    and (t is None or x.dtype is getattr(torch, t))):
+                out.append(x.data_ptr())
+                continue
+        out.append(_addr(x, name, t, numel))
+    return out
+
+
+def _token_rows(x, name: str, dtype: str | None, tokens: int, heads: int, head_dim: int, stride: int):
+    """Address of a [tokens, heads, head_dim] tensor whose tokens are ``stride`` elements apart (0: dense)."""
+    dense = heads * head_dim
+    row = stride or dense
+    shape = getattr(x, "shape", None)
+    if row == dense or shape is None:
+        return _dense(dtype, (x, name, tokens * dense))[0]
+    if tuple(shape) != (tokens, heads, head_dim):
+        raise ValueError(f"{name} must have shape {(tokens, heads, head_dim)} for these params (got {tuple(shape)})")
+    for have, want, size in zip(x.stride(), (row, head_dim, 1), shape):
+        if size > 1 and have != want:
+            raise ValueError(f"{name} must have strides {(row, head_dim, 1)} for these params (got {x.stride()})")
+    _addr(x[0].reshape(-1), name, dtype, dense)  # the device and the element type
+    return x.data_ptr()
+
+
+def _packed_qkv(q, k, v, p: MhaPackedParams, t: str | None):
+    n, h, g, d = p.tokens, p.num_heads, p.num_kv_heads, p.head_dim
+    return [_token_rows(q, "q", t, n, h, d, p.q_stride), _token_rows(k, "k", t, n, g, d, p.k_stride),
+            _token_rows(v, "v", t, n, g, d, p.v_stride)]
+
+
+def mha_packed_forward(q, k, v, seq_offsets, o, lse, params: MhaPackedParams, dtype: int, stream=None) -> None:
+    """O and LSE of causal attention over packed sequences (include/mha_packed.h)."""
+    t, rows = _in_dtype(dtype), params.tokens * params.num_heads
+    rc = library().mha_packed_forward(
+        *_packed_qkv(q, k, v, params, t),
+        *_dense(t, (seq_offsets, "seq_offsets", params.num_seqs + 1, "int32"), (o, "o", rows * params.head_dim),
+                (lse, "lse", rows * 2, "float32")),
+        ctypes.byref(params), int(dtype), _stream(stream))
+    _check(rc, "mha_packed_forward")
+
+
+def mha_packed_workspace_size(params: MhaPackedParams, dtype: int) -> int:
+    return int(library().mha_packed_workspace_size(ctypes.byref(params), int(dtype)))
+
+
+def mha_packed_backward(q, k, v, o, d_out, lse, seq_offsets, dq, dk, dv, workspace, workspace_bytes: int,
+                        params: MhaPackedParams, dtype: int, stream=None) -> None:
+    """dQ, dK and dV of causal attention over packed sequences (include/mha_packed.h)."""
+    t, rows = _in_dtype(dtype), params.tokens * params.num_heads
+    n_q, n_kv = rows * params.head_dim, params.tokens * params.num_kv_heads * params.head_dim
+    rc = library().mha_packed_backward(
+        *_packed_qkv(q, k, v, params, t),
+        *_dense(t, (o, "o", n_q), (d_out, "d_out", n_q), (lse, "lse", rows * 2, "float32"),
+                (seq_offsets, "seq_offsets", params.num_seqs + 1, "int32"), (dq, "dq", n_q), (dk, "dk", n_kv),
+                (dv, "dv", n_kv)),
+        _addr(workspace, "workspace", min_bytes=int(workspace_bytes)), int(workspace_bytes), ctypes.byref(params),
+        int(dtype), _stream(stream))
+    _check(rc, "mha_packed_backward")
+
+
+def mha_packed_forward_select_kernel(q, k, v, o, params: MhaPackedParams, dtype: int) -> int:
+    """DGRAD_KERNEL_TC (1) or DGRAD_KERNEL_SIMT (2) for these buffers, or a negative status."""
+    t = _in_dtype(dtype)
+    return int(library().mha_packed_forward_select_kernel(
+        *_packed_qkv(q, k, v, params, t), *_dense(t, (o, "o", params.tokens * params.num_heads * params.head_dim)),
+        ctypes.byref(params), int(dtype)))
+
+
+def mha_packed_backward_select_kernel(q, k, v, o, d_out, dq, dk, dv, params: MhaPackedParams, dtype: int) -> int:
+    """DGRAD_KERNEL_TC (1) or DGRAD_KERNEL_SIMT (2) for these buffers, or a negative status."""
+    t = _in_dtype(dtype)
+    n_q = params.tokens * params.num_heads * params.head_dim
+    n_kv = params.tokens * params.num_kv_heads * params.head_dim
+    return int(library().mha_packed_backward_select_kernel(
+        *_packed_qkv(q, k, v, params, t),
+        *_dense(t, (o, "o", n_q), (d_out, "d_out", n_q), (dq, "dq", n_q), (dk, "dk", n_kv), (dv, "dv", n_kv)),
+        ctypes.byref(params), int(dtype)))
+
+
+def mha_packed_set_kernel(kernel: int) -> int:
+    return int(library().mha_packed_set_kernel(int(kernel)))
+
+
+def mha_packed_check_errors(stream=None) -> int:
+    """Returns the status without raising: 0, DGRAD_ERR_CUDA = 5, DGRAD_ERR_TIMEOUT = 6, or
+    DGRAD_ERR_INVALID_ARG = 1 for malformed seq_offsets."""
+    return int(library().mha_packed_check_errors(_stream(stream)))
+
+
+def residual_rmsnorm_forward(f, x, gate, w_post, w_pre, h, y, rstd, params: ResidualRmsnormParams, dtype: int,
+                             stream=None) -> None:
+    """H = X + scale * gate * RmsNorm(F, W_post) and Y = RmsNorm(H, W_pre) (include/residual_rmsnorm.h).
+    ``gate`` is None for RESIDUAL_GATE_NONE; ``rstd`` may be None."""
+    t, m, n = _in_dtype(dtype), params.m, params.n
+    rc = library().residual_rmsnorm_forward(
+        *_dense(t, (f, "f", m * n), (x, "x", m * n),
+                (gate, "gate", n if params.gate_kind == RESIDUAL_GATE_CHANNEL else m * n), (w_post, "w_post", n),
+                (w_pre, "w_pre", n), (h, "h", m * n), (y, "y", m * n), (rstd, "rstd", 2 * m, "float32")),
+        ctypes.byref(params), int(dtype), _stream(stream))
+    _check(rc, "residual_rmsnorm_forward")
+
+
+def residual_rmsnorm_workspace_size(params: ResidualRmsnormParams, dtype: int) -> int:
+    return int(library().residual_rmsnorm_workspace_size(ctypes.byref(params), int(dtype)))
+
+
+def residual_rmsnorm_backward(f, h, gate, w_post, w_pre, rstd, dy, dh, df, dx, dgate, dw_post, dw_pre, workspace,
+                              workspace_bytes: int, params: ResidualRmsnormParams, dtype: int, stream=None) -> None:
+    """Gradients of residual_rmsnorm_forward (include/residual_rmsnorm.h).  ``dh`` may be None; ``gate`` and
+    ``dgate`` are None for RESIDUAL_GATE_NONE."""
+    t, m, n = _in_dtype(dtype), params.m, params.n
+    channel = params.gate_kind == RESIDUAL_GATE_CHANNEL
+    n_gate = n if channel else m * n
+    rc = library().residual_rmsnorm_backward(
+        *_dense(t, (f, "f", m * n), (h, "h", m * n), (gate, "gate", n_gate), (w_post, "w_post", n),
+                (w_pre, "w_pre", n), (rstd, "rstd", 2 * m, "float32"), (dy, "dy", m * n), (dh, "dh", m * n),
+                (df, "df", m * n), (dx, "dx", m * n), (dgate, "dgate", n_gate, "float32" if channel else t),
+                (dw_post, "dw_post", n, "float32"), (dw_pre, "dw_pre", n, "float32")),
+        _addr(workspace, "workspace", min_bytes=int(workspace_bytes)), int(workspace_bytes), ctypes.byref(params),
+        int(dtype), _stream(stream))
+    _check(rc, "residual_rmsnorm_backward")

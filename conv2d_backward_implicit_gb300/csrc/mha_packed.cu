@@ -1,0 +1,156 @@
+// mha_packed.cu -- the C entry points of causal attention over packed sequences
+// (include/mha_packed.h): argument checks, kernel choice and launches.
+#include <atomic>
+
+#include "mha_packed_internal.cuh"
+#include "nvtx_range.h"
+
+namespace mhapk {
+
+unsigned take_simt_error(cudaError_t &e);
+
+namespace {
+
+std::atomic<int> g_kernel_choice{DGRAD_KERNEL_AUTO};
+
+bool aligned(const void *ptr, uintptr_t a) { return (reinterpret_cast<uintptr_t>(ptr) & (a - 1)) == 0; }
+
+int64_t row_of(uint32_t stride, uint32_t heads, uint32_t hd) {
+    return stride ? (int64_t)stride : (int64_t)heads * hd;
+}
+
+int validate(const mha_packed_params *p, int dtype) {
+    if (!p) return DGRAD_ERR_INVALID_ARG;
+    if (dtype != DGRAD_F32 && dtype != DGRAD_BF16 && dtype != DGRAD_F16) return DGRAD_ERR_INVALID_ARG;
+    if (p->tokens == 0 || p->num_heads == 0 || p->num_kv_heads == 0 || p->head_dim == 0 ||
+        p->num_heads % p->num_kv_heads != 0)
+        return DGRAD_ERR_SHAPE;
+    if (p->head_dim > 256u || p->tokens > (1u << 30) || p->num_seqs > (1u << 30) ||
+        p->num_heads > (uint32_t)INT32_MAX / 256)
+        return DGRAD_ERR_UNSUPPORTED;
+    const int64_t qd = (int64_t)p->num_heads * p->head_dim, kd = (int64_t)p->num_kv_heads * p->head_dim;
+    if (row_of(p->q_stride, p->num_heads, p->head_dim) < qd || row_of(p->k_stride, p->num_kv_heads, p->head_dim) < kd ||
+        row_of(p->v_stride, p->num_kv_heads, p->head_dim) < kd)
+        return DGRAD_ERR_SHAPE;
+    // Thread blocks of the smallest tile (32 rows) and most heads; also the warps of the delta kernel.
+    if (unit_bound(p, 32) * p->num_heads > INT32_MAX || (int64_t)p->tokens * p->num_heads / 8 > INT32_MAX)
+        return DGRAD_ERR_UNSUPPORTED;
+    return DGRAD_OK;
+}
+
+// The tensor-core kernels' conditions on params and the tensors they view through TMA or store in 16-byte pieces.
+template <typename... P>
+bool tc_applies(const mha_packed_params *p, int dtype, const P *...ptr) {
+    return dtype != DGRAD_F32 && p->head_dim % 8 == 0 && p->head_dim <= 128 && p->q_stride % 8 == 0 &&
+           p->k_stride % 8 == 0 && p->v_stride % 8 == 0 && (aligned(ptr, 16) && ...);
+}
+
+int choose(bool tc) {
+    const int choice = g_kernel_choice.load();
+    if (choice == DGRAD_KERNEL_SIMT) return DGRAD_KERNEL_SIMT;
+    if (choice == DGRAD_KERNEL_TC) return tc ? DGRAD_KERNEL_TC : -DGRAD_ERR_UNSUPPORTED;
+    return tc ? DGRAD_KERNEL_TC : DGRAD_KERNEL_SIMT;
+}
+
+template <typename... P>
+int select(const mha_packed_params *p, int dtype, const P *...ptr) {
+    if (((ptr == nullptr) || ...)) return -DGRAD_ERR_INVALID_ARG;
+    const int v = validate(p, dtype);
+    if (v != DGRAD_OK) return -v;
+    const uintptr_t e = dtype == DGRAD_F32 ? 4 : 2;
+    if (!(aligned(ptr, e) && ...)) return -DGRAD_ERR_ALIGNMENT;
+    return choose(tc_applies(p, dtype, ptr...));
+}
+
+Args make_args(const void *q, const void *k, const void *v, const int32_t *off, const mha_packed_params *p) {
+    Args a{};
+    a.q = q, a.k = k, a.v = v, a.off = off;
+    a.tokens = (int)p->tokens;
+    a.seqs = (int)p->num_seqs;
+    a.nh = (int)p->num_heads;
+    a.nkv = (int)p->num_kv_heads;
+    a.hpk = a.nh / a.nkv;
+    a.hd = (int)p->head_dim;
+    a.window = p->window_size >= p->tokens ? 0 : (int)p->window_size;  // a window over everything masks nothing
+    a.qs = row_of(p->q_stride, p->num_heads, p->head_dim);
+    a.ks = row_of(p->k_stride, p->num_kv_heads, p->head_dim);
+    a.vs = row_of(p->v_stride, p->num_kv_heads, p->head_dim);
+    a.scale = 1.0f / sqrtf((float)a.hd);
+    return a;
+}
+
+size_t workspace_bytes_of(const mha_packed_params *p) {
+    return (size_t)p->tokens * p->num_heads * sizeof(float2);
+}
+
+}  // namespace
+}  // namespace mhapk
+
+extern "C" {
+
+int mha_packed_forward(const void *q, const void *k, const void *v, const int32_t *seq_offsets, void *o, float *lse,
+                       const mha_packed_params *p, int dtype, struct CUstream_st *stream) {
+    using namespace mhapk;
+    dgrad::NvtxRange range("mha_packed_forward");
+    const int kern = select(p, dtype, q, k, v, static_cast<const void *>(o));
+    if (kern < 0) return -kern;
+    if (!seq_offsets || !lse) return DGRAD_ERR_INVALID_ARG;
+    if (!aligned(seq_offsets, 4) || !aligned(lse, 4)) return DGRAD_ERR_ALIGNMENT;
+    Args a = make_args(q, k, v, seq_offsets, p);
+    a.out = o;
+    a.lse = lse;
+    return forward_simt(a, p, dtype, static_cast<cudaStream_t>(stream));
+}
+
+size_t mha_packed_workspace_size(const mha_packed_params *p, int dtype) {
+    return mhapk::validate(p, dtype) == DGRAD_OK ? mhapk::workspace_bytes_of(p) : 0;
+}
+
+int mha_packed_backward(const void *q, const void *k, const void *v, const void *o, const void *d_out,
+                        const float *lse, const int32_t *seq_offsets, void *dq, void *dk, void *dv, void *workspace,
+                        size_t workspace_bytes, const mha_packed_params *p, int dtype, struct CUstream_st *stream) {
+    using namespace mhapk;
+    dgrad::NvtxRange range("mha_packed_backward");
+    const int kern = select(p, dtype, q, k, v, o, d_out, static_cast<const void *>(dq), static_cast<const void *>(dk),
+                            static_cast<const void *>(dv));
+    if (kern < 0) return -kern;
+    if (!seq_offsets || !lse || !workspace) return DGRAD_ERR_INVALID_ARG;
+    if (!aligned(seq_offsets, 4) || !aligned(lse, 4) || !aligned(workspace, 16)) return DGRAD_ERR_ALIGNMENT;
+    if (workspace_bytes < workspace_bytes_of(p)) return DGRAD_ERR_WORKSPACE;
+    Args a = make_args(q, k, v, seq_offsets, p);
+    a.o = o, a.go = d_out;
+    a.lse_in = lse;
+    a.dq = dq, a.dk = dk, a.dv = dv;
+    a.stats = static_cast<float2 *>(workspace);
+    return backward_simt(a, p, dtype, static_cast<cudaStream_t>(stream));
+}
+
+int mha_packed_forward_select_kernel(const void *q, const void *k, const void *v, const void *o,
+                                     const mha_packed_params *p, int dtype) {
+    return mhapk::select(p, dtype, q, k, v, o);
+}
+
+int mha_packed_backward_select_kernel(const void *q, const void *k, const void *v, const void *o, const void *d_out,
+                                      const void *dq, const void *dk, const void *dv, const mha_packed_params *p,
+                                      int dtype) {
+    return mhapk::select(p, dtype, q, k, v, o, d_out, dq, dk, dv);
+}
+
+int mha_packed_set_kernel(int kernel) {
+    if (kernel != DGRAD_KERNEL_AUTO && kernel != DGRAD_KERNEL_TC && kernel != DGRAD_KERNEL_SIMT)
+        return DGRAD_ERR_INVALID_ARG;
+    return mhapk::g_kernel_choice.exchange(kernel);
+}
+
+int mha_packed_check_errors(struct CUstream_st *stream) {
+    using namespace mhapk;
+    cudaError_t e = cudaStreamSynchronize(static_cast<cudaStream_t>(stream));
+    const unsigned word = take_simt_error(e);
+    if (e != cudaSuccess) {
+        (void)cudaGetLastError();
+        return DGRAD_ERR_CUDA;
+    }
+    return word & kErrTimeout ? DGRAD_ERR_TIMEOUT : word & kErrOffsets ? DGRAD_ERR_INVALID_ARG : DGRAD_OK;
+}
+
+}  // extern "C"

@@ -1,0 +1,146 @@
+// mha_packed_internal.cuh -- what the packed-attention translation units share:
+// the launch arguments, the device-side walk from a work-unit index to a
+// (sequence, tile) pair, and the row-by-row recomputation of a tile.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include <cmath>
+#include <cstdint>
+
+#include "mha_packed.h"
+
+namespace mhapk {
+
+// Bits of the device error words.
+constexpr unsigned kErrTimeout = 1u, kErrOffsets = 2u;
+
+struct Args {
+    const void *q, *k, *v;
+    const int32_t *off;  // [seqs + 1]
+    const void *o, *go;  // backward inputs
+    void *out;           // forward O
+    void *dq, *dk, *dv;
+    const float *lse_in;
+    float *lse;
+    float2 *stats;  // workspace: [heads][tokens] (statistic, delta)
+    int tokens, seqs, nh, nkv, hpk, hd, window;
+    int64_t qs, ks, vs;  // elements between two tokens' rows
+    float scale;         // 1 / sqrt(head_dim)
+};
+
+struct Unit {
+    int begin, len;  // the sequence's first row and its length
+    int p0;          // the tile's first row within the sequence
+    bool pad;        // rows of no sequence
+    bool live;       // false: this index names no tile
+};
+
+// Upper bound of the number of tiles of `rows` rows over all sequences and the
+// (up to two) runs of rows outside them: sum of ceil(len / rows) is at most
+// floor(tokens / rows) + the number of segments.
+inline int64_t unit_bound(const mha_packed_params *p, int rows) {
+    return (int64_t)p->tokens / rows + p->num_seqs + 2;
+}
+
+__device__ __forceinline__ int clamp_row(int x, int tokens) { return x < 0 ? 0 : (x > tokens ? tokens : x); }
+
+// Segment i: sequence i, or (i == seqs, seqs + 1) the rows before the first and after the last sequence.
+__device__ __forceinline__ void segment(const Args &a, int i, int &begin, int &len) {
+    int lo, hi;
+    if (i < a.seqs) {
+        lo = __ldg(a.off + i), hi = __ldg(a.off + i + 1);
+    } else if (i == a.seqs) {
+        lo = 0, hi = __ldg(a.off);
+    } else {
+        lo = __ldg(a.off + a.seqs), hi = a.tokens;
+    }
+    begin = clamp_row(lo, a.tokens);
+    hi = clamp_row(hi, a.tokens);
+    len = hi > begin ? hi - begin : 0;
+}
+
+// Tile `u` of `rows` rows, every thread of the block calling (blockDim.x a
+// multiple of 32, at most 1024).  Segments are numbered as above, the tiles of one
+// in descending order, so that under the causal mask the tiles with the most keys
+// come first.  Each thread adds up the tiles of a run of segments, the block scans
+// those sums, and the thread whose run holds `u` walks it: two rounds of loads for
+// any number of sequences.  `check`: raise the error flag where offsets are malformed.
+__device__ __forceinline__ Unit find_unit(const Args &a, int64_t u, int rows, bool check, unsigned *error) {
+    __shared__ int64_t warp_sum[32];
+    __shared__ Unit found;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, n = a.seqs + 2;
+    const int per = (n + (int)blockDim.x - 1) / (int)blockDim.x;
+    const int i0 = tid * per < n ? tid * per : n, i1 = i0 + per < n ? i0 + per : n;
+    int64_t sum = 0;
+    for (int i = i0; i < i1; ++i) {
+        int begin, len;
+        segment(a, i, begin, len);
+        sum += (len + rows - 1) / rows;
+        if (check && i < a.seqs) {
+            const int lo = __ldg(a.off + i), hi = __ldg(a.off + i + 1);
+            if (lo < 0 || hi < lo || hi > a.tokens) atomicOr(error, kErrOffsets);
+        }
+    }
+    int64_t incl = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int64_t x = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += x;
+    }
+    if (lane == 31) warp_sum[warp] = incl;
+    if (tid == 0) found.live = false;
+    __syncthreads();
+    for (int w = 0; w < warp; ++w) incl += warp_sum[w];
+    int64_t at = incl - sum;
+    if (u >= at && u < incl)
+        for (int i = i0; i < i1; ++i) {
+            int begin, len;
+            segment(a, i, begin, len);
+            const int tiles = (len + rows - 1) / rows;
+            if (u < at + tiles) {
+                found.begin = begin;
+                found.len = len;
+                found.p0 = (tiles - 1 - (int)(u - at)) * rows;
+                found.pad = i >= a.seqs;
+                found.live = true;
+                break;
+            }
+            at += tiles;
+        }
+    __syncthreads();
+    return found;
+}
+
+template <typename T>
+__device__ __forceinline__ float to_f(T v) {
+    if constexpr (sizeof(T) == 4) {
+        return v;
+    } else {
+        return (float)v;
+    }
+}
+template <typename T>
+__device__ __forceinline__ T from_f(float v) {
+    if constexpr (sizeof(T) == 4) {
+        return v;
+    } else {
+        return (T)v;
+    }
+}
+
+__device__ __forceinline__ float warp_sum(float x) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+    return x;
+}
+
+// Forward: one launcher per kernel family; all return a dgrad_status.
+int forward_simt(const Args &a, const mha_packed_params *p, int dtype, cudaStream_t st);
+int forward_tc(const Args &a, const mha_packed_params *p, int dtype, cudaStream_t st);
+int backward_simt(const Args &a, const mha_packed_params *p, int dtype, cudaStream_t st);
+int backward_tc(const Args &a, const mha_packed_params *p, int dtype, cudaStream_t st);
+
+}  // namespace mhapk

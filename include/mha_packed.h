@@ -1,0 +1,117 @@
+/*
+ * mha_packed.h -- C ABI of causal attention over packed sequences, forward and
+ * backward (GB300, sm_103a).
+ *
+ * Several sequences lie one after another in tensors of `tokens` rows:
+ * Q, O, dO and dQ [tokens][num_heads][head_dim], K, V, dK and dV
+ * [tokens][num_kv_heads][head_dim], LSE [tokens][num_heads][2].  seq_offsets
+ * (num_seqs + 1 int32 values in device memory) holds the row at which each
+ * sequence begins and, last, the row after the last one; sequences may be empty.
+ * Within its sequence the query at row pos attends the keys t with t <= pos and,
+ * when window_size > 0, pos < t + window_size.  With KV head g = h / (num_heads /
+ * num_kv_heads) of query head h:
+ *
+ *   s(pos, t) = (Q[pos][h][:] . K[t][g][:]) / sqrt(head_dim)
+ *   LSE[pos][h] = (m, l):  m = max over t of s,  l = log(sum over t of exp(s - m))
+ *   P(pos, t) = exp(min(s - m, 0) - l)
+ *   O[pos][h][:] = sum over t of P V[t][g][:]
+ *   dP(pos, t) = dO[pos][h][:] . V[t][g][:],   delta(pos) = dO[pos][h][:] . O[pos][h][:]
+ *   dS = P (dP - delta)
+ *   dQ[pos][h][:] = sum over t of dS K[t][g][:] / sqrt(head_dim)
+ *   dK[t][g][:] = sum over pos and the heads of g of dS Q[pos][h][:] / sqrt(head_dim)
+ *   dV[t][g][:] = sum over pos and the heads of g of P dO[pos][h][:]
+ *
+ * LSE has the layout of mha_grad_v.h, so mha_grad_v takes it for a single
+ * sequence.  Rows that belong to no sequence (before seq_offsets[0] or from
+ * seq_offsets[num_seqs] on) get O = 0, LSE = (0, +inf) and zero gradients.  What
+ * a query does not attend never reaches its results, infinities and NaN included.
+ *
+ * Arguments: device pointers owned by the caller.  All tensors but LSE (float32)
+ * have the element type `dtype` (dgrad_dtype of conv2d_grad_input.h); outputs are
+ * overwritten.  Q, K and V may be strided by token (q_stride, k_stride, v_stride:
+ * elements between the starts of two tokens' rows, 0 for dense rows), as slices of
+ * a fused projection are; everything else is dense.  `stream` may be NULL; the
+ * calls only enqueue work.  The backward pass uses a caller's workspace of
+ * mha_packed_workspace_size bytes, which holds nothing between calls.
+ *
+ * Arithmetic: sums, maxima and statistics are float32.  The CUDA-core kernels
+ * (every type and shape) compute in float32 throughout.  The tensor-core kernels
+ * (see mha_packed_select_kernel) form scores and dP with tcgen05 (exact products,
+ * float32 sums) and round P and dS to the input type for the products that
+ * follow.  Every result is the same from run to run: nothing is added atomically.
+ *
+ * Errors (dgrad_status), checked on the host before any work, outputs untouched:
+ * DGRAD_ERR_INVALID_ARG for a NULL pointer or params, or an unknown dtype;
+ * DGRAD_ERR_SHAPE for tokens, num_heads, num_kv_heads or head_dim equal to 0,
+ * num_heads not a multiple of num_kv_heads, or a stride smaller than a dense row;
+ * DGRAD_ERR_ALIGNMENT for a pointer not aligned to its element size (the
+ * workspace: 16 bytes); DGRAD_ERR_UNSUPPORTED for head_dim above 256, more than
+ * 2^30 tokens or sequences, more than 2^31 - 1 thread blocks, or a forced kernel
+ * that does not apply; DGRAD_ERR_WORKSPACE for a workspace that is too small; DGRAD_ERR_CUDA
+ * when a launch fails.  seq_offsets lies on the device and is checked there:
+ * values that decrease or leave [0, tokens] are clamped (no access leaves the
+ * tensors; the results mean nothing) and raise the flag that
+ * mha_packed_check_errors reports as DGRAD_ERR_INVALID_ARG.
+ */
+#ifndef MHA_PACKED_H
+#define MHA_PACKED_H
+
+#include <stddef.h>
+#include <stdint.h>
+
+#include "conv2d_grad_input.h"
+
+#ifdef __cplusplus
+extern "C" {
+#endif
+
+typedef struct mha_packed_params {
+    uint32_t tokens;       /* rows of Q, K and V */
+    uint32_t num_seqs;     /* sequences; seq_offsets has one value more */
+    uint32_t num_heads;    /* query heads */
+    uint32_t num_kv_heads; /* key/value heads; num_heads is a multiple of it */
+    uint32_t head_dim;     /* elements per head */
+    uint32_t window_size;  /* > 0: query pos reaches key t only when pos < t + window_size */
+    uint32_t q_stride;     /* elements from one token's Q row to the next; 0: num_heads * head_dim */
+    uint32_t k_stride;     /* the same of K; 0: num_kv_heads * head_dim */
+    uint32_t v_stride;     /* the same of V; 0: num_kv_heads * head_dim */
+} mha_packed_params;
+
+/* O and LSE as defined above. */
+int mha_packed_forward(const void *q, const void *k, const void *v, const int32_t *seq_offsets, void *o, float *lse,
+                       const mha_packed_params *p, int dtype, struct CUstream_st *stream);
+
+/* Bytes of workspace mha_packed_backward needs (0 for params it refuses). */
+size_t mha_packed_workspace_size(const mha_packed_params *p, int dtype);
+
+/* dQ, dK and dV as defined above, from the forward's O and LSE. */
+int mha_packed_backward(const void *q, const void *k, const void *v, const void *o, const void *d_out,
+                        const float *lse, const int32_t *seq_offsets, void *dq, void *dk, void *dv, void *workspace,
+                        size_t workspace_bytes, const mha_packed_params *p, int dtype, struct CUstream_st *stream);
+
+/* Which kernels run for these arguments: DGRAD_KERNEL_TC or DGRAD_KERNEL_SIMT,
+ * or a negative dgrad_status.  The tensor-core kernels take DGRAD_BF16 /
+ * DGRAD_F16 with head_dim a multiple of 8 up to 128, strides that are multiples
+ * of 8 elements and 16-byte aligned pointers (their TMA tensor maps).  The forward
+ * looks at q, k, v and o, the backward at all seven tensors; host logic only. */
+int mha_packed_forward_select_kernel(const void *q, const void *k, const void *v, const void *o,
+                                     const mha_packed_params *p, int dtype);
+int mha_packed_backward_select_kernel(const void *q, const void *k, const void *v, const void *o, const void *d_out,
+                                      const void *dq, const void *dk, const void *dv, const mha_packed_params *p,
+                                      int dtype);
+
+/* Process-wide kernel choice for both directions: DGRAD_KERNEL_AUTO (default),
+ * DGRAD_KERNEL_TC or DGRAD_KERNEL_SIMT.  Returns the previous choice, or
+ * DGRAD_ERR_INVALID_ARG for another value. */
+int mha_packed_set_kernel(int kernel);
+
+/* Synchronises `stream`, then reports and clears a pending CUDA error
+ * (DGRAD_ERR_CUDA), the tensor-core kernels' timeout flag (DGRAD_ERR_TIMEOUT) or
+ * the flag of malformed seq_offsets (DGRAD_ERR_INVALID_ARG). */
+int mha_packed_check_errors(struct CUstream_st *stream);
+
+#ifdef __cplusplus
+}
+#endif
+
+#endif /* MHA_PACKED_H */

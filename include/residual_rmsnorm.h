@@ -1,0 +1,89 @@
+/*
+ * residual_rmsnorm.h -- C ABI of the residual step between two blocks: the norm
+ * after a block, its gate and scale, the residual add and the norm before the
+ * next block, in one pass, and its gradients (GB300, sm_103a).
+ *
+ * With F the block's output, X the residual stream (both [m][n]), weights W_post
+ * and W_pre [n], and a gate that is absent, one value per channel [n], or one per
+ * element [m][n]:
+ *
+ *   rp[i] = 1 / sqrt(mean over j of F[i, j]^2 + eps)
+ *   Z = F rp W_post
+ *   H = X + scale * gate * Z          (the new residual stream)
+ *   rq[i] = 1 / sqrt(mean over j of H[i, j]^2 + eps)
+ *   Y = H rq W_pre                    (the next block's input)
+ *   rstd[i] = (rp[i], rq[i])
+ *
+ * and, from dY, the gradient dH that reaches H by other ways, and rstd:
+ *
+ *   G   = dH + rq (W_pre dY - H rq^2 mean(W_pre dY H)),   dX = G
+ *   dW_pre = sum over i of dY H rq
+ *   dgate  = scale G Z   (summed over i for a gate per channel)
+ *   dZ  = scale G gate,   dW_post = sum over i of dZ F rp
+ *   dF  = rp (W_post dZ - F rp^2 mean(W_post dZ F))
+ *
+ * Arguments: device pointers owned by the caller, all dense row-major.  F, X, H, Y,
+ * the gate, the weights, dY, dH, dF, dX and a per-element dgate have the element
+ * type `dtype` (dgrad_dtype of conv2d_grad_input.h); rstd [m][2], dW_post, dW_pre
+ * and a per-channel dgate are float32.  Outputs are overwritten.  gate and dgate are
+ * NULL for RESIDUAL_GATE_NONE; rstd may be NULL in the forward (then it is not
+ * written); dh may be NULL (nothing else reaches H).  H may be X's buffer and dX may
+ * be dH's (a row is read before it is written); no other buffers may overlap.
+ * `stream` may be NULL; the calls only enqueue work.
+ *
+ * Arithmetic: float32 throughout, each output rounded once; Y is formed from H
+ * before H is rounded, while the backward reads the rounded H.  The sums over rows
+ * are made per thread block in a fixed order and then added up in a fixed order, so
+ * results are the same from run to run.
+ *
+ * Errors (dgrad_status), checked on the host before any work, outputs untouched:
+ * DGRAD_ERR_INVALID_ARG for a NULL pointer or params, an unknown dtype or gate kind,
+ * a non-finite or negative eps, a non-finite scale, or a gate given for
+ * RESIDUAL_GATE_NONE; DGRAD_ERR_SHAPE for m or n equal to 0; DGRAD_ERR_ALIGNMENT for a
+ * pointer not aligned to its element size (the workspace: 16 bytes);
+ * DGRAD_ERR_UNSUPPORTED for n above 2^20 or m above 2^31 - 1; DGRAD_ERR_WORKSPACE for a
+ * workspace that is too small; DGRAD_ERR_CUDA when a launch fails.
+ */
+#ifndef RESIDUAL_RMSNORM_H
+#define RESIDUAL_RMSNORM_H
+
+#include <stddef.h>
+#include <stdint.h>
+
+#include "conv2d_grad_input.h"
+
+#ifdef __cplusplus
+extern "C" {
+#endif
+
+enum residual_gate_kind {
+    RESIDUAL_GATE_NONE = 0,    /* H = X + scale * Z */
+    RESIDUAL_GATE_CHANNEL = 1, /* gate [n] */
+    RESIDUAL_GATE_ELEMENT = 2  /* gate [m][n] */
+};
+
+typedef struct residual_rmsnorm_params {
+    uint32_t m;         /* rows (tokens) */
+    uint32_t n;         /* columns (channels) */
+    uint32_t gate_kind; /* residual_gate_kind */
+    float eps;          /* added to both mean squares */
+    float scale;        /* of the gated branch */
+} residual_rmsnorm_params;
+
+int residual_rmsnorm_forward(const void *f, const void *x, const void *gate, const void *w_post, const void *w_pre,
+                             void *h, void *y, float *rstd, const residual_rmsnorm_params *p, int dtype,
+                             struct CUstream_st *stream);
+
+/* Bytes of workspace residual_rmsnorm_backward needs (0 for params it refuses). */
+size_t residual_rmsnorm_workspace_size(const residual_rmsnorm_params *p, int dtype);
+
+int residual_rmsnorm_backward(const void *f, const void *h, const void *gate, const void *w_post, const void *w_pre,
+                              const float *rstd, const void *dy, const void *dh, void *df, void *dx, void *dgate,
+                              float *dw_post, float *dw_pre, void *workspace, size_t workspace_bytes,
+                              const residual_rmsnorm_params *p, int dtype, struct CUstream_st *stream);
+
+#ifdef __cplusplus
+}
+#endif
+
+#endif /* RESIDUAL_RMSNORM_H */
