@@ -8,6 +8,7 @@
 namespace mhapk {
 
 unsigned take_simt_error(cudaError_t &e);
+unsigned take_fwd_error(cudaError_t &e);
 
 namespace {
 
@@ -99,7 +100,8 @@ int mha_packed_forward(const void *q, const void *k, const void *v, const int32_
     Args a = make_args(q, k, v, seq_offsets, p);
     a.out = o;
     a.lse = lse;
-    return forward_simt(a, p, dtype, static_cast<cudaStream_t>(stream));
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    return kern == DGRAD_KERNEL_TC ? forward_tc(a, p, dtype, st) : forward_simt(a, p, dtype, st);
 }
 
 size_t mha_packed_workspace_size(const mha_packed_params *p, int dtype) {
@@ -145,7 +147,7 @@ int mha_packed_set_kernel(int kernel) {
 int mha_packed_check_errors(struct CUstream_st *stream) {
     using namespace mhapk;
     cudaError_t e = cudaStreamSynchronize(static_cast<cudaStream_t>(stream));
-    const unsigned word = take_simt_error(e);
+    const unsigned word = take_simt_error(e) | take_fwd_error(e);
     if (e != cudaSuccess) {
         (void)cudaGetLastError();
         return DGRAD_ERR_CUDA;

@@ -1,0 +1,465 @@
+// mha_packed_fwd.cu -- tensor-core forward of causal attention over packed
+// sequences (include/mha_packed.h): bf16 / fp16, head_dim a multiple of 8 up to 128
+// (padded to D = 64 or 128 by the TMA copies' zero fill), sm_103a.
+//
+// One block per work unit: two tiles of 128 queries that read the same K and V
+// tiles -- two heads of one group at the same positions when the group is even, else
+// two runs of 128 positions of one head -- so that each byte of K and V that enters
+// shared memory serves 256 rows of scores.  For every block of 128 keys, from the
+// diagonal down to the first that the window reaches:
+//   S_i[pos][t] = Q_i . K^T                tcgen05 M128 N128 K16, D / 16 steps
+//   P_i = 2^(S_i c - m_i c), c = log2(e) / sqrt(head_dim), masked, rounded to 16 bits
+//   O_i[pos][:] += P_i V                   tcgen05 M128 N(D) K16, 8 steps, P from tensor memory
+// Tensor memory holds S_0, S_1 (128 columns each, P_i over the first 64 of S_i) and
+// O_0, O_1 (D each).
+//   * warps 0-3 and 4-7: the softmax of tile 0 and 1, one query per thread.  The
+//     maximum m_i that scales P and O may lag the true one: O and the sum are rescaled
+//     only when it grew by more than 2^8 (P stays below 2^8, far from fp16's limit), so
+//     most blocks skip the pass over O.  The true maximum is kept beside it for LSE.
+//   * warp 8 (converged, lane 0 issuing): per key block PV_0, S_0 of the next block,
+//     PV_1, S_1 of the next: while one tile's products run, the other's softmax does.
+//     The products of one thread run in order, so S_i may overwrite P_i behind PV_i.
+//   * warps 9 and 10 (one thread each): TMA copies of K (and Q tile 0) and V (and Q
+//     tile 1).
+// V rows past the sequence's end are zeroed in shared memory (other sequences' rows,
+// possibly with infinities); what is masked inside the sequence has P = 0, and if a
+// value there is not finite the product with 0 leaves a NaN in O: the tile is then
+// recomputed row by row over the attended keys alone.
+// Every wait is bounded; on timeout the kernel raises its error word, lets the copies
+// and products in flight finish, frees tensor memory and returns.
+#include "mha_packed_tc.cuh"
+
+namespace mhapk {
+
+__device__ unsigned int g_fwd_error_word = 0;
+
+unsigned take_fwd_error(cudaError_t &e) {
+    unsigned int word = 0;
+    const unsigned int zero = 0;
+    if (e == cudaSuccess) e = cudaMemcpyFromSymbol(&word, g_fwd_error_word, sizeof(word));
+    if (e == cudaSuccess && word) e = cudaMemcpyToSymbol(g_fwd_error_word, &zero, sizeof(zero));
+    return word;
+}
+
+namespace {
+
+constexpr int kRows = 128;                     // queries per tile, keys per step
+constexpr uint32_t kHalf = kRows * 128;        // bytes of a [128][64] 16-bit half tile
+constexpr int kSoftWarps = 8, kMmaWarp = 8, kLoadWarp = 9;  // K, then V
+constexpr uint32_t kColS = 0, kColO = 256;     // + 128 i, + 128 i
+constexpr int kThreads = 32 * (kLoadWarp + 2);
+constexpr float kLag = 8.0f;                   // log2 of how far the scaling maximum may lag
+
+template <int D>
+struct Cfg {
+    static constexpr int kHalves = D / 64;
+    static constexpr uint32_t kTile = kHalf * kHalves;
+    static constexpr int kStages = D == 64 ? 4 : 2;
+    static constexpr uint32_t kOffQ = 1024, kOffK = kOffQ + 2 * kTile, kOffV = kOffK + kStages * kTile;
+    static constexpr uint32_t kSmem = 1024 + kOffV + kStages * kTile;  // + 1 KB alignment slack
+    static_assert(kSmem + 1024 <= 232448, "shared memory over the per-block limit");
+};
+
+struct FwdArgs {
+    Args a;
+    CUtensorMap q_map, k_map, v_map;
+    uint32_t idesc1, idesc2;
+    int pair_heads;  // the two tiles are two heads of a group (else two runs of positions)
+};
+
+struct Ctl {
+    uint64_t q_full[2], k_full[4], k_empty[4], v_full[4], v_empty[4];
+    uint64_t s_full[2], p_ready[2], o_full[2], mma_done;
+    uint32_t tmem_base;
+    int abort_flag, bad[2];
+};
+static_assert(sizeof(Ctl) <= 1024, "control block too large");
+
+struct Tile {
+    int head, p0, live;  // query head, first position, rows of the sequence in it (0: no tile)
+    int lo, hi;          // key blocks [lo, hi)
+};
+
+__device__ __forceinline__ Tile tile_of(const FwdArgs &p, const Unit &u, int pair, int i) {
+    Tile t;
+    t.head = p.pair_heads ? 2 * pair + i : pair;
+    t.p0 = u.p0 + (p.pair_heads ? 0 : kRows * i);
+    t.live = u.len - t.p0 < kRows ? u.len - t.p0 : kRows;
+    if (t.live < 0) t.live = 0;
+    t.hi = t.live ? (t.p0 + t.live - 1) / kRows + 1 : 0;
+    t.lo = p.a.window > 0 && t.p0 - p.a.window + 1 > 0 ? (t.p0 - p.a.window + 1) / kRows : 0;
+    if (!t.live) t.lo = 0;
+    return t;
+}
+
+// One loading thread: K and Q tile 0 (tensor 0), or V and Q tile 1 (tensor 1).
+template <int D>
+__device__ void role_load(const FwdArgs &p, Ctl &c, uint32_t smem, const Unit &u, const Tile &own, int g, int lo,
+                          int hi, int tensor, const Waiter &w) {
+    using C = Cfg<D>;
+    const CUtensorMap *map = tensor ? &p.v_map : &p.k_map;
+    uint64_t *full = tensor ? c.v_full : c.k_full, *empty = tensor ? c.v_empty : c.k_empty;
+    const uint32_t ring = smem + (tensor ? C::kOffV : C::kOffK);
+    if (own.live)
+        load_rows<D>(smem + C::kOffQ + (uint32_t)tensor * C::kTile, &p.q_map, p.a.hd, own.head, u.begin + own.p0, kRows,
+                     su32(&c.q_full[tensor]));
+    int it = 0;
+    for (int b = hi - 1; b >= lo; --b, ++it) {
+        const int s = it % C::kStages;
+        if (!wait(su32(&empty[s]), (uint32_t)(((it / C::kStages) & 1) ^ 1), w)) break;
+        load_rows<D>(ring + (uint32_t)s * C::kTile, map, p.a.hd, g, u.begin + kRows * b, kRows, su32(&full[s]));
+    }
+    // Copies still landing must finish before the block exits.
+    if (own.live) drain(su32(&c.q_full[tensor]), 0, w);
+    for (int q = it > C::kStages ? it - C::kStages : 0; q < it; ++q)
+        drain(su32(&full[q % C::kStages]), (uint32_t)((q / C::kStages) & 1), w);
+}
+
+// All products of the unit; returns early when aborting.
+template <int D>
+__device__ __forceinline__ void issue_products(const FwdArgs &p, Ctl &c, uint32_t smem, uint32_t tmem, const Unit &u,
+                                               const Tile (&t)[2], int lo, int hi, int lane, const Waiter &w) {
+    using C = Cfg<D>;
+    const uint32_t leader = lane == 0;
+    int phase[2] = {0, 0};  // products PV issued of each tile
+    bool q_seen[2] = {false, false};
+    int it = 0;
+    // Iteration b: PV of block b + 1, then S of block b, tile by tile.
+    for (int b = hi - 1; b >= lo - 1; --b, ++it) {
+        const bool more = b >= lo, prev = b + 1 < hi;
+        const int ks = it % C::kStages, vs = (it - 1) % C::kStages;
+        if (more && !wait_warp(su32(&c.k_full[ks]), (uint32_t)((it / C::kStages) & 1), w)) return;
+        if (prev) {
+            if (!wait_warp(su32(&c.v_full[vs]), (uint32_t)(((it - 1) / C::kStages) & 1), w)) return;
+            const int keys = u.len - kRows * (b + 1);
+            if (keys < kRows) zero_rows(smem + C::kOffV + (uint32_t)vs * C::kTile, keys, kRows, C::kHalves, lane);
+        }
+        tc_after();
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            if (prev && b + 1 >= t[i].lo && b + 1 < t[i].hi) {
+                if (!wait_warp(su32(&c.p_ready[i]), (uint32_t)(phase[i] & 1), w)) return;
+                tc_after();
+                const uint64_t vd = desc_mn(smem + C::kOffV + (uint32_t)vs * C::kTile, kHalf, 1024u);
+#pragma unroll
+                for (int k = 0; k < 8; ++k)  // A: 8 columns (16 keys) per step; B: two groups of 8 keys (2 KB)
+                    tc_mma_f16_ts_if(tmem + kColO + 128u * i, tmem + kColS + 128u * i + 8u * k, vd + 128u * k, p.idesc2,
+                                     phase[i] > 0 || k > 0, leader);
+                ++phase[i];
+                if (b + 1 == t[i].lo) tc_commit_to_if(su32(&c.o_full[i]), leader);
+            }
+            if (more && b >= t[i].lo && b < t[i].hi) {
+                if (!q_seen[i] && !wait_warp(su32(&c.q_full[i]), 0, w)) return;
+                q_seen[i] = true;
+                const uint64_t qd = desc_k(smem + C::kOffQ + (uint32_t)i * C::kTile);
+                const uint64_t kd = desc_k(smem + C::kOffK + (uint32_t)ks * C::kTile);
+#pragma unroll
+                for (int k = 0; k < D / 16; ++k) {  // +32 bytes of each row, then the next half
+                    const uint64_t step = 2u * (k % 4) + (uint64_t)(k / 4) * (kHalf >> 4);
+                    tc_mma_f16_if(tmem + kColS + 128u * i, qd + step, kd + step, p.idesc1, k > 0, leader);
+                }
+                tc_commit_to_if(su32(&c.s_full[i]), leader);
+            }
+        }
+        if (prev) tc_commit_to_if(su32(&c.v_empty[vs]), leader);
+        if (more) tc_commit_to_if(su32(&c.k_empty[ks]), leader);
+    }
+}
+
+template <int D>
+__device__ void role_mma(const FwdArgs &p, Ctl &c, uint32_t smem, uint32_t tmem, const Unit &u, const Tile (&t)[2],
+                         int lo, int hi, int lane, const Waiter &w) {
+    issue_products<D>(p, c, smem, tmem, u, t, lo, hi, lane, w);
+    tc_commit_to_if(su32(&c.mma_done), lane == 0);  // nothing may still run when tensor memory is released
+    drain(su32(&c.mma_done), 0, w);
+    __syncwarp();
+}
+
+// 32 scores of one row, keys base .. base + 31: those outside [from, to] (relative to base) become -inf.
+__device__ __forceinline__ void mask32(uint32_t (&v)[32], int from, int to) {
+#pragma unroll
+    for (int e = 0; e < 32; ++e)
+        if (e < from || e > to) v[e] = 0xFF800000u;
+}
+__device__ __forceinline__ float max32(const uint32_t (&v)[32], float m) {
+#pragma unroll
+    for (int e = 0; e < 32; e += 2) m = fmaxf(m, fmaxf(__uint_as_float(v[e]), __uint_as_float(v[e + 1])));
+    return m;
+}
+// P of 32 scores: 2^(s c - mc), added to sum and packed two per word.
+template <bool F16>
+__device__ __forceinline__ void exp32(const uint32_t (&v)[32], float cs, float mc, float2 &sum, uint32_t (&pk)[16]) {
+    const float2 c2 = make_float2(cs, cs), m2 = make_float2(-mc, -mc);
+#pragma unroll
+    for (int e = 0; e < 32; e += 2) {
+        const float2 x = __ffma2_rn(make_float2(__uint_as_float(v[e]), __uint_as_float(v[e + 1])), c2, m2);
+        const float2 y = make_float2(fast_exp2(x.x), fast_exp2(x.y));
+        sum = __fadd2_rn(sum, y);
+        pk[e >> 1] = pack2<F16>(y.x, y.y);
+    }
+}
+
+template <int D, bool F16>
+__device__ void role_soft(const FwdArgs &p, Ctl &c, uint32_t smem, uint32_t tmem, const Unit &u, const Tile &t, int i,
+                          int warp, int lane, const Waiter &w) {
+    using C = Cfg<D>;
+    const int quad = warp & 3, pos = t.p0 + 32 * quad + lane;
+    const uint32_t lane_tm = (uint32_t)(32 * quad) << 16;
+    const uint32_t s_tm = tmem + lane_tm + kColS + 128u * i, o_tm = tmem + lane_tm + kColO + 128u * i;
+    const float cs = p.a.scale * 1.4426950408889634f;
+    float used = -INFINITY, top = -INFINITY;  // the maximum that scales, the true one
+    float2 sum = make_float2(0.f, 0.f);
+    int it = 0;
+    for (int b = t.hi - 1; b >= t.lo; --b, ++it) {
+        if (!wait_warp(su32(&c.s_full[i]), (uint32_t)(it & 1), w)) return;
+        tc_after();
+        const int base = kRows * b;
+        const bool whole = base + kRows - 1 <= t.p0 && (p.a.window == 0 || t.p0 + kRows - 1 < base + p.a.window);
+        const int to = pos - base, from = p.a.window > 0 ? pos - p.a.window + 1 - base : 0;
+        uint32_t v0[32], v1[32];
+        float m = top;
+        // Chunks 2 and 3 for their maximum, then 0 and 1, which stay in registers: their P overwrites columns that
+        // are read, and chunks 2 and 3 are read again afterwards (columns 64 .. 127, which P never covers).
+        tc_ld_32x32(s_tm + 64, v0);
+        tc_ld_32x32(s_tm + 96, v1);
+        tc_wait_ld(v0);
+        tc_wait_ld(v1);
+        if (!whole) mask32(v0, from - 64, to - 64), mask32(v1, from - 96, to - 96);
+        m = max32(v0, m);
+        m = max32(v1, m);
+        tc_ld_32x32(s_tm, v0);
+        tc_ld_32x32(s_tm + 32, v1);
+        tc_wait_ld(v0);
+        tc_wait_ld(v1);
+        if (!whole) mask32(v0, from, to), mask32(v1, from - 32, to - 32);
+        m = max32(v0, m);
+        m = max32(v1, m);
+        top = m;
+        if (__any_sync(0xffffffffu, (m - used) * cs > kLag)) {
+            if (it > 0) {  // before the first product O holds nothing
+                const float keep = m == -INFINITY ? 1.f : fast_exp2((used - m) * cs);
+                sum.x *= keep, sum.y *= keep;
+#pragma unroll
+                for (int k = 0; k < D / 32; ++k) {  // S of this block is behind PV of the last: O is complete
+                    uint32_t o[32];
+                    tc_ld_32x32(o_tm + 32 * k, o);
+                    tc_wait_ld(o);
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * keep);
+                    tc_st_32x32(o_tm + 32 * k, o);
+                }
+            }
+            used = m;
+        }
+        const float mc = used == -INFINITY ? 0.f : used * cs;
+        uint32_t pk[16];
+        exp32<F16>(v0, cs, mc, sum, pk);
+        tc_st_32x16(s_tm, pk);
+        exp32<F16>(v1, cs, mc, sum, pk);
+        tc_st_32x16(s_tm + 16, pk);
+        tc_ld_32x32(s_tm + 64, v0);
+        tc_ld_32x32(s_tm + 96, v1);
+        tc_wait_ld(v0);
+        tc_wait_ld(v1);
+        if (!whole) mask32(v0, from - 64, to - 64), mask32(v1, from - 96, to - 96);
+        exp32<F16>(v0, cs, mc, sum, pk);
+        tc_st_32x16(s_tm + 32, pk);
+        exp32<F16>(v1, cs, mc, sum, pk);
+        tc_st_32x16(s_tm + 48, pk);
+        tc_wait_st();
+        tc_before();
+        __syncwarp();
+        if (lane == 0) bar_arrive(su32(&c.p_ready[i]));
+    }
+    if (!wait_warp(su32(&c.o_full[i]), 0, w)) return;
+    tc_after();
+    // O rows through this warp's part of its Q tile (read by then), 16-byte chunk j of row r at j ^ (r & 7).
+    constexpr int kChunks = D / 8;
+    const float total = sum.x + sum.y, inv = 1.0f / total;
+    const uint32_t stage = smem + C::kOffQ + (uint32_t)i * C::kTile + (uint32_t)quad * (C::kTile / 4);
+    const bool row_live = 32 * quad + lane < t.live;
+    bool good = true;
+#pragma unroll
+    for (int k = 0; k < D / 32; ++k) {
+        uint32_t o[32];
+        tc_ld_32x32(o_tm + 32 * k, o);
+        tc_wait_ld(o);
+        float x[32];
+#pragma unroll
+        for (int e = 0; e < 32; ++e) {
+            x[e] = __uint_as_float(o[e]) * inv;
+            good = good && finite(x[e]);
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            sts128(stage + (uint32_t)lane * (2 * D) + (uint32_t)(((4 * k + j) ^ (lane & 7)) << 4),
+                   pack2<F16>(x[8 * j], x[8 * j + 1]), pack2<F16>(x[8 * j + 2], x[8 * j + 3]),
+                   pack2<F16>(x[8 * j + 4], x[8 * j + 5]), pack2<F16>(x[8 * j + 6], x[8 * j + 7]));
+    }
+    if (__any_sync(0xffffffffu, row_live && !good) && lane == 0) c.bad[i] = 1;
+    const int64_t row0 = (int64_t)u.begin + t.p0 + 32 * quad;
+    if (row_live) {
+        // The sum is relative to `used`; LSE wants it relative to the true maximum.
+        const float ln2 = 0.6931471805599453f;
+        const float l = logf(total) - (top - used) * cs * ln2;
+        float *st = p.a.lse + ((row0 + lane) * p.a.nh + t.head) * 2;
+        st[0] = top * p.a.scale, st[1] = l;
+    }
+    __syncwarp();
+    uint16_t *out = static_cast<uint16_t *>(p.a.out) + (row0 * p.a.nh + t.head) * p.a.hd;
+    const int j = lane % kChunks;
+    for (int r = lane / kChunks; r < 32; r += 32 / kChunks) {
+        if (32 * quad + r >= t.live || 8 * j >= p.a.hd) continue;
+        const uint4 x = lds128(stage + (uint32_t)r * (2 * D) + (uint32_t)((j ^ (r & 7)) << 4));
+        *reinterpret_cast<uint4 *>(out + (int64_t)r * p.a.nh * p.a.hd + 8 * j) = x;
+    }
+}
+
+// A tile row by row over the attended keys, one warp per row: for tiles where a masked value is not finite.
+template <int D, bool F16>
+__device__ void recompute(const FwdArgs &p, const Unit &u, const Tile &t, int g) {
+    using T = typename std::conditional<F16, __half, __nv_bfloat16>::type;
+    constexpr int N = D / 32;
+    const Args &a = p.a;
+    const int lane = threadIdx.x & 31, warps = blockDim.x >> 5;
+    for (int r = threadIdx.x >> 5; r < t.live; r += warps) {
+        const int pos = t.p0 + r;
+        const int64_t row = (int64_t)u.begin + pos;
+        const T *q = static_cast<const T *>(a.q) + row * a.qs + (int64_t)t.head * a.hd;
+        float qv[N], acc[N], m = -INFINITY, l = 0.f;
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const int d = lane + 32 * i;
+            qv[i] = d < a.hd ? to_f(q[d]) : 0.f;
+            acc[i] = 0.f;
+        }
+        for (int x = a.window > 0 && pos - a.window + 1 > 0 ? pos - a.window + 1 : 0; x <= pos; ++x) {
+            const int64_t key = (int64_t)u.begin + x;
+            const T *k = static_cast<const T *>(a.k) + key * a.ks + (int64_t)g * a.hd;
+            const T *v = static_cast<const T *>(a.v) + key * a.vs + (int64_t)g * a.hd;
+            float s = 0.f;
+#pragma unroll
+            for (int i = 0; i < N; ++i)
+                if (lane + 32 * i < a.hd) s = fmaf(qv[i], to_f(k[lane + 32 * i]), s);
+            s = warp_sum(s) * a.scale;
+            const float now = fmaxf(m, s), keep = now == -INFINITY ? 1.f : expf(m - now), e = expf(s - now);
+            l = l * keep + e;
+#pragma unroll
+            for (int i = 0; i < N; ++i)
+                if (lane + 32 * i < a.hd) acc[i] = acc[i] * keep + e * to_f(v[lane + 32 * i]);
+            m = now;
+        }
+        T *o = static_cast<T *>(a.out) + (row * a.nh + t.head) * a.hd;
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            if (lane + 32 * i < a.hd) o[lane + 32 * i] = from_f<T>(acc[i] / l);
+        if (lane == 0) {
+            float *st = a.lse + (row * a.nh + t.head) * 2;
+            st[0] = m, st[1] = logf(l);
+        }
+    }
+}
+
+template <int D, bool F16>
+__global__ void __launch_bounds__(kThreads, 1) forward_tc_kernel(const __grid_constant__ FwdArgs p) {
+    using C = Cfg<D>;
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    const uint32_t smem = (su32(smem_raw) + 1023u) & ~1023u;
+    Ctl &c = *reinterpret_cast<Ctl *>(smem_raw + (smem - su32(smem_raw)));
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < 4; ++s) {
+            bar_init(su32(&c.k_full[s]), 1);
+            bar_init(su32(&c.v_full[s]), 1);
+            bar_init(su32(&c.k_empty[s]), 1);
+            bar_init(su32(&c.v_empty[s]), 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            bar_init(su32(&c.q_full[i]), 1);
+            bar_init(su32(&c.s_full[i]), 1);
+            bar_init(su32(&c.p_ready[i]), 4);
+            bar_init(su32(&c.o_full[i]), 1);
+            c.bad[i] = 0;
+        }
+        bar_init(su32(&c.mma_done), 1);
+        c.abort_flag = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == kMmaWarp) tc_alloc(su32(&c.tmem_base), 512);
+    tc_before();
+    __syncthreads();
+    tc_after();
+    const uint32_t tmem = c.tmem_base;
+    if (threadIdx.x == 0) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+
+    const unsigned pairs = p.pair_heads ? p.a.nh / 2 : p.a.nh;
+    const int pair = (int)(blockIdx.x % pairs);
+    const Unit u = find_unit(p.a, blockIdx.x / pairs, p.pair_heads ? kRows : 2 * kRows, blockIdx.x == 0,
+                             &g_fwd_error_word);
+    const Waiter w{&c.abort_flag, &g_fwd_error_word};
+    if (u.live) {
+        const Tile t[2] = {tile_of(p, u, pair, 0), tile_of(p, u, pair, 1)};
+        const int g = t[0].head / p.a.hpk;
+        if (u.pad) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+                for (int r = warp; r < t[i].live; r += kThreads / 32) {
+                    const int64_t at = ((int64_t)u.begin + t[i].p0 + r) * p.a.nh + t[i].head;
+                    for (int d = lane; d < p.a.hd; d += 32) static_cast<uint16_t *>(p.a.out)[at * p.a.hd + d] = 0;
+                    if (lane == 0) p.a.lse[2 * at] = 0.f, p.a.lse[2 * at + 1] = INFINITY;
+                }
+        } else {
+            // Tile 0 is never empty; with an empty tile 1 its range is empty too.
+            const int lo = t[1].live && t[1].lo < t[0].lo ? t[1].lo : t[0].lo;
+            const int hi = t[1].hi > t[0].hi ? t[1].hi : t[0].hi;
+            if (warp < kSoftWarps) {
+                const int i = warp >> 2;
+                const Tile own = i ? t[1] : t[0];
+                if (own.live) role_soft<D, F16>(p, c, smem, tmem, u, own, i, warp, lane, w);
+            } else if (warp == kMmaWarp) {
+                role_mma<D>(p, c, smem, tmem, u, t, lo, hi, lane, w);
+            } else {
+                const int tensor = warp - kLoadWarp;
+                if (lane == 0) role_load<D>(p, c, smem, u, tensor ? t[1] : t[0], g, lo, hi, tensor, w);
+                __syncwarp();
+            }
+            tc_before();
+            __syncthreads();
+            tc_after();
+            if (!c.abort_flag) {
+                if (c.bad[0]) recompute<D, F16>(p, u, t[0], g);
+                if (c.bad[1]) recompute<D, F16>(p, u, t[1], g);
+            }
+        }
+    }
+    __syncthreads();
+    if (warp == kMmaWarp) tc_dealloc(tmem, 512);
+}
+
+template <int D, bool F16>
+int launch(const FwdArgs &q, int64_t blocks, cudaStream_t st) {
+    static std::atomic<uint64_t> configured{0};
+    return launch_tc(forward_tc_kernel<D, F16>, blocks, kThreads, Cfg<D>::kSmem, configured, q, st);
+}
+
+}  // namespace
+
+int forward_tc(const Args &a, const mha_packed_params *p, int dtype, cudaStream_t st) {
+    FwdArgs q{};
+    q.a = a;
+    q.pair_heads = a.hpk % 2 == 0;
+    const int D = a.hd <= 64 ? 64 : 128;
+    q.idesc1 = instr_desc(dtype, kRows, kRows, false);
+    q.idesc2 = instr_desc(dtype, kRows, D, true);
+    if (!encode_rows(&q.q_map, a.q, a.tokens, a.nh, a.hd, a.qs, kRows) ||
+        !encode_rows(&q.k_map, a.k, a.tokens, a.nkv, a.hd, a.ks, kRows) ||
+        !encode_rows(&q.v_map, a.v, a.tokens, a.nkv, a.hd, a.vs, kRows))
+        return DGRAD_ERR_UNSUPPORTED;
+    const int64_t blocks = q.pair_heads ? unit_bound(p, kRows) * (a.nh / 2) : unit_bound(p, 2 * kRows) * a.nh;
+    const bool f16 = dtype == DGRAD_F16;
+    if (D == 64) return f16 ? launch<64, true>(q, blocks, st) : launch<64, false>(q, blocks, st);
+    return f16 ? launch<128, true>(q, blocks, st) : launch<128, false>(q, blocks, st);
+}
+
+}  // namespace mhapk

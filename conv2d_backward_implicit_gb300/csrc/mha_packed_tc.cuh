@@ -1,0 +1,178 @@
+// mha_packed_tc.cuh -- what the tensor-core kernels of packed attention share:
+// bounded waits, tensor maps, launch set-up.
+#pragma once
+
+#include <cuda.h>
+#include <cudaTypedefs.h>
+
+#include <atomic>
+
+#include "mha_packed_internal.cuh"
+#include "tc_helpers.cuh"
+
+namespace mhapk {
+namespace {
+
+using namespace tch;
+
+constexpr uint64_t kWaitLimitNs = 2000000000ull;  // 2 s: far beyond any step of any valid problem
+
+// Waits are bounded: on timeout the kernel's error word and its block's abort flag are raised, and the roles leave.
+struct Waiter {
+    volatile int *abort_flag;
+    unsigned *error;
+};
+__device__ __noinline__ bool wait_long(uint32_t bar, uint32_t parity, Waiter w, bool honour_abort) {
+    const uint64_t t0 = now_ns();
+    const uint64_t max_spins = kWaitLimitNs / 16 + (1u << 20);
+    for (uint64_t spin = 1;; ++spin) {
+        if (bar_try(bar, parity)) return true;
+        if (honour_abort && *w.abort_flag) return false;
+        if (((spin & 31u) == 0 && now_ns() - t0 > kWaitLimitNs) || spin > max_spins) {
+            *w.abort_flag = 1;
+            atomicOr(w.error, kErrTimeout);
+            return false;
+        }
+    }
+}
+// false: the block is aborting.
+__device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity, const Waiter &w) {
+    return bar_try(bar, parity) || wait_long(bar, parity, w, true);
+}
+// For work already in flight (copies, MMAs): goes on while aborting.
+__device__ __forceinline__ void drain(uint32_t bar, uint32_t parity, const Waiter &w) {
+    if (!bar_try(bar, parity)) wait_long(bar, parity, w, false);
+}
+// Whole warp, one verdict for all lanes.
+__device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity, const Waiter &w) {
+    return __all_sync(0xffffffffu, wait(bar, parity, w)) != 0;
+}
+
+__device__ __forceinline__ void tc_st_32x32(uint32_t taddr, const uint32_t (&r)[32]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, "
+        "%14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(taddr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
+        "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
+        "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+        : "memory");
+}
+
+__device__ __forceinline__ float fast_exp2(float x) {  // the SFU's 2^x
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// Two floats rounded to a pair of the input type (low half first).
+template <bool F16>
+__device__ __forceinline__ uint32_t pack2(float a, float b) {
+    if constexpr (F16) {
+        const __half2 h = __floats2half2_rn(a, b);
+        return *reinterpret_cast<const uint32_t *>(&h);
+    } else {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+        return *reinterpret_cast<const uint32_t *>(&h);
+    }
+}
+
+__device__ __forceinline__ bool finite(float x) { return fabsf(x) <= 3.402823466e38f; }
+
+// Zero rows [from, rows) of a [rows][D] tile held as D / 64 halves of 128-byte rows: one warp, before the tensor core
+// reads it.
+__device__ __forceinline__ void zero_rows(uint32_t tile, int from, int rows, int halves, int lane) {
+    for (int h = 0; h < halves; ++h)
+        for (int r = from + (lane >> 3); r < rows; r += 4)
+            sts128(tile + (uint32_t)(h * rows + r) * 128u + (uint32_t)(lane & 7) * 16u, 0, 0, 0, 0);
+    fence_async_proxy();
+    __syncwarp();
+}
+
+inline PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
+    static PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
+        void *ptr = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000, cudaEnableDefault, &q) !=
+                cudaSuccess ||
+            q != cudaDriverEntryPointSuccess)
+            ptr = nullptr;
+        return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(ptr);
+    }();
+    return fn;
+}
+
+// [tokens][heads][hd] 16-bit elements, `row` elements from token to token, in boxes of `rows` tokens of one head that
+// land as halves [rows][64] (128-byte swizzle): with hd a multiple of 64 all halves in one copy, through a view
+// [hd / 64][tokens][heads][64]; else one half per copy, elements past hd reading as zero.  Tokens past the last read as
+// zero too.
+inline bool encode_rows(CUtensorMap *m, const void *ptr, int tokens, int heads, int hd, int64_t row, int rows) {
+    PFN_cuTensorMapEncodeTiled_v12000 fn = encode_fn();
+    if (!fn) return false;
+    const bool whole = hd % 64 == 0;
+    const cuuint64_t dims[4] = {(cuuint64_t)(whole ? 64 : hd), (cuuint64_t)heads, (cuuint64_t)tokens,
+                                (cuuint64_t)(whole ? hd / 64 : 1)};
+    const cuuint64_t strides[3] = {(cuuint64_t)hd * 2, (cuuint64_t)row * 2, 128};
+    const cuuint32_t box[4] = {64, 1, (cuuint32_t)rows, (cuuint32_t)(whole ? hd / 64 : 1)};
+    const cuuint32_t es[4] = {1, 1, 1, 1};
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT16, 4, const_cast<void *>(ptr), dims, strides, box, es,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap *map, int x, int y, int z, int w,
+                                            uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], "
+        "[%6];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(bar)
+        : "memory");
+}
+
+// One tile of D / 64 halves of `rows` rows through a map of encode_rows: one thread; `bar` counts its arrival and bytes.
+template <int D>
+__device__ __forceinline__ void load_rows(uint32_t dst, const CUtensorMap *map, int hd, int head, int token, int rows,
+                                          uint32_t bar) {
+    bar_expect_tx(bar, (uint32_t)rows * 128u * (D / 64));
+    if (D == 64 || hd == D) {
+        tma_load_4d(dst, map, 0, head, token, 0, bar);
+    } else {
+#pragma unroll
+        for (int h = 0; h < D / 64; ++h) tma_load_4d(dst + (uint32_t)(h * rows) * 128u, map, 64 * h, head, token, 0, bar);
+    }
+}
+
+inline uint32_t instr_desc(int dtype, int m, int n, bool b_mn_major) {  // D float32, A and B of the input type
+    const uint32_t fmt = dtype == DGRAD_BF16 ? 1u : 0u;
+    return (1u << 4) | (fmt << 7) | (fmt << 10) | (b_mn_major ? 1u << 16 : 0u) | ((uint32_t)(n >> 3) << 17) |
+           ((uint32_t)(m >> 4) << 24);
+}
+
+// One launch with programmatic serialisation; `configured` remembers per device that the shared-memory limit is raised.
+template <typename K, typename A>
+int launch_tc(K kern, int64_t blocks, int threads, uint32_t smem, std::atomic<uint64_t> &configured, const A &args,
+              cudaStream_t st) {
+    if (blocks > INT32_MAX) return DGRAD_ERR_UNSUPPORTED;
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return DGRAD_ERR_CUDA;
+    const uint64_t bit = dev < 64 ? (uint64_t)1 << dev : 0;
+    if (!bit || !(configured.load() & bit)) {
+        if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
+            return DGRAD_ERR_CUDA;
+        configured.fetch_or(bit);
+    }
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)blocks);
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kern, args) == cudaSuccess ? DGRAD_OK : DGRAD_ERR_CUDA;
+}
+
+}  // namespace
+}  // namespace mhapk

@@ -156,7 +156,7 @@ CASES = {
 
 
 def problem(case, dtype, seed=1):
-    lens, H, G, d, *rest = CASES[case]
+    lens, H, G, d, *rest = (CASES | LONG)[case]
     names = ("window", "head", "tail", "fused")
     return Problem(lens, H, G, d, dtype=dtype, seed=seed + sum(lens) + d, **dict(zip(names, rest)))
 
@@ -169,6 +169,29 @@ def test_cuda_core_kernels(dg, case, dtype, parity_log):
     try:
         check_forward(dg, p, dg.DGRAD_KERNEL_SIMT, parity_log, f"simt {dtype} {case}")
         check_backward(dg, p, dg.DGRAD_KERNEL_SIMT, parity_log, f"simt {dtype} {case}")
+    finally:
+        dg.mha_packed_set_kernel(dg.DGRAD_KERNEL_AUTO)
+
+
+# More key blocks than ring stages, tiles and blocks that end inside a sequence, windows that skip blocks.
+LONG = {
+    "long": ([1000], 4, 2, 128),
+    "long 64": ([1111, 640], 4, 1, 64),
+    "long odd group": ([900, 259], 3, 1, 128),
+    "long window": ([1300], 4, 2, 64, 300),
+    "long window odd": ([1200], 1, 1, 128, 129, 0, 0, True),
+    "long head 96": ([700], 2, 1, 96),
+}
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("case", list(CASES) + list(LONG))
+def test_tensor_core_kernels(dg, case, dtype, parity_log):
+    p = problem(case, dtype)
+    dg.mha_packed_set_kernel(dg.DGRAD_KERNEL_TC)
+    try:
+        check_forward(dg, p, dg.DGRAD_KERNEL_TC, parity_log, f"tc {dtype} {case}")
+        check_backward(dg, p, dg.DGRAD_KERNEL_TC, parity_log, f"tc {dtype} {case}")
     finally:
         dg.mha_packed_set_kernel(dg.DGRAD_KERNEL_AUTO)
 
