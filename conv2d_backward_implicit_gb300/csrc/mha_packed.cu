@@ -9,6 +9,7 @@ namespace mhapk {
 
 unsigned take_simt_error(cudaError_t &e);
 unsigned take_fwd_error(cudaError_t &e);
+unsigned take_bwd_error(cudaError_t &e);
 
 namespace {
 
@@ -80,8 +81,11 @@ Args make_args(const void *q, const void *k, const void *v, const int32_t *off, 
     return a;
 }
 
+// The statistics of every head and row, behind a header of two maxima.
+constexpr size_t kHeader = 256;
+
 size_t workspace_bytes_of(const mha_packed_params *p) {
-    return (size_t)p->tokens * p->num_heads * sizeof(float2);
+    return kHeader + (size_t)p->tokens * p->num_heads * sizeof(float2);
 }
 
 }  // namespace
@@ -123,8 +127,10 @@ int mha_packed_backward(const void *q, const void *k, const void *v, const void 
     a.o = o, a.go = d_out;
     a.lse_in = lse;
     a.dq = dq, a.dk = dk, a.dv = dv;
-    a.stats = static_cast<float2 *>(workspace);
-    return backward_simt(a, p, dtype, static_cast<cudaStream_t>(stream));
+    a.stats = reinterpret_cast<float2 *>(static_cast<char *>(workspace) + kHeader);
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (kern == DGRAD_KERNEL_TC) return backward_tc(a, static_cast<unsigned *>(workspace), p, dtype, st);
+    return backward_simt(a, p, dtype, st);
 }
 
 int mha_packed_forward_select_kernel(const void *q, const void *k, const void *v, const void *o,
@@ -147,7 +153,7 @@ int mha_packed_set_kernel(int kernel) {
 int mha_packed_check_errors(struct CUstream_st *stream) {
     using namespace mhapk;
     cudaError_t e = cudaStreamSynchronize(static_cast<cudaStream_t>(stream));
-    const unsigned word = take_simt_error(e) | take_fwd_error(e);
+    const unsigned word = take_simt_error(e) | take_fwd_error(e) | take_bwd_error(e);
     if (e != cudaSuccess) {
         (void)cudaGetLastError();
         return DGRAD_ERR_CUDA;

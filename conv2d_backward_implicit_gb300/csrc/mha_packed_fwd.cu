@@ -12,7 +12,8 @@
 //   O_i[pos][:] += P_i V                   tcgen05 M128 N(D) K16, 8 steps, P from tensor memory
 // Tensor memory holds S_0, S_1 (128 columns each, P_i over the first 64 of S_i) and
 // O_0, O_1 (D each).
-//   * warps 0-3 and 4-7: the softmax of tile 0 and 1, one query per thread.  The
+//   * warps 0-3 and 4-7: the softmax of tile 0 and 1, one query per thread.  fp16's P
+//     carries a factor 2^7, which cancels in O / sum.  The
 //     maximum m_i that scales P and O may lag the true one: O and the sum are rescaled
 //     only when it grew by more than 2^8 (P stays below 2^8, far from fp16's limit), so
 //     most blocks skip the pass over O.  The true maximum is kept beside it for LSE.
@@ -49,6 +50,7 @@ constexpr int kSoftWarps = 8, kMmaWarp = 8, kLoadWarp = 9;  // K, then V
 constexpr uint32_t kColS = 0, kColO = 256;     // + 128 i, + 128 i
 constexpr int kThreads = 32 * (kLoadWarp + 2);
 constexpr float kLag = 8.0f;                   // log2 of how far the scaling maximum may lag
+constexpr float kShift16 = 7.0f;               // log2 of fp16's scale of P: P <= 2^15, and 7 more bits below
 
 template <int D>
 struct Cfg {
@@ -251,7 +253,7 @@ __device__ void role_soft(const FwdArgs &p, Ctl &c, uint32_t smem, uint32_t tmem
             }
             used = m;
         }
-        const float mc = used == -INFINITY ? 0.f : used * cs;
+        const float mc = (used == -INFINITY ? 0.f : used * cs) - (F16 ? kShift16 : 0.f);
         uint32_t pk[16];
         exp32<F16>(v0, cs, mc, sum, pk);
         tc_st_32x16(s_tm, pk);
@@ -301,7 +303,7 @@ __device__ void role_soft(const FwdArgs &p, Ctl &c, uint32_t smem, uint32_t tmem
     if (row_live) {
         // The sum is relative to `used`; LSE wants it relative to the true maximum.
         const float ln2 = 0.6931471805599453f;
-        const float l = logf(total) - (top - used) * cs * ln2;
+        const float l = logf(total) - ((top - used) * cs + (F16 ? kShift16 : 0.f)) * ln2;
         float *st = p.a.lse + ((row0 + lane) * p.a.nh + t.head) * 2;
         st[0] = top * p.a.scale, st[1] = l;
     }

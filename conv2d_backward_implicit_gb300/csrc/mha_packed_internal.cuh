@@ -142,6 +142,6 @@ __device__ __forceinline__ float warp_sum(float x) {
 int forward_simt(const Args &a, const mha_packed_params *p, int dtype, cudaStream_t st);
 int forward_tc(const Args &a, const mha_packed_params *p, int dtype, cudaStream_t st);
 int backward_simt(const Args &a, const mha_packed_params *p, int dtype, cudaStream_t st);
-int backward_tc(const Args &a, const mha_packed_params *p, int dtype, cudaStream_t st);
+int backward_tc(const Args &a, unsigned *norms, const mha_packed_params *p, int dtype, cudaStream_t st);
 
 }  // namespace mhapk

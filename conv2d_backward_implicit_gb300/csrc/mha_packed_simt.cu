@@ -330,7 +330,7 @@ __global__ void __launch_bounds__(kThreads) backward_simt_kernel(const Args a) {
                         if (pos < u.len && t <= pos && (a.window == 0 || pos - t < a.window)) {
                             const int64_t at = (int64_t)u.begin + pos;
                             const float *l = a.lse_in + (at * a.nh + h) * 2;
-                            p = expf(fminf(s[i][j] * a.scale - __ldg(l), 0.f) - __ldg(l + 1));
+                            p = expf(s[i][j] * a.scale - __ldg(l) - __ldg(l + 1));
                             d = p * (dp[i][j] - a.stats[(int64_t)h * a.tokens + at].y);
                         }
                         ds_s[(RT * ty + i) * PP + tx + 16 * j] = d;

@@ -13,7 +13,7 @@
  *
  *   s(pos, t) = (Q[pos][h][:] . K[t][g][:]) / sqrt(head_dim)
  *   LSE[pos][h] = (m, l):  m = max over t of s,  l = log(sum over t of exp(s - m))
- *   P(pos, t) = exp(min(s - m, 0) - l)
+ *   P(pos, t) = exp(s - m - l)
  *   O[pos][h][:] = sum over t of P V[t][g][:]
  *   dP(pos, t) = dO[pos][h][:] . V[t][g][:],   delta(pos) = dO[pos][h][:] . O[pos][h][:]
  *   dS = P (dP - delta)

@@ -82,7 +82,7 @@ def forward_bounds(q, k, v, offsets, window: int, u: float, out: float, tiny: fl
             g = h // per
             err = np.where(keep, _score_error(q[a:b, h], k[a:b, g], d, 1 / np.sqrt(d)), 0.0).max(1)
             s = (q[a:b, h] @ k[a:b, g].T) / np.sqrt(d)
-            p = np.where(keep, np.exp(np.minimum(s - lse[a:b, h, :1], 0) - lse[a:b, h, 1:]), 0.0)
+            p = np.where(keep, np.exp(s - lse[a:b, h, :1] - lse[a:b, h, 1:]), 0.0)
             rel = 2 * err + (n + 8) * 2 * E32
             bo[a:b, h] = (rel + u)[:, None] * (p @ np.abs(v[a:b, g])) + out * np.abs(o[a:b, h]) + tiny
             bl[a:b, h, 0] = err + 4 * E32 * np.abs(lse[a:b, h, 0])
@@ -101,7 +101,7 @@ def backward(q, k, v, o, d_out, lse, offsets, window: int):
             for h in range(H):
                 g = h // per
                 s = (q[a:b, h] @ k[a:b, g].T) / np.sqrt(d)
-                p = np.where(keep, np.exp(np.minimum(s - lse[a:b, h, :1], 0) - lse[a:b, h, 1:]), 0.0)
+                p = np.where(keep, np.exp(s - lse[a:b, h, :1] - lse[a:b, h, 1:]), 0.0)
                 delta = (d_out[a:b, h] * o[a:b, h]).sum(1, keepdims=True)
                 ds = np.where(keep, p * (d_out[a:b, h] @ v[a:b, g].T - delta), 0.0)
                 dq[a:b, h] = _masked_dot(ds, k[a:b, g], keep) / np.sqrt(d)
@@ -121,7 +121,7 @@ def backward_bounds(q, k, v, o, d_out, lse, offsets, window: int, u: float, out:
         for h in range(H):
             g = h // per
             s = (q[a:b, h] @ k[a:b, g].T) / np.sqrt(d)
-            p = np.where(keep, np.exp(np.minimum(s - lse[a:b, h, :1], 0) - lse[a:b, h, 1:]), 0.0)
+            p = np.where(keep, np.exp(s - lse[a:b, h, :1] - lse[a:b, h, 1:]), 0.0)
             delta = (d_out[a:b, h] * o[a:b, h]).sum(1, keepdims=True)
             ds = np.abs(p * (d_out[a:b, h] @ v[a:b, g].T - delta))
             rel = _score_error(q[a:b, h], k[a:b, g], d, 1 / np.sqrt(d)) + 8 * E32 \
