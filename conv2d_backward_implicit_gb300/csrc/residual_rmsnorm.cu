@@ -9,15 +9,13 @@
 // another, each a shuffle reduction plus, for teams of several warps, one barrier of
 // that team alone.
 //
-// Forward: a block of up to 512 threads takes one row per team and ends, so that several
-// blocks per SM keep loads in flight while others reduce.
-//
-// Backward: one persistent block of 16 warps per SM, because the sums over rows (the
-// weights' and the channel gate's gradients) stay in registers from row to row.  What
-// covers the loads' latency is a ring of kRing / ITER rows per thread in shared memory, filled
-// with cp.async: a thread copies and reads its own pieces only, so the ring needs no
-// barrier.  At the end teams add up in a fixed order, each block writes one partial row,
-// and a second kernel adds those in a fixed order.
+// With many rows, one persistent block of 16 warps per SM: what is the same for every
+// row (weights, gate) and the backward's sums over rows stay in registers, and what
+// covers the loads' latency is a ring of rows per thread in shared memory, filled with
+// cp.async -- a thread copies and reads its own pieces only, so the ring needs no
+// barrier.  After the backward, teams add up their sums in a fixed order, each block
+// writes one partial row, and a second kernel adds those in a fixed order.
+// With few rows the forward takes one row per team and ends.
 //
 // Rows too long for that (more than 512 threads x 4 pieces, x 2 in the 16-bit backward,
 // x 8 single elements) take kernels that read the row again for each statistic.
@@ -26,6 +24,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <atomic>
 #include <cmath>
 #include <cstdint>
 #include <type_traits>
@@ -38,6 +37,7 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kMaxBlocks = 152;  // of the backward: one for each SM
+constexpr int kRingRows = 2;     // rows per team from which the forward's ring pays
 constexpr uint32_t kMaxN = 1u << 20;
 
 struct Args {
@@ -93,48 +93,126 @@ __device__ __forceinline__ void team_barrier(int team, int warps) {
     asm volatile("bar.sync %0, %1;" ::"r"(1 + team), "r"(32 * warps) : "memory");
 }
 
-// Sum over a team of `tw` warps; `red` [2][16] floats, `turn` alternates between its halves: when a half is written
-// again, every thread of the team has passed the barrier after which nobody reads it.
+// Sum over a team of `tw` warps (a power of two); `red` [2][16] floats, `turn` alternates between its halves: when a
+// half is written again, every thread of the team has passed the barrier after which nobody reads it.
 __device__ __forceinline__ float team_sum(float x, float *red, int &turn, int tw, int warp) {
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
     if (tw == 1) return x;
     float *r = red + 16 * turn;
     turn ^= 1;
-    const int team = warp / tw, first = team * tw;
-    if ((threadIdx.x & 31) == 0) r[warp] = x;
+    const int team = warp / tw, lane = threadIdx.x & 31;
+    if (lane == 0) r[warp] = x;
     team_barrier(team, tw);
-    float t = 0.f;
-    for (int w = 0; w < tw; ++w) t += r[first + w];
-    return t;
+    x = r[team * tw + (lane & (tw - 1))];
+    for (int o = tw >> 1; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+    return x;
 }
 
-// A piece of a row: V elements, 16 bytes or one element.
+// A piece of a row: V elements, 16 bytes or one element, seen as V2 pairs of floats (a single element's partner is 0).
 template <typename T, bool VEC>
 struct Piece {
-    static constexpr int V = VEC ? 16 / (int)sizeof(T) : 1;
+    static constexpr int V = VEC ? 16 / (int)sizeof(T) : 1, V2 = VEC ? V / 2 : 1;
     using Raw = typename std::conditional<VEC, uint4, T>::type;
     Raw raw;
     __device__ __forceinline__ void load(const void *base, int64_t piece) {
         raw = __ldg(static_cast<const Raw *>(base) + piece);
     }
     __device__ __forceinline__ void zero() { raw = Raw{}; }
-    __device__ __forceinline__ float get(int e) const { return to_f(reinterpret_cast<const T *>(&raw)[e]); }
-};
-template <typename T, bool VEC>
-__device__ __forceinline__ void store_piece(void *base, int64_t piece, const float *x) {
-    if constexpr (VEC) {
-        uint4 w;
-        T *t = reinterpret_cast<T *>(&w);
-#pragma unroll
-        for (int e = 0; e < 16 / (int)sizeof(T); ++e) t[e] = from_f<T>(x[e]);
-        static_cast<uint4 *>(base)[piece] = w;
-    } else {
-        static_cast<T *>(base)[piece] = from_f<T>(x[0]);
+    __device__ __forceinline__ float2 get(int p) const {
+        if constexpr (!VEC) {
+            return make_float2(to_f(raw), 0.f);
+        } else if constexpr (sizeof(T) == 4) {
+            return reinterpret_cast<const float2 *>(&raw)[p];
+        } else {
+            const uint32_t w = reinterpret_cast<const uint32_t *>(&raw)[p];
+            if constexpr (std::is_same<T, __half>::value)
+                return __half22float2(*reinterpret_cast<const __half2 *>(&w));
+            else
+                return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+        }
     }
+    __device__ __forceinline__ void set(const float2 (&x)[V2]) {
+        if constexpr (!VEC) {
+            raw = from_f<T>(x[0].x);
+        } else {
+            T *t = reinterpret_cast<T *>(&raw);
+#pragma unroll
+            for (int p = 0; p < V2; ++p) {
+                if constexpr (std::is_same<T, __nv_bfloat16>::value)
+                    *reinterpret_cast<__nv_bfloat162 *>(t + 2 * p) = __floats2bfloat162_rn(x[p].x, x[p].y);
+                else if constexpr (std::is_same<T, __half>::value)
+                    *reinterpret_cast<__half2 *>(t + 2 * p) = __floats2half2_rn(x[p].x, x[p].y);
+                else
+                    *reinterpret_cast<float2 *>(t + 2 * p) = x[p];
+            }
+        }
+    }
+    __device__ __forceinline__ void store(void *base, int64_t piece) const { static_cast<Raw *>(base)[piece] = raw; }
+};
+__device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
+__device__ __forceinline__ float sum2(float2 x) { return x.x + x.y; }
+__device__ __forceinline__ float2 add2(float2 x, float2 y) { return __fadd2_rn(x, y); }
+__device__ __forceinline__ float2 mul2(float2 x, float2 y) { return __fmul2_rn(x, y); }
+__device__ __forceinline__ float2 fma2(float2 x, float2 y, float2 z) { return __ffma2_rn(x, y, z); }
+
+__device__ __forceinline__ float rstd_of(float sum, const Args &a) { return 1.0f / sqrtf(sum / (float)a.n + a.eps); }
+
+__device__ __forceinline__ void copy16(void *dst, const void *src) {  // asynchronous, shared <- global
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((uint32_t)__cvta_generic_to_shared(dst)), "l"(src)
+                 : "memory");
+}
+__device__ __forceinline__ void copies_end() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int PENDING>
+__device__ __forceinline__ void copies_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(PENDING) : "memory");
 }
 
-// pieces: of a row.  Thread `t` of a team holds pieces t, t + 32 tw, ...
+// The forward's arithmetic on one row, whose pieces this thread holds: `coef` = scale gate W_post.
+template <typename T, int ITER, bool VEC>
+struct ForwardRow {
+    using P = Piece<T, VEC>;
+    float2 h[ITER][P::V2];
+    float rp, rq;
+    template <typename Coef>
+    __device__ __forceinline__ void run(const P (&f)[ITER], const P (&x)[ITER], Coef coef, const Args &a, float *red,
+                                        int &turn, int tw, int warp) {
+        float2 s = both(0.f);
+#pragma unroll
+        for (int i = 0; i < ITER; ++i)
+#pragma unroll
+            for (int p = 0; p < P::V2; ++p) s = fma2(f[i].get(p), f[i].get(p), s);
+        rp = rstd_of(team_sum(sum2(s), red, turn, tw, warp), a);
+        s = both(0.f);
+#pragma unroll
+        for (int i = 0; i < ITER; ++i)
+#pragma unroll
+            for (int p = 0; p < P::V2; ++p) {
+                h[i][p] = fma2(coef(i, p), mul2(f[i].get(p), both(rp)), x[i].get(p));
+                s = fma2(h[i][p], h[i][p], s);
+            }
+        rq = rstd_of(team_sum(sum2(s), red, turn, tw, warp), a);
+    }
+    __device__ __forceinline__ void store(const P (&wq)[ITER], const Args &a, int64_t row, int pieces, int t,
+                                          int step) const {
+#pragma unroll
+        for (int i = 0; i < ITER; ++i) {
+            const int c = t + i * step;
+            if (c >= pieces) continue;
+            float2 y[P::V2];
+#pragma unroll
+            for (int p = 0; p < P::V2; ++p) y[p] = mul2(mul2(h[i][p], both(rq)), wq[i].get(p));
+            P o;
+            o.set(h[i]);
+            o.store(a.h, row * pieces + c);
+            o.set(y);
+            o.store(a.y, row * pieces + c);
+        }
+        if (t == 0 && a.rstd) a.rstd[2 * row] = rp, a.rstd[2 * row + 1] = rq;
+    }
+};
+
+// One row per team.  pieces: of a row; thread `t` of a team holds pieces t, t + 32 tw, ...
 template <typename T, int ITER, bool VEC>
 __global__ void __launch_bounds__(512) forward_kernel(const Args a, int tw, int pieces) {
     using P = Piece<T, VEC>;
@@ -151,204 +229,249 @@ __global__ void __launch_bounds__(512) forward_kernel(const Args a, int tw, int 
 #pragma unroll
     for (int i = 0; i < ITER; ++i) {
         const int c = t + i * step;
+        f[i].zero(), x[i].zero(), g[i].zero(), wp[i].zero(), wq[i].zero();
         if (c < pieces) {
             f[i].load(a.f, at + c), x[i].load(a.x, at + c);
             if (a.kind == RESIDUAL_GATE_ELEMENT) g[i].load(a.gate, at + c);
-        } else {
-            f[i].zero(), x[i].zero(), g[i].zero();
-        }
-    }
-#pragma unroll
-    for (int i = 0; i < ITER; ++i) {
-        const int c = t + i * step;
-        if (c < pieces) {
-            wp[i].load(a.w_post, c), wq[i].load(a.w_pre, c);
             if (a.kind == RESIDUAL_GATE_CHANNEL) g[i].load(a.gate, c);
-        } else {
-            wp[i].zero(), wq[i].zero(), g[i].zero();
+            wp[i].load(a.w_post, c), wq[i].load(a.w_pre, c);
         }
     }
-    float sum = 0.f;
-#pragma unroll
-    for (int i = 0; i < ITER; ++i)
-#pragma unroll
-        for (int e = 0; e < P::V; ++e) sum = fmaf(f[i].get(e), f[i].get(e), sum);
-    const float rp = 1.0f / sqrtf(team_sum(sum, red, turn, tw, warp) / (float)a.n + a.eps);
-    float h[ITER][P::V];
-    sum = 0.f;
-#pragma unroll
-    for (int i = 0; i < ITER; ++i)
-#pragma unroll
-        for (int e = 0; e < P::V; ++e) {
-            const float gate = a.kind == RESIDUAL_GATE_NONE ? 1.f : g[i].get(e);
-            h[i][e] = fmaf(a.scale * gate, f[i].get(e) * rp * wp[i].get(e), x[i].get(e));
-            sum = fmaf(h[i][e], h[i][e], sum);
-        }
-    const float rq = 1.0f / sqrtf(team_sum(sum, red, turn, tw, warp) / (float)a.n + a.eps);
-#pragma unroll
-    for (int i = 0; i < ITER; ++i) {
-        const int c = t + i * step;
-        if (c >= pieces) continue;
-        float y[P::V];
-#pragma unroll
-        for (int e = 0; e < P::V; ++e) y[e] = h[i][e] * rq * wq[i].get(e);
-        store_piece<T, VEC>(a.h, at + c, h[i]);
-        store_piece<T, VEC>(a.y, at + c, y);
-    }
-    if (t == 0 && a.rstd) a.rstd[2 * row] = rp, a.rstd[2 * row + 1] = rq;
+    ForwardRow<T, ITER, VEC> r;
+    r.run(f, x,
+          [&](int i, int p) {
+              const float2 w = mul2(wp[i].get(p), both(a.scale));
+              return a.kind == RESIDUAL_GATE_NONE ? w : mul2(w, g[i].get(p));
+          },
+          a, red, turn, tw, warp);
+    r.store(wq, a, row, pieces, t, step);
 }
 
-// The backward's inputs of one row and piece: 0 f, 1 h, 2 dy, 3 dh, 4 gate (per element).
-constexpr int kTensors = 5;
-// The ring's rows times ITER: 160 KB of shared memory for 16-byte pieces of 512 threads.
-constexpr int kRing = 4;
+// The ring's shared memory: 208 KB for 512 threads' 16-byte pieces, as many rows as fit (a thread's row: `tensors` x
+// `iter` pieces), at most 6.
+constexpr int ring_rows(int tensors, int iter) {
+    return 26 / (tensors * iter) > 6 ? 6 : 26 / (tensors * iter) > 0 ? 26 / (tensors * iter) : 1;
+}
 
-template <typename T, int ITER, bool VEC>
-__global__ void __launch_bounds__(512, 1) backward_kernel(const Args a, int tw, int pieces) {
-    using P = Piece<T, VEC>;
-    constexpr int V = P::V, RING = VEC ? kRing / ITER : 1;
-    extern __shared__ uint4 ring[];  // VEC: [stage][tensor][ITER][512]; then the teams' sums [3][n]
+// Persistent: each team walks its rows, the next ones' pieces in flight.  RING: rows of the ring.
+template <typename T, int ITER, bool ELEMENT, int RING>
+__global__ void __launch_bounds__(512, 1) forward_ring_kernel(const Args a, int tw, int pieces) {
+    using P = Piece<T, true>;
+    constexpr int K = ELEMENT ? 3 : 2;
+    extern __shared__ uint4 ring[];  // [RING][K][ITER][512]
     __shared__ float red[32];
     if (threadIdx.x == 0) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int warp = threadIdx.x >> 5, teams = 16 / tw, team = warp / tw;
     const int t = (warp - team * tw) * 32 + (threadIdx.x & 31), step = 32 * tw;
     const int64_t first = (int64_t)blockIdx.x * teams + team, stride = (int64_t)gridDim.x * teams;
-    const bool channel = a.kind == RESIDUAL_GATE_CHANNEL, element = a.kind == RESIDUAL_GATE_ELEMENT;
-    const void *src[kTensors] = {a.f, a.h, a.dy, a.dh, element ? a.gate : nullptr};
-    int turn = 0;
-    P wp[ITER], wq[ITER], gc[ITER], next[VEC ? 1 : kTensors][VEC ? 1 : ITER];
+    auto slot_of = [&](int slot, int k, int i) { return ring + ((slot * K + k) * ITER + i) * 512 + threadIdx.x; };
+    auto fetch = [&](int64_t row, int slot) {  // one group per row, empty past the last
+#pragma unroll
+        for (int i = 0; i < ITER; ++i) {
+            const int c = t + i * step;
+            if (row < a.m && c < pieces) {
+                copy16(slot_of(slot, 0, i), static_cast<const uint4 *>(a.f) + row * pieces + c);
+                copy16(slot_of(slot, 1, i), static_cast<const uint4 *>(a.x) + row * pieces + c);
+                if (ELEMENT) copy16(slot_of(slot, 2, i), static_cast<const uint4 *>(a.gate) + row * pieces + c);
+            }
+        }
+        copies_end();
+    };
+#pragma unroll
+    for (int s = 0; s < RING - 1; ++s) fetch(first + s * stride, s);
+    P wq[ITER];
+    float2 coef[ITER][P::V2];
+#pragma unroll
+    for (int i = 0; i < ITER; ++i) {
+        const int c = t + i * step;
+        P wp, g;
+        wp.zero(), g.zero(), wq[i].zero();
+        if (c < pieces) {
+            wp.load(a.w_post, c), wq[i].load(a.w_pre, c);
+            if (a.kind == RESIDUAL_GATE_CHANNEL) g.load(a.gate, c);
+        }
+#pragma unroll
+        for (int p = 0; p < P::V2; ++p) {
+            coef[i][p] = mul2(wp.get(p), both(a.scale));
+            if (a.kind == RESIDUAL_GATE_CHANNEL) coef[i][p] = mul2(coef[i][p], g.get(p));
+        }
+    }
+    int turn = 0, slot = 0;
+    for (int64_t row = first; row < a.m; row += stride) {
+        copies_wait<RING - 2>();  // RING - 1 rows are asked for: the oldest has landed
+        // The slot that this fills was read in the last iteration, by this thread alone.
+        fetch(row + (RING - 1) * stride, slot == 0 ? RING - 1 : slot - 1);
+        P f[ITER], x[ITER], g[ITER];
+#pragma unroll
+        for (int i = 0; i < ITER; ++i) {
+            f[i].zero(), x[i].zero(), g[i].zero();
+            if (t + i * step < pieces) {
+                f[i].raw = *slot_of(slot, 0, i), x[i].raw = *slot_of(slot, 1, i);
+                if (ELEMENT) g[i].raw = *slot_of(slot, 2, i);
+            }
+        }
+        ForwardRow<T, ITER, true> r;
+        r.run(f, x, [&](int i, int p) { return ELEMENT ? mul2(coef[i][p], g[i].get(p)) : coef[i][p]; }, a, red, turn, tw,
+              warp);
+        r.store(wq, a, row, pieces, t, step);
+        slot = slot == RING - 1 ? 0 : slot + 1;
+    }
+    copies_wait<0>();
+}
+
+// The backward.  With A = scale gate W_post (dZ W_post = G A), its sums over rows are
+//   post = sum of G F rp (times the gate where it is per element), pre = sum of dY H rq:
+// dW_post = scale gate post and dgate = scale W_post post for a channel's gate, so one sum serves both.
+// VEC: a ring of RING rows as in the forward; else the next row's elements wait in registers.
+template <typename T, int ITER, bool VEC, bool ELEMENT, int RING>
+__global__ void __launch_bounds__(512, 1) backward_kernel(const Args a, int tw, int pieces) {
+    using P = Piece<T, VEC>;
+    constexpr int V2 = P::V2, K = ELEMENT ? 5 : 4;  // 0 f, 1 h, 2 dy, 3 dh, 4 gate
+    extern __shared__ uint4 ring[];  // VEC: [RING][K][ITER][512]; then the teams' sums [2][n]
+    __shared__ float red[32];
+    if (threadIdx.x == 0) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int warp = threadIdx.x >> 5, teams = 16 / tw, team = warp / tw;
+    const int t = (warp - team * tw) * 32 + (threadIdx.x & 31), step = 32 * tw;
+    const int64_t first = (int64_t)blockIdx.x * teams + team, stride = (int64_t)gridDim.x * teams;
+    P next[VEC ? 1 : K][VEC ? 1 : ITER];
+    auto slot_of = [&](int slot, int k, int i) { return ring + ((slot * K + k) * ITER + i) * 512 + threadIdx.x; };
+    auto fetch = [&](int64_t row, int slot) {
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            const void *src = k == 0 ? a.f : k == 1 ? a.h : k == 2 ? a.dy : k == 3 ? a.dh : a.gate;
+#pragma unroll
+            for (int i = 0; i < ITER; ++i) {
+                const int c = t + i * step;
+                const bool in = row < a.m && c < pieces && src;
+                if constexpr (VEC) {
+                    if (in) copy16(slot_of(slot, k, i), static_cast<const uint4 *>(src) + row * pieces + c);
+                } else {
+                    next[k][i].zero();
+                    if (in) next[k][i].load(src, row * pieces + c);
+                }
+            }
+        }
+        if constexpr (VEC) copies_end();
+    };
+    float2 rstd_next = both(0.f);
+    auto fetch_rstd = [&](int64_t row) {
+        if (row < a.m) rstd_next = make_float2(__ldg(a.rstd + 2 * row), __ldg(a.rstd + 2 * row + 1));
+    };
+#pragma unroll
+    for (int s = 0; s < (RING > 1 ? RING - 1 : 1); ++s) fetch(first + s * stride, s);
+    fetch_rstd(first);
+    P wq[ITER], wp[ITER], gc[ITER];
+    float2 post[ITER][V2], pre[ITER][V2];
 #pragma unroll
     for (int i = 0; i < ITER; ++i) {
         const int c = t + i * step;
         wp[i].zero(), wq[i].zero(), gc[i].zero();
         if (c < pieces) {
             wp[i].load(a.w_post, c), wq[i].load(a.w_pre, c);
-            if (channel) gc[i].load(a.gate, c);
+            if (a.kind == RESIDUAL_GATE_CHANNEL) gc[i].load(a.gate, c);
         }
+#pragma unroll
+        for (int p = 0; p < V2; ++p) post[i][p] = pre[i][p] = both(0.f);
     }
-    // Asks for a row: into the ring's slot (one cp.async group per row, empty past the last), or into registers.
-    auto fetch = [&](int64_t row, int slot) {
-#pragma unroll
-        for (int k = 0; k < kTensors; ++k)
-#pragma unroll
-            for (int i = 0; i < ITER; ++i) {
-                const int c = t + i * step;
-                const bool in = row < a.m && c < pieces && src[k];
-                if constexpr (VEC) {
-                    if (in) {
-                        const uint32_t dst = (uint32_t)__cvta_generic_to_shared(
-                            ring + ((slot * kTensors + k) * ITER + i) * 512 + threadIdx.x);
-                        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst),
-                                     "l"(static_cast<const uint4 *>(src[k]) + row * pieces + c)
-                                     : "memory");
-                    }
-                } else {
-                    next[k][i].zero();
-                    if (in) next[k][i].load(src[k], row * pieces + c);
-                }
-            }
-        if constexpr (VEC) asm volatile("cp.async.commit_group;" ::: "memory");
-    };
-    float post[ITER][V], pre[ITER][V], gsum[ITER][V];
-#pragma unroll
-    for (int i = 0; i < ITER; ++i)
-#pragma unroll
-        for (int e = 0; e < V; ++e) post[i][e] = pre[i][e] = gsum[i][e] = 0.f;
-    float2 rstd_next = make_float2(0.f, 0.f);
-    auto fetch_rstd = [&](int64_t row) {
-        if (row < a.m) rstd_next = make_float2(__ldg(a.rstd + 2 * row), __ldg(a.rstd + 2 * row + 1));
-    };
-    if constexpr (VEC) {
-#pragma unroll
-        for (int s = 0; s < (RING > 1 ? RING - 1 : 1); ++s) fetch(first + s * stride, s);
-    } else {
-        fetch(first, 0);
-    }
-    fetch_rstd(first);
-    int slot = 0;
+    // scale W_post, and with it the gate: A.
+    auto weight = [&](int i, int p) { return mul2(wp[i].get(p), both(a.scale)); };
+    const bool channel = a.kind == RESIDUAL_GATE_CHANNEL;
+    int turn = 0, slot = 0;
     for (int64_t row = first; row < a.m; row += stride) {
-        P cur[VEC ? 1 : kTensors][VEC ? 1 : ITER];
+        P cur[VEC ? 1 : K][VEC ? 1 : ITER];
         if constexpr (VEC) {
-            // Rows row .. row + RING - 2 strides are asked for; this one has landed when RING - 2 groups are pending.
-            asm volatile("cp.async.wait_group %0;" ::"n"(RING > 2 ? RING - 2 : 0) : "memory");
+            copies_wait<(RING > 1 ? RING - 2 : 0)>();
         } else {
 #pragma unroll
-            for (int k = 0; k < kTensors; ++k)
+            for (int k = 0; k < K; ++k)
 #pragma unroll
                 for (int i = 0; i < ITER; ++i) cur[k][i] = next[k][i];
         }
         const float rp = rstd_next.x, rq = rstd_next.y;
-        // The slot that this fills was read in the last iteration, by this thread alone.
-        if (!VEC || RING > 1) fetch(row + (VEC ? RING - 1 : 1) * stride, (slot + RING - 1) % RING);
+        if (!VEC)
+            fetch(row + stride, 0);
+        else if (RING > 1)
+            fetch(row + (RING - 1) * stride, slot == 0 ? RING - 1 : slot - 1);
         fetch_rstd(row + stride);
         auto piece = [&](int k, int i) {
             P p;
             if constexpr (VEC)
-                p.raw = ring[((slot * kTensors + k) * ITER + i) * 512 + threadIdx.x];
+                p.raw = *slot_of(slot, k, i);
             else
                 p = cur[k][i];
             return p;
         };
-        float sum = 0.f;
+        float2 s = both(0.f);
 #pragma unroll
         for (int i = 0; i < ITER; ++i) {
             if (t + i * step >= pieces) continue;
             const P h = piece(1, i), dy = piece(2, i);
 #pragma unroll
-            for (int e = 0; e < V; ++e) {
-                const float hy = dy.get(e) * h.get(e);
-                sum = fmaf(wq[i].get(e), hy, sum);
-                pre[i][e] = fmaf(hy, rq, pre[i][e]);
+            for (int p = 0; p < V2; ++p) {
+                const float2 hy = mul2(dy.get(p), h.get(p));
+                s = fma2(wq[i].get(p), hy, s);
+                pre[i][p] = fma2(hy, both(rq), pre[i][p]);
             }
         }
-        const float c1 = rq * rq * (team_sum(sum, red, turn, tw, warp) / (float)a.n);
-        float g[ITER][V];
-        sum = 0.f;
+        const float c1 = rq * rq * (team_sum(sum2(s), red, turn, tw, warp) / (float)a.n);
+        float2 g[ITER][V2];
+        s = both(0.f);
 #pragma unroll
         for (int i = 0; i < ITER; ++i) {
             if (t + i * step >= pieces) continue;
             const P h = piece(1, i), dy = piece(2, i), f = piece(0, i);
-            P dh;
+            P dh, gate = gc[i];
             dh.zero();
             if (a.dh) dh = piece(3, i);
-            P gate = gc[i];
-            if (element) gate = piece(4, i);
+            if (ELEMENT) gate = piece(4, i);
 #pragma unroll
-            for (int e = 0; e < V; ++e) {
-                g[i][e] = fmaf(rq, wq[i].get(e) * dy.get(e) - h.get(e) * c1, dh.get(e));
-                const float u = a.scale * g[i][e], dz = a.kind == RESIDUAL_GATE_NONE ? u : u * gate.get(e);
-                sum = fmaf(wp[i].get(e) * dz, f.get(e), sum);
+            for (int p = 0; p < V2; ++p) {
+                const float2 x = fma2(h.get(p), both(-c1), mul2(wq[i].get(p), dy.get(p)));
+                g[i][p] = fma2(x, both(rq), dh.get(p));
+                float2 ga = mul2(g[i][p], weight(i, p));
+                if (ELEMENT || channel) ga = mul2(ga, gate.get(p));
+                s = fma2(ga, f.get(p), s);
             }
         }
-        const float c2 = rp * rp * (team_sum(sum, red, turn, tw, warp) / (float)a.n);
+        const float c2 = rp * rp * rp * (team_sum(sum2(s), red, turn, tw, warp) / (float)a.n);
 #pragma unroll
         for (int i = 0; i < ITER; ++i) {
             const int c = t + i * step;
             if (c >= pieces) continue;
             const P f = piece(0, i);
-            P gate = gc[i];
-            if (element) gate = piece(4, i);
-            float df[V], dg[V];
+            P gate = gc[i], o;
+            if (ELEMENT) gate = piece(4, i);
+            float2 df[V2], dg[V2];
 #pragma unroll
-            for (int e = 0; e < V; ++e) {
-                const float u = a.scale * g[i][e], fn = f.get(e) * rp, w = wp[i].get(e);
-                const float dz = a.kind == RESIDUAL_GATE_NONE ? u : u * gate.get(e);
-                df[e] = rp * (w * dz - f.get(e) * c2);
-                post[i][e] = fmaf(dz, fn, post[i][e]);
-                dg[e] = u * fn * w;
-                gsum[i][e] += dg[e];
+            for (int p = 0; p < V2; ++p) {
+                const float2 w = weight(i, p), fn = mul2(f.get(p), both(rp)), gf = mul2(g[i][p], fn);
+                float2 ga = mul2(g[i][p], w);
+                if (ELEMENT || channel) ga = mul2(ga, gate.get(p));
+                df[p] = fma2(f.get(p), both(-c2), mul2(ga, both(rp)));
+                if (ELEMENT) {
+                    post[i][p] = fma2(gf, gate.get(p), post[i][p]);
+                    dg[p] = mul2(gf, w);
+                } else {
+                    post[i][p] = add2(post[i][p], gf);
+                }
             }
-            store_piece<T, VEC>(a.df, row * pieces + c, df);
-            store_piece<T, VEC>(a.dx, row * pieces + c, g[i]);
-            if (element) store_piece<T, VEC>(a.dgate, row * pieces + c, dg);
+            o.set(df);
+            o.store(a.df, row * pieces + c);
+            o.set(g[i]);
+            o.store(a.dx, row * pieces + c);
+            if (ELEMENT) {
+                o.set(dg);
+                o.store(a.dgate, row * pieces + c);
+            }
         }
         if (VEC && RING == 1) fetch(row + stride, 0);  // the row is read: its place is the next one's
-        slot = (slot + 1) % RING;
+        slot = slot == RING - 1 ? 0 : slot + 1;
     }
     // One partial row per block, teams added in their order.
-    float *part = a.partial + (int64_t)blockIdx.x * 3 * a.n, *all = reinterpret_cast<float *>(ring);
-    if constexpr (VEC) asm volatile("cp.async.wait_group 0;" ::: "memory");
+    float *part = a.partial + (int64_t)blockIdx.x * 2 * a.n, *all = reinterpret_cast<float *>(ring);
+    if constexpr (VEC) copies_wait<0>();
     for (int k = 0; k < teams; ++k) {
         __syncthreads();
         if (team != k) continue;
@@ -358,11 +481,11 @@ __global__ void __launch_bounds__(512, 1) backward_kernel(const Args a, int tw, 
             const int c = t + i * step;
             if (c >= pieces) continue;
 #pragma unroll
-            for (int e = 0; e < V; ++e) {
-                const int j = c * V + e;
-                dst[j] = post[i][e] + (k ? all[j] : 0.f);
-                dst[a.n + j] = pre[i][e] + (k ? all[a.n + j] : 0.f);
-                if (channel) dst[2 * a.n + j] = gsum[i][e] + (k ? all[2 * a.n + j] : 0.f);
+            for (int e = 0; e < P::V; ++e) {
+                const int j = c * P::V + e;
+                const float x = e % 2 ? post[i][e / 2].y : post[i][e / 2].x, y = e % 2 ? pre[i][e / 2].y : pre[i][e / 2].x;
+                dst[j] = x + (k ? all[j] : 0.f);
+                dst[a.n + j] = y + (k ? all[a.n + j] : 0.f);
             }
         }
     }
@@ -396,15 +519,13 @@ __global__ void __launch_bounds__(kThreads) forward_row_kernel(const Args a) {
     if (threadIdx.x == 0 && a.rstd) a.rstd[2 * row] = rp, a.rstd[2 * row + 1] = rq;
 }
 
-// Partial sums of block b: partial[b][0] dw_post, [1] dw_pre, [2] dgate (per channel), n values each; thread j % 256
-// alone adds to column j.
+// Partial sums of block b: partial[b][0] post, [1] pre as above, n values each; thread j % 256 alone adds to column j.
 template <typename T>
 __global__ void __launch_bounds__(kThreads) backward_row_kernel(const Args a) {
     __shared__ float s[kThreads / 32];
     const T *wp = static_cast<const T *>(a.w_post), *wq = static_cast<const T *>(a.w_pre);
-    float *part = a.partial + (int64_t)blockIdx.x * 3 * a.n;
-    for (int j = threadIdx.x; j < 3 * a.n; j += kThreads) part[j] = 0.f;
-    __syncthreads();
+    float *part = a.partial + (int64_t)blockIdx.x * 2 * a.n;
+    for (int j = threadIdx.x; j < a.n; j += kThreads) part[j] = part[a.n + j] = 0.f;
     for (int64_t row = blockIdx.x; row < a.m; row += gridDim.x) {
         const int64_t at = row * a.n;
         const T *f = static_cast<const T *>(a.f) + at, *h = static_cast<const T *>(a.h) + at;
@@ -423,42 +544,46 @@ __global__ void __launch_bounds__(kThreads) backward_row_kernel(const Args a) {
             sum = fmaf(to_f(wp[j]) * (a.scale * total(j) * gate_at<T>(a, row, j)), to_f(f[j]), sum);
         const float e = rp * rp * (block_sum(sum, s) / (float)a.n);
         for (int j = threadIdx.x; j < a.n; j += kThreads) {
-            const float gj = total(j), u = a.scale * gj, fn = to_f(f[j]) * rp, dz = u * gate_at<T>(a, row, j);
-            const float dg = u * fn * to_f(wp[j]);
-            df[j] = from_f<T>(rp * (to_f(wp[j]) * dz - to_f(f[j]) * e));
-            part[j] += dz * fn;
+            const float gj = total(j), gf = gj * to_f(f[j]) * rp, gate = gate_at<T>(a, row, j);
+            const float w = to_f(wp[j]) * a.scale;
+            df[j] = from_f<T>(rp * (w * gj * gate - to_f(f[j]) * e));
+            part[j] += a.kind == RESIDUAL_GATE_ELEMENT ? gf * gate : gf;
             part[a.n + j] += to_f(dy[j]) * to_f(h[j]) * rq;
-            if (a.kind == RESIDUAL_GATE_CHANNEL) part[2 * a.n + j] += dg;
-            if (a.kind == RESIDUAL_GATE_ELEMENT) static_cast<T *>(a.dgate)[at + j] = from_f<T>(dg);
+            if (a.kind == RESIDUAL_GATE_ELEMENT) static_cast<T *>(a.dgate)[at + j] = from_f<T>(gf * w);
             dx[j] = from_f<T>(gj);  // last: dX may be dH's buffer
         }
     }
 }
 
-// Columns of the blocks' partial rows added up: 32 columns per block, 8 warps taking every 8th row, then their sums in
-// order.
+// The blocks' partial rows added up: 32 columns per block, 8 warps taking every 8th row, then their sums in order.
+template <typename T>
 __global__ void __launch_bounds__(kThreads) partial_sum_kernel(const Args a) {
     __shared__ float s[kThreads / 32][32];
+    if (threadIdx.x == 0) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int64_t j = (int64_t)blockIdx.x * 32 + lane, cols = (int64_t)(a.kind == RESIDUAL_GATE_CHANNEL ? 3 : 2) * a.n;
+    const int64_t j = (int64_t)blockIdx.x * 32 + lane;
     float t = 0.f;
-    if (j < cols) {
+    if (j < 2 * (int64_t)a.n) {
 #pragma unroll 8
-        for (int b = warp; b < a.blocks; b += kThreads / 32) t += __ldcg(a.partial + (int64_t)b * 3 * a.n + j);
+        for (int b = warp; b < a.blocks; b += kThreads / 32) t += __ldcg(a.partial + (int64_t)b * 2 * a.n + j);
     }
     s[warp][lane] = t;
     __syncthreads();
-    if (warp != 0 || j >= cols) return;
+    if (warp != 0 || j >= 2 * (int64_t)a.n) return;
     t = 0.f;
 #pragma unroll
     for (int w = 0; w < kThreads / 32; ++w) t += s[w][lane];
-    if (j < a.n)
-        a.dw_post[j] = t;
-    else if (j < 2 * (int64_t)a.n)
+    if (j >= a.n) {
         a.dw_pre[j - a.n] = t;
-    else
-        static_cast<float *>(a.dgate)[j - 2 * (int64_t)a.n] = t;
+        return;
+    }
+    t *= a.scale;
+    if (a.kind == RESIDUAL_GATE_CHANNEL) {
+        static_cast<float *>(a.dgate)[j] = t * to_f(static_cast<const T *>(a.w_post)[j]);
+        t *= to_f(static_cast<const T *>(a.gate)[j]);
+    }
+    a.dw_post[j] = t;
 }
 
 bool aligned(const void *ptr, uintptr_t a) { return (reinterpret_cast<uintptr_t>(ptr) & (a - 1)) == 0; }
@@ -487,7 +612,7 @@ int check(const residual_rmsnorm_params *p, int dtype, const void *gate, const P
 int blocks_of(const residual_rmsnorm_params *p) { return p->m < (uint32_t)kMaxBlocks ? (int)p->m : kMaxBlocks; }
 
 size_t workspace_bytes_of(const residual_rmsnorm_params *p) {
-    return (size_t)blocks_of(p) * 3 * p->n * sizeof(float);
+    return (size_t)blocks_of(p) * 2 * p->n * sizeof(float);
 }
 
 // A launch that may start while the kernel before it ends (each kernel waits before it touches memory).
@@ -506,15 +631,17 @@ int launch(K kern, int64_t blocks, int threads, size_t smem, cudaStream_t st, A.
     return cudaLaunchKernelEx(&cfg, kern, args...) == cudaSuccess ? DGRAD_OK : DGRAD_ERR_CUDA;
 }
 
-// How a row of `pieces` is laid over a team: `warps` (a power of two up to 16) x 32 threads x `iter` pieces, as few
-// pieces per thread as 16 warps allow but at least `least`; iter 0 when 4 pieces (8 single elements) do not reach.
+// How a row of `pieces` is laid over a team of `warps` (a power of two) x 32 threads x `iter` pieces: teams of up to 8
+// warps first, then two pieces per thread, then 16 warps; iter 0 when `most` pieces per thread do not reach.
 struct Layout {
     int warps, iter;
 };
-Layout layout_of(int64_t pieces, int least, int most) {
-    for (int it = least; it <= most; it *= 2)
-        for (int w = 1; w <= 16; w *= 2)
-            if (pieces <= (int64_t)32 * w * it) return {w, it};
+Layout layout_of(int64_t pieces, int most) {
+    for (int w = 1; w <= 8; w *= 2)
+        if (pieces <= 32 * w) return {w, 1};
+    if (pieces <= 32 * 8 * 2 && most >= 2) return {8, 2};
+    for (int it = 1; it <= most; it *= 2)
+        if (pieces <= (int64_t)32 * 16 * it) return {16, it};
     return {0, 0};
 }
 
@@ -523,35 +650,71 @@ bool vector_applies(int n, size_t esize, const P *...ptr) {
     return (size_t)n * esize % 16 == 0 && (aligned(ptr, 16) && ...);
 }
 
+// Dynamic shared memory above 48 KB is allowed once per kernel and device.
+template <typename K>
+int allow_smem(K kern, size_t smem, std::atomic<uint64_t> &configured) {
+    if (smem <= 48 * 1024) return DGRAD_OK;
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return DGRAD_ERR_CUDA;
+    const uint64_t bit = dev < 64 ? (uint64_t)1 << dev : 0;
+    if (bit && (configured.load() & bit)) return DGRAD_OK;
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
+        return DGRAD_ERR_CUDA;
+    configured.fetch_or(bit);
+    return DGRAD_OK;
+}
+
+template <typename T, int ITER, bool ELEMENT>
+int forward_ring(const Args &a, int tw, int pieces, cudaStream_t st) {
+    constexpr int R = ring_rows(ELEMENT ? 3 : 2, ITER);
+    const size_t smem = (size_t)R * (ELEMENT ? 3 : 2) * ITER * 512 * 16;
+    static std::atomic<uint64_t> configured{0};
+    auto kern = forward_ring_kernel<T, ITER, ELEMENT, R>;
+    const int rc = allow_smem(kern, smem, configured);
+    return rc != DGRAD_OK ? rc : launch(kern, kMaxBlocks, 512, smem, st, a, tw, pieces);
+}
+
 template <typename T, int ITER, bool VEC>
-int forward_iter(const Args &a, int tw, int pieces, cudaStream_t st) {
+int forward_direct(const Args &a, int tw, int pieces, cudaStream_t st) {
     const int warps = tw < 8 ? 8 : tw, teams = warps / tw;
     return launch(forward_kernel<T, ITER, VEC>, ((int64_t)a.m + teams - 1) / teams, 32 * warps, 0, st, a, tw, pieces);
+}
+
+template <typename T, int ITER>
+int forward_vec(const Args &a, int tw, int pieces, cudaStream_t st) {
+    if (a.m <= kRingRows * kMaxBlocks * (16 / tw)) return forward_direct<T, ITER, true>(a, tw, pieces, st);
+    if (a.kind == RESIDUAL_GATE_ELEMENT) return forward_ring<T, ITER, true>(a, tw, pieces, st);
+    return forward_ring<T, ITER, false>(a, tw, pieces, st);
 }
 
 template <typename T>
 int forward_t(const Args &a, cudaStream_t st) {
     const bool vec = vector_applies(a.n, sizeof(T), a.f, a.x, a.gate, a.w_post, a.w_pre, a.h, a.y);
     const int pieces = vec ? a.n * (int)sizeof(T) / 16 : a.n;
-    const Layout l = layout_of(pieces, 1, vec ? 4 : 8);
-    if (vec && l.iter == 1) return forward_iter<T, 1, true>(a, l.warps, pieces, st);
-    if (vec && l.iter == 2) return forward_iter<T, 2, true>(a, l.warps, pieces, st);
-    if (vec && l.iter == 4) return forward_iter<T, 4, true>(a, l.warps, pieces, st);
-    if (l.iter == 1 || l.iter == 2) return forward_iter<T, 2, false>(a, l.warps, pieces, st);
-    if (l.iter == 4 || l.iter == 8) return forward_iter<T, 8, false>(a, l.warps, pieces, st);
+    const Layout l = layout_of(pieces, vec ? 4 : 8);
+    if (vec && l.iter == 1) return forward_vec<T, 1>(a, l.warps, pieces, st);
+    if (vec && l.iter == 2) return forward_vec<T, 2>(a, l.warps, pieces, st);
+    if (vec && l.iter == 4) return forward_vec<T, 4>(a, l.warps, pieces, st);
+    if (l.iter == 1 || l.iter == 2) return forward_direct<T, 2, false>(a, l.warps, pieces, st);
+    if (l.iter == 4 || l.iter == 8) return forward_direct<T, 8, false>(a, l.warps, pieces, st);
     forward_row_kernel<T><<<a.m, kThreads, 0, st>>>(a);
     return cudaGetLastError() == cudaSuccess ? DGRAD_OK : DGRAD_ERR_CUDA;
 }
 
-template <typename T, int ITER, bool VEC>
+template <typename T, int ITER, bool VEC, bool ELEMENT>
 int backward_iter(const Args &a, int tw, int pieces, cudaStream_t st) {
-    const size_t ring = VEC ? (size_t)kRing * kTensors * 512 * 16 : 0;
-    const size_t sums = tw < 16 ? (size_t)3 * a.n * sizeof(float) : 0, smem = std::max(ring, sums);
-    auto kern = backward_kernel<T, ITER, VEC>;
-    if (smem > 48 * 1024 &&
-        cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
-        return DGRAD_ERR_CUDA;
-    return launch(kern, a.blocks, 512, smem, st, a, tw, pieces);
+    constexpr int K = ELEMENT ? 5 : 4, R = VEC ? ring_rows(K, ITER) : 1;
+    const size_t row = VEC ? (size_t)K * ITER * 512 * 16 : 0, sums = tw < 16 ? (size_t)2 * a.n * sizeof(float) : 0;
+    const size_t smem = std::max(R * row, sums);
+    static std::atomic<uint64_t> configured{0};
+    auto kern = backward_kernel<T, ITER, VEC, ELEMENT, R>;
+    const int rc = allow_smem(kern, smem, configured);
+    return rc != DGRAD_OK ? rc : launch(kern, a.blocks, 512, smem, st, a, tw, pieces);
+}
+template <typename T, int ITER, bool VEC>
+int backward_kind(const Args &a, int tw, int pieces, cudaStream_t st) {
+    if (a.kind == RESIDUAL_GATE_ELEMENT) return backward_iter<T, ITER, VEC, true>(a, tw, pieces, st);
+    return backward_iter<T, ITER, VEC, false>(a, tw, pieces, st);
 }
 
 template <typename T>
@@ -560,17 +723,17 @@ int backward_rows(Args &a, cudaStream_t st) {
     const bool vec =
         vector_applies(a.n, sizeof(T), a.f, a.h, a.gate, a.w_post, a.w_pre, a.dy, a.dh, a.df, a.dx, dgate);
     const int pieces = vec ? a.n * (int)sizeof(T) / 16 : a.n;
-    const Layout l = layout_of(pieces, 1, vec ? (sizeof(T) == 4 ? 4 : 2) : 8);
+    const Layout l = layout_of(pieces, vec ? (sizeof(T) == 4 ? 4 : 2) : 8);
     if (l.iter) {
         const int64_t teams = 16 / l.warps, need = (a.m + teams - 1) / teams;
         a.blocks = need < a.blocks ? (int)need : a.blocks;
     }
-    if (vec && l.iter == 1) return backward_iter<T, 1, true>(a, l.warps, pieces, st);
-    if (vec && l.iter == 2) return backward_iter<T, 2, true>(a, l.warps, pieces, st);
+    if (vec && l.iter == 1) return backward_kind<T, 1, true>(a, l.warps, pieces, st);
+    if (vec && l.iter == 2) return backward_kind<T, 2, true>(a, l.warps, pieces, st);
     if constexpr (sizeof(T) == 4)
-        if (vec && l.iter == 4) return backward_iter<T, 4, true>(a, l.warps, pieces, st);
-    if (!vec && (l.iter == 1 || l.iter == 2)) return backward_iter<T, 2, false>(a, l.warps, pieces, st);
-    if (!vec && (l.iter == 4 || l.iter == 8)) return backward_iter<T, 8, false>(a, l.warps, pieces, st);
+        if (vec && l.iter == 4) return backward_kind<T, 4, true>(a, l.warps, pieces, st);
+    if (!vec && (l.iter == 1 || l.iter == 2)) return backward_kind<T, 2, false>(a, l.warps, pieces, st);
+    if (!vec && (l.iter == 4 || l.iter == 8)) return backward_kind<T, 8, false>(a, l.warps, pieces, st);
     backward_row_kernel<T><<<a.blocks, kThreads, 0, st>>>(a);
     return cudaGetLastError() == cudaSuccess ? DGRAD_OK : DGRAD_ERR_CUDA;
 }
@@ -579,8 +742,7 @@ template <typename T>
 int backward_t(Args &a, cudaStream_t st) {
     const int rc = backward_rows<T>(a, st);
     if (rc != DGRAD_OK) return rc;
-    const int64_t cols = (int64_t)(a.kind == RESIDUAL_GATE_CHANNEL ? 3 : 2) * a.n;
-    return launch(partial_sum_kernel, (cols + 31) / 32, kThreads, 0, st, a);
+    return launch(partial_sum_kernel<T>, (2 * (int64_t)a.n + 31) / 32, kThreads, 0, st, a);
 }
 
 }  // namespace
