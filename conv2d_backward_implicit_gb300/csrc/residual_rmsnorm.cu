@@ -109,6 +109,35 @@ __device__ __forceinline__ float team_sum(float x, float *red, int &turn, int tw
     return x;
 }
 
+// Four sums at once over a team, `red` [2][64] floats.  Within a warp each step halves what a lane carries (6 shuffles):
+// after xor 16 and 8, lanes 8 k .. 8 k + 7 hold sum k.
+__device__ __forceinline__ float4 team_sum4(float4 x, float *red, int &turn, int tw, int warp) {
+    const int lane = threadIdx.x & 31;
+    const bool hi = lane & 16, up = lane & 8;
+    float a = hi ? x.z : x.x, b = hi ? x.w : x.y;
+    a += __shfl_xor_sync(0xffffffffu, hi ? x.x : x.z, 16);
+    b += __shfl_xor_sync(0xffffffffu, hi ? x.y : x.w, 16);
+    float v = up ? b : a;
+    v += __shfl_xor_sync(0xffffffffu, up ? a : b, 8);
+#pragma unroll
+    for (int o = 4; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    if (tw > 1) {
+        float *r = red + 64 * turn;
+        turn ^= 1;
+        const int team = warp / tw;
+        if ((lane & 7) == 0) r[warp * 4 + (lane >> 3)] = v;
+        team_barrier(team, tw);
+        const int n = 4 * tw, at = team * n;
+        v = r[at + (lane & (n - 1))];
+        if (tw == 16) v += r[at + 32 + lane];
+        for (int o = (n < 32 ? n : 32) >> 1; o >= 4; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+        return make_float4(__shfl_sync(0xffffffffu, v, 0), __shfl_sync(0xffffffffu, v, 1),
+                           __shfl_sync(0xffffffffu, v, 2), __shfl_sync(0xffffffffu, v, 3));
+    }
+    return make_float4(__shfl_sync(0xffffffffu, v, 0), __shfl_sync(0xffffffffu, v, 8), __shfl_sync(0xffffffffu, v, 16),
+                       __shfl_sync(0xffffffffu, v, 24));
+}
+
 // A piece of a row: V elements, 16 bytes or one element, seen as V2 pairs of floats (a single element's partner is 0).
 template <typename T, bool VEC>
 struct Piece {
@@ -320,8 +349,10 @@ __global__ void __launch_bounds__(512, 1) forward_ring_kernel(const Args a, int 
     copies_wait<0>();
 }
 
-// The backward.  With A = scale gate W_post (dZ W_post = G A), its sums over rows are
-//   post = sum of G F rp (times the gate where it is per element), pre = sum of dY H rq:
+// The backward.  With A = scale gate W_post (so W_post dZ = G A), the sum over F's row takes G apart,
+//   sum G A F = sum A F dH + rq (sum A F W_pre dY - c1 sum A F H),  c1 = rq^2 mean(W_pre dY H),
+// so that both statistics of a row come from four sums of one pass, one reduction and one barrier.  The sums over
+// rows are post = sum of G F rp (times the gate where it is per element) and pre = sum of dY H rq:
 // dW_post = scale gate post and dgate = scale W_post post for a channel's gate, so one sum serves both.
 // VEC: a ring of RING rows as in the forward; else the next row's elements wait in registers.
 template <typename T, int ITER, bool VEC, bool ELEMENT, int RING>
@@ -329,7 +360,7 @@ __global__ void __launch_bounds__(512, 1) backward_kernel(const Args a, int tw, 
     using P = Piece<T, VEC>;
     constexpr int V2 = P::V2, K = ELEMENT ? 5 : 4;  // 0 f, 1 h, 2 dy, 3 dh, 4 gate
     extern __shared__ uint4 ring[];  // VEC: [RING][K][ITER][512]; then the teams' sums [2][n]
-    __shared__ float red[32];
+    __shared__ float red[128];
     if (threadIdx.x == 0) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int warp = threadIdx.x >> 5, teams = 16 / tw, team = warp / tw;
@@ -403,21 +434,7 @@ __global__ void __launch_bounds__(512, 1) backward_kernel(const Args a, int tw, 
                 p = cur[k][i];
             return p;
         };
-        float2 s = both(0.f);
-#pragma unroll
-        for (int i = 0; i < ITER; ++i) {
-            if (t + i * step >= pieces) continue;
-            const P h = piece(1, i), dy = piece(2, i);
-#pragma unroll
-            for (int p = 0; p < V2; ++p) {
-                const float2 hy = mul2(dy.get(p), h.get(p));
-                s = fma2(wq[i].get(p), hy, s);
-                pre[i][p] = fma2(hy, both(rq), pre[i][p]);
-            }
-        }
-        const float c1 = rq * rq * (team_sum(sum2(s), red, turn, tw, warp) / (float)a.n);
-        float2 g[ITER][V2];
-        s = both(0.f);
+        float2 s1 = both(0.f), s2 = both(0.f), s3 = both(0.f), s4 = both(0.f);
 #pragma unroll
         for (int i = 0; i < ITER; ++i) {
             if (t + i * step >= pieces) continue;
@@ -428,26 +445,35 @@ __global__ void __launch_bounds__(512, 1) backward_kernel(const Args a, int tw, 
             if (ELEMENT) gate = piece(4, i);
 #pragma unroll
             for (int p = 0; p < V2; ++p) {
-                const float2 x = fma2(h.get(p), both(-c1), mul2(wq[i].get(p), dy.get(p)));
-                g[i][p] = fma2(x, both(rq), dh.get(p));
-                float2 ga = mul2(g[i][p], weight(i, p));
-                if (ELEMENT || channel) ga = mul2(ga, gate.get(p));
-                s = fma2(ga, f.get(p), s);
+                const float2 wy = mul2(wq[i].get(p), dy.get(p));
+                float2 af = mul2(weight(i, p), f.get(p));
+                if (ELEMENT || channel) af = mul2(af, gate.get(p));
+                s1 = fma2(wy, h.get(p), s1);
+                s2 = fma2(af, dh.get(p), s2);
+                s3 = fma2(af, wy, s3);
+                s4 = fma2(af, h.get(p), s4);
+                pre[i][p] = fma2(mul2(dy.get(p), h.get(p)), both(rq), pre[i][p]);
             }
         }
-        const float c2 = rp * rp * rp * (team_sum(sum2(s), red, turn, tw, warp) / (float)a.n);
+        const float4 z = team_sum4(make_float4(sum2(s1), sum2(s2), sum2(s3), sum2(s4)), red, turn, tw, warp);
+        const float c1 = rq * rq * (z.x / (float)a.n);
+        const float c2 = rp * rp * rp * (fmaf(rq, z.z - c1 * z.w, z.y) / (float)a.n);
 #pragma unroll
         for (int i = 0; i < ITER; ++i) {
             const int c = t + i * step;
             if (c >= pieces) continue;
-            const P f = piece(0, i);
-            P gate = gc[i], o;
+            const P h = piece(1, i), dy = piece(2, i), f = piece(0, i);
+            P dh, gate = gc[i], o;
+            dh.zero();
+            if (a.dh) dh = piece(3, i);
             if (ELEMENT) gate = piece(4, i);
-            float2 df[V2], dg[V2];
+            float2 g[V2], df[V2], dg[V2];
 #pragma unroll
             for (int p = 0; p < V2; ++p) {
-                const float2 w = weight(i, p), fn = mul2(f.get(p), both(rp)), gf = mul2(g[i][p], fn);
-                float2 ga = mul2(g[i][p], w);
+                const float2 x = fma2(h.get(p), both(-c1), mul2(wq[i].get(p), dy.get(p)));
+                g[p] = fma2(x, both(rq), dh.get(p));
+                const float2 w = weight(i, p), gf = mul2(g[p], mul2(f.get(p), both(rp)));
+                float2 ga = mul2(g[p], w);
                 if (ELEMENT || channel) ga = mul2(ga, gate.get(p));
                 df[p] = fma2(f.get(p), both(-c2), mul2(ga, both(rp)));
                 if (ELEMENT) {
@@ -459,7 +485,7 @@ __global__ void __launch_bounds__(512, 1) backward_kernel(const Args a, int tw, 
             }
             o.set(df);
             o.store(a.df, row * pieces + c);
-            o.set(g[i]);
+            o.set(g);
             o.store(a.dx, row * pieces + c);
             if (ELEMENT) {
                 o.set(dg);
