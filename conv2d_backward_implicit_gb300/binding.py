@@ -95,6 +95,8 @@ def library_path() -> str:
 def library() -> ctypes.CDLL:
     """The loaded C library (raises if it has not been built)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             path = library_path()
@@ -398,54 +400,92 @@ def mha_grad_v_check_errors(stream=None) -> int:
     return int(library().mha_grad_v_check_errors(_stream(stream)))
 
 
-def _dense(dtype: str | None, *buffers):
-    """Addresses of dense buffers given as (x, name, elements) or (x, name, elements, dtype): the checks of
-    _addr, with one comparison per property for a torch tensor that passes them."""
-    import torch
-    device, out = -1, []
-    for x, name, numel, *own in buffers:
-        t = own[0] if own else dtype
-        if isinstance(x, torch.Tensor) and x.is_cuda:
-            if device < 0:
-                device = torch.cuda.current_device()
-            if (x.get_device() == device and x.numel() == numel and x.is_contiguous()
-                    and (t is None or x.dtype is getattr(torch, t))):
-                out.append(x.data_ptr())
-                continue
-        out.append(_addr(x, name, t, numel))
+_types: dict = {}
+
+
+def _torch_types() -> dict:
+    """torch's element types by dgrad_dtype code and by name (torch is imported at the first call)."""
+    if not _types:
+        import torch
+        _types.update({DGRAD_F32: torch.float32, DGRAD_BF16: torch.bfloat16, DGRAD_F16: torch.float16,
+                       "float32": torch.float32, "int32": torch.int32, "current_device": torch.cuda.current_device})
+    return _types
+
+
+def _dense(dtype, device: int, *buffers):
+    """Addresses of dense buffers given as (x, name, elements, type), with ``dtype`` (a dgrad_dtype code) where the
+    type is None.  These are the checks of _addr, one comparison per property for a tensor that passes them; whatever
+    does not pass goes to _addr, which names what is wrong."""
+    types, out = _torch_types(), []
+    for x, name, numel, t in buffers:
+        if x is not None and type(x) is not int:
+            try:
+                if (x.get_device() == device and x.numel() == numel and x.is_contiguous()
+                        and x.dtype is types[dtype if t is None else t]):
+                    out.append(x.data_ptr())
+                    continue
+            except (AttributeError, KeyError):
+                pass
+            x = _addr(x, name, _in_dtype(dtype) if t is None else t, numel)
+        out.append(x)
     return out
 
 
-def _token_rows(x, name: str, dtype: str | None, tokens: int, heads: int, head_dim: int, stride: int):
+def _device_of(*tensors) -> int:
+    """The current device, or a number no tensor has when none of the arguments is on a GPU (then _addr says so)."""
+    if any(getattr(x, "is_cuda", False) for x in tensors):
+        return _torch_types()["current_device"]()
+    return -2
+
+
+def _stream_on(stream, device: int):
+    """_stream for a torch stream, with one comparison when it belongs to ``device``."""
+    if stream is None or type(stream) is int:
+        return stream
+    return stream.cuda_stream if getattr(stream, "device_index", None) == device else _stream(stream)
+
+
+def _token_rows(x, name: str, dtype, device: int, tokens: int, heads: int, head_dim: int, stride: int):
     """Address of a [tokens, heads, head_dim] tensor whose tokens are ``stride`` elements apart (0: dense)."""
     dense = heads * head_dim
     row = stride or dense
     shape = getattr(x, "shape", None)
     if row == dense or shape is None:
-        return _dense(dtype, (x, name, tokens * dense))[0]
+        return _dense(dtype, device, (x, name, tokens * dense, None))[0]
     if tuple(shape) != (tokens, heads, head_dim):
         raise ValueError(f"{name} must have shape {(tokens, heads, head_dim)} for these params (got {tuple(shape)})")
     for have, want, size in zip(x.stride(), (row, head_dim, 1), shape):
         if size > 1 and have != want:
             raise ValueError(f"{name} must have strides {(row, head_dim, 1)} for these params (got {x.stride()})")
-    _addr(x[0].reshape(-1), name, dtype, dense)  # the device and the element type
+    if x.get_device() != device or x.dtype is not _torch_types().get(dtype):
+        _addr(x[0].reshape(-1), name, _in_dtype(dtype), dense)  # says what is wrong
     return x.data_ptr()
 
 
-def _packed_qkv(q, k, v, p: MhaPackedParams, t: str | None):
+def _packed_qkv(q, k, v, p: MhaPackedParams, t, dev: int):
     n, h, g, d = p.tokens, p.num_heads, p.num_kv_heads, p.head_dim
-    return [_token_rows(q, "q", t, n, h, d, p.q_stride), _token_rows(k, "k", t, n, g, d, p.k_stride),
-            _token_rows(v, "v", t, n, g, d, p.v_stride)]
+    return [_token_rows(q, "q", t, dev, n, h, d, p.q_stride), _token_rows(k, "k", t, dev, n, g, d, p.k_stride),
+            _token_rows(v, "v", t, dev, n, g, d, p.v_stride)]
+
+
+def _workspace(x, nbytes: int, device: int):
+    """Address of a workspace of at least ``nbytes`` bytes."""
+    try:
+        if x.get_device() == device and x.is_contiguous() and x.numel() * x.element_size() >= nbytes:
+            return x.data_ptr()
+    except AttributeError:
+        pass
+    return _addr(x, "workspace", min_bytes=int(nbytes))
 
 
 def mha_packed_forward(q, k, v, seq_offsets, o, lse, params: MhaPackedParams, dtype: int, stream=None) -> None:
     """O and LSE of causal attention over packed sequences (include/mha_packed.h)."""
-    t, rows = _in_dtype(dtype), params.tokens * params.num_heads
+    dev, rows = _device_of(q), params.tokens * params.num_heads
     rc = library().mha_packed_forward(
-        *_packed_qkv(q, k, v, params, t),
-        *_dense(t, (seq_offsets, "seq_offsets", params.num_seqs + 1, "int32"), (o, "o", rows * params.head_dim),
-                (lse, "lse", rows * 2, "float32")),
-        ctypes.byref(params), int(dtype), _stream(stream))
+        *_packed_qkv(q, k, v, params, dtype, dev),
+        *_dense(dtype, dev, (seq_offsets, "seq_offsets", params.num_seqs + 1, "int32"),
+                (o, "o", rows * params.head_dim, None), (lse, "lse", rows * 2, "float32")),
+        ctypes.byref(params), int(dtype), _stream_on(stream, dev))
     _check(rc, "mha_packed_forward")
 
 
@@ -456,34 +496,35 @@ def mha_packed_workspace_size(params: MhaPackedParams, dtype: int) -> int:
 def mha_packed_backward(q, k, v, o, d_out, lse, seq_offsets, dq, dk, dv, workspace, workspace_bytes: int,
                         params: MhaPackedParams, dtype: int, stream=None) -> None:
     """dQ, dK and dV of causal attention over packed sequences (include/mha_packed.h)."""
-    t, rows = _in_dtype(dtype), params.tokens * params.num_heads
+    dev, rows = _device_of(q), params.tokens * params.num_heads
     n_q, n_kv = rows * params.head_dim, params.tokens * params.num_kv_heads * params.head_dim
     rc = library().mha_packed_backward(
-        *_packed_qkv(q, k, v, params, t),
-        *_dense(t, (o, "o", n_q), (d_out, "d_out", n_q), (lse, "lse", rows * 2, "float32"),
-                (seq_offsets, "seq_offsets", params.num_seqs + 1, "int32"), (dq, "dq", n_q), (dk, "dk", n_kv),
-                (dv, "dv", n_kv)),
-        _addr(workspace, "workspace", min_bytes=int(workspace_bytes)), int(workspace_bytes), ctypes.byref(params),
-        int(dtype), _stream(stream))
+        *_packed_qkv(q, k, v, params, dtype, dev),
+        *_dense(dtype, dev, (o, "o", n_q, None), (d_out, "d_out", n_q, None), (lse, "lse", rows * 2, "float32"),
+                (seq_offsets, "seq_offsets", params.num_seqs + 1, "int32"), (dq, "dq", n_q, None),
+                (dk, "dk", n_kv, None), (dv, "dv", n_kv, None)),
+        _workspace(workspace, workspace_bytes, dev), int(workspace_bytes), ctypes.byref(params),
+        int(dtype), _stream_on(stream, dev))
     _check(rc, "mha_packed_backward")
 
 
 def mha_packed_forward_select_kernel(q, k, v, o, params: MhaPackedParams, dtype: int) -> int:
     """DGRAD_KERNEL_TC (1) or DGRAD_KERNEL_SIMT (2) for these buffers, or a negative status."""
-    t = _in_dtype(dtype)
+    dev, n = _device_of(q), params.tokens * params.num_heads * params.head_dim
     return int(library().mha_packed_forward_select_kernel(
-        *_packed_qkv(q, k, v, params, t), *_dense(t, (o, "o", params.tokens * params.num_heads * params.head_dim)),
+        *_packed_qkv(q, k, v, params, dtype, dev), *_dense(dtype, dev, (o, "o", n, None)),
         ctypes.byref(params), int(dtype)))
 
 
 def mha_packed_backward_select_kernel(q, k, v, o, d_out, dq, dk, dv, params: MhaPackedParams, dtype: int) -> int:
     """DGRAD_KERNEL_TC (1) or DGRAD_KERNEL_SIMT (2) for these buffers, or a negative status."""
-    t = _in_dtype(dtype)
+    dev = _device_of(q)
     n_q = params.tokens * params.num_heads * params.head_dim
     n_kv = params.tokens * params.num_kv_heads * params.head_dim
     return int(library().mha_packed_backward_select_kernel(
-        *_packed_qkv(q, k, v, params, t),
-        *_dense(t, (o, "o", n_q), (d_out, "d_out", n_q), (dq, "dq", n_q), (dk, "dk", n_kv), (dv, "dv", n_kv)),
+        *_packed_qkv(q, k, v, params, dtype, dev),
+        *_dense(dtype, dev, *((x, name, n, None) for x, name, n in (
+            (o, "o", n_q), (d_out, "d_out", n_q), (dq, "dq", n_q), (dk, "dk", n_kv), (dv, "dv", n_kv)))),
         ctypes.byref(params), int(dtype)))
 
 
@@ -501,12 +542,14 @@ def residual_rmsnorm_forward(f, x, gate, w_post, w_pre, h, y, rstd, params: Resi
                              stream=None) -> None:
     """H = X + scale * gate * RmsNorm(F, W_post) and Y = RmsNorm(H, W_pre) (include/residual_rmsnorm.h).
     ``gate`` is None for RESIDUAL_GATE_NONE; ``rstd`` may be None."""
-    t, m, n = _in_dtype(dtype), params.m, params.n
+    dev, m, n = _device_of(f), params.m, params.n
+    mn = m * n
     rc = library().residual_rmsnorm_forward(
-        *_dense(t, (f, "f", m * n), (x, "x", m * n),
-                (gate, "gate", n if params.gate_kind == RESIDUAL_GATE_CHANNEL else m * n), (w_post, "w_post", n),
-                (w_pre, "w_pre", n), (h, "h", m * n), (y, "y", m * n), (rstd, "rstd", 2 * m, "float32")),
-        ctypes.byref(params), int(dtype), _stream(stream))
+        *_dense(dtype, dev, (f, "f", mn, None), (x, "x", mn, None),
+                (gate, "gate", n if params.gate_kind == RESIDUAL_GATE_CHANNEL else mn, None),
+                (w_post, "w_post", n, None), (w_pre, "w_pre", n, None), (h, "h", mn, None), (y, "y", mn, None),
+                (rstd, "rstd", 2 * m, "float32")),
+        ctypes.byref(params), int(dtype), _stream_on(stream, dev))
     _check(rc, "residual_rmsnorm_forward")
 
 
@@ -518,14 +561,16 @@ def residual_rmsnorm_backward(f, h, gate, w_post, w_pre, rstd, dy, dh, df, dx, d
                               workspace_bytes: int, params: ResidualRmsnormParams, dtype: int, stream=None) -> None:
     """Gradients of residual_rmsnorm_forward (include/residual_rmsnorm.h).  ``dh`` may be None; ``gate`` and
     ``dgate`` are None for RESIDUAL_GATE_NONE."""
-    t, m, n = _in_dtype(dtype), params.m, params.n
+    dev, m, n = _device_of(f), params.m, params.n
     channel = params.gate_kind == RESIDUAL_GATE_CHANNEL
-    n_gate = n if channel else m * n
+    mn = m * n
+    n_gate = n if channel else mn
     rc = library().residual_rmsnorm_backward(
-        *_dense(t, (f, "f", m * n), (h, "h", m * n), (gate, "gate", n_gate), (w_post, "w_post", n),
-                (w_pre, "w_pre", n), (rstd, "rstd", 2 * m, "float32"), (dy, "dy", m * n), (dh, "dh", m * n),
-                (df, "df", m * n), (dx, "dx", m * n), (dgate, "dgate", n_gate, "float32" if channel else t),
-                (dw_post, "dw_post", n, "float32"), (dw_pre, "dw_pre", n, "float32")),
-        _addr(workspace, "workspace", min_bytes=int(workspace_bytes)), int(workspace_bytes), ctypes.byref(params),
-        int(dtype), _stream(stream))
+        *_dense(dtype, dev, (f, "f", mn, None), (h, "h", mn, None), (gate, "gate", n_gate, None),
+                (w_post, "w_post", n, None), (w_pre, "w_pre", n, None), (rstd, "rstd", 2 * m, "float32"),
+                (dy, "dy", mn, None), (dh, "dh", mn, None), (df, "df", mn, None), (dx, "dx", mn, None),
+                (dgate, "dgate", n_gate, "float32" if channel else None), (dw_post, "dw_post", n, "float32"),
+                (dw_pre, "dw_pre", n, "float32")),
+        _workspace(workspace, workspace_bytes, dev), int(workspace_bytes), ctypes.byref(params),
+        int(dtype), _stream_on(stream, dev))
     _check(rc, "residual_rmsnorm_backward")
