@@ -15,15 +15,17 @@
 //                                 tensor memory, X as the MN-major operand
 // so scores are formed twice (7 products in place of 5), and in return every gradient
 // is one block's sum in a fixed order: no atomics, nothing to zero or convert after.
-// Tensor memory: acc1 and acc2 (D columns each), and per step parity S and G (64
-// columns each, P and dS over their first halves).
-//   * warps 0-3 and 4-7: P and dS of the even and the odd steps, one resident row per
-//     thread; at the end dK / dQ and dV;
-//   * warp 8 (converged, lane 0 issuing): S and G of step j + 1, then acc of step j:
-//     one step's products run while the other parity's exponentials do;
-//   * warps 9 and 10 (one thread each): TMA copies of X1 and X2 (128 rows a copy, two
-//     steps) and of R1 and R2;
-//   * warp 11: with keys resident, the statistics of each step's 64 queries.
+// Tensor memory: acc1 and acc2 (D columns each), and a ring of two (D = 128) or three
+// buffers of S and G (64 columns each, P and dS over the first 16 of each 32).
+//   * warps 0-7 and 8-15: P and dS of the even and the odd steps, half a resident row
+//     (32 columns) per thread; at the end dK / dQ and dV;
+//   * warp 16 (converged, lane 0 issuing): S and G of each step, as far ahead as the ring
+//     has buffers; warp 17: acc of each step whose P and dS are written.  Two warps,
+//     because a warp's waits and commits (about 750 cycles a step) otherwise stand
+//     between its products;
+//   * warp 18 (one thread): TMA copies of X1 and X2 (128 rows a copy, two steps) and of R1
+//     and R2;
+//   * warp 19: with keys resident, the statistics of each step's 64 queries.
 // fp16 has 5 exponent bits: P is scaled by 2^13 (P <= 1) and dS by the power of two
 // that brings 2 max|dO| max|V| (row norms; |dP - delta| cannot be larger) to 2^15 at
 // most, both taken out of the sums at the end; the two maxima come from the first launch.
@@ -50,11 +52,10 @@ namespace {
 constexpr int kRows = 128;           // resident rows, rows of a streamed copy
 constexpr int kCols = 64;            // streamed rows of a step
 constexpr uint32_t kHalf = kRows * 128;
-constexpr int kSoftWarps = 8, kMmaWarp = 8, kLoadWarp = 9, kStatWarp = 11;
-constexpr int kThreads = 32 * 12;
+constexpr int kSoftWarps = 16, kMmaWarp = 16, kLoadWarp = 18, kStatWarp = 19;
+constexpr int kThreads = 32 * 20;
 constexpr int kStatSlots = 4;
 constexpr uint32_t kStatBytes = kCols * 8;
-constexpr uint32_t kColAcc1 = 0, kColAcc2 = 128, kColS = 256, kColG = 384;  // S, G: + 64 per parity
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kPShift = 13.0f;     // log2 of fp16's scale of P
 
@@ -63,6 +64,8 @@ struct Cfg {
     static constexpr int kHalves = D / 64;
     static constexpr uint32_t kTile = kHalf * kHalves;
     static constexpr int kStages = D == 64 ? 4 : 2;
+    static constexpr int kBufs = D == 64 ? 3 : 2;  // of S and G
+    static constexpr uint32_t kColAcc1 = 0, kColAcc2 = D, kColS = 2 * D, kColG = kColS + 64 * kBufs;  // + 64 per buffer
     static constexpr uint32_t kOffStat = 1024, kOffR = kOffStat + kStatSlots * kStatBytes + 1024;
     static constexpr uint32_t kOffX1 = kOffR + 2 * kTile, kOffX2 = kOffX1 + kStages * kTile;
     static constexpr uint32_t kSmem = 1024 + kOffX2 + kStages * kTile;  // + 1 KB alignment slack
@@ -80,7 +83,7 @@ struct BwdArgs {
 
 struct Ctl {
     uint64_t r_full, x_full[4], x_empty[4], st_full[kStatSlots], st_empty[kStatSlots];
-    uint64_t s_full[2], p_ready[2], acc_full, mma_done;
+    uint64_t s_full[3], g_full[3], p_ready[3], free[3], acc_full, mma_done[2];
     uint32_t tmem_base;
     int abort_flag, bad;
 };
@@ -197,27 +200,27 @@ __global__ void __launch_bounds__(256) stats_kernel(const Args a, unsigned *norm
 }
 
 // ----------------------------------------------------------- second launch
-// One loading thread: X1 and R1 (which 0) or X2 and R2 (which 1).
+// The loading thread: R1 and R2, then X1 and X2 of every ring slot.
 template <int D, bool KEYS>
 __device__ void role_load(const BwdArgs &p, Ctl &c, uint32_t smem, const Unit &u, const Walk &k, int head, int g,
-                          int which, const Waiter &w) {
+                          const Waiter &w) {
     using C = Cfg<D>;
-    const CUtensorMap *res = KEYS ? (which ? &p.v_map : &p.k_map) : (which ? &p.go_map : &p.q_map);
-    const CUtensorMap *str = KEYS ? (which ? &p.go_map : &p.q_map) : (which ? &p.v_map : &p.k_map);
-    const uint32_t ring = smem + (which ? C::kOffX2 : C::kOffX1);
-    load_rows<D>(smem + C::kOffR + (uint32_t)which * C::kTile, res, p.a.hd, head, u.begin + u.p0, kRows, su32(&c.r_full));
+    const CUtensorMap *r1 = KEYS ? &p.k_map : &p.q_map, *r2 = KEYS ? &p.v_map : &p.go_map;
+    const CUtensorMap *x1 = KEYS ? &p.q_map : &p.k_map, *x2 = KEYS ? &p.go_map : &p.v_map;
+    load_rows<D>(smem + C::kOffR, r1, p.a.hd, head, u.begin + u.p0, kRows, su32(&c.r_full));
+    load_rows<D>(smem + C::kOffR + C::kTile, r2, p.a.hd, head, u.begin + u.p0, kRows, su32(&c.r_full));
     const int n = k.copies();
     int it = 0;
     bool ok = true;
     for (int b = 0; b < n && ok; ++b)
         for (int r = 0; r < k.heads; ++r, ++it) {
-            const int s = it % C::kStages;
+            const int s = it % C::kStages, h = KEYS ? g * p.a.hpk + r : g, row = u.begin + k.lo + kRows * b;
             if (!wait(su32(&c.x_empty[s]), (uint32_t)(((it / C::kStages) & 1) ^ 1), w)) {
                 ok = false;
                 break;
             }
-            load_rows<D>(ring + (uint32_t)s * C::kTile, str, p.a.hd, KEYS ? g * p.a.hpk + r : g,
-                         u.begin + k.lo + kRows * b, kRows, su32(&c.x_full[s]));
+            load_rows<D>(smem + C::kOffX1 + (uint32_t)s * C::kTile, x1, p.a.hd, h, row, kRows, su32(&c.x_full[s]));
+            load_rows<D>(smem + C::kOffX2 + (uint32_t)s * C::kTile, x2, p.a.hd, h, row, kRows, su32(&c.x_full[s]));
         }
     // Copies still landing must finish before the block exits.
     drain(su32(&c.r_full), 0, w);
@@ -249,71 +252,85 @@ __device__ void role_stats(const BwdArgs &p, Ctl &c, uint32_t smem, const Unit &
         }
 }
 
+// The ring walk of one product warp: visit(slot, half, step, first use of the slot, last use, first row of the copy)
+// for every step, until it returns false.
+template <int STAGES, typename F>
+__device__ __forceinline__ bool for_steps(const Walk &k, F visit) {
+    const int n = k.copies();
+    int it = 0, step = 0;
+    for (int b = 0; b < n; ++b)
+        for (int r = 0; r < k.heads; ++r, ++it) {
+            const int c0 = k.lo + kRows * b, ns = k.steps(c0);
+            for (int s = 0; s < ns; ++s, ++step)
+                if (!visit(it % STAGES, (uint32_t)((it / STAGES) & 1), s, step, s == 0, s == ns - 1, c0)) return false;
+        }
+    return true;
+}
+
+// S and G of every step, into the next buffer once the sums have read what it held.
 template <int D, bool KEYS>
-__device__ __forceinline__ void issue_products(const BwdArgs &p, Ctl &c, uint32_t smem, uint32_t tmem, const Unit &u,
-                                               const Walk &k, int lane, const Waiter &w) {
+__device__ __forceinline__ void issue_scores(const BwdArgs &p, Ctl &c, uint32_t smem, uint32_t tmem, int seq_end,
+                                             const Walk &k, int lane, const Waiter &w) {
     using C = Cfg<D>;
     const uint32_t leader = lane == 0;
     const uint64_t r1 = desc_k(smem + C::kOffR), r2 = desc_k(smem + C::kOffR + C::kTile);
     if (!wait_warp(su32(&c.r_full), 0, w)) return;
-    // S and G of one step: streamed rows 64 s .. of ring slot `slot`.
-    auto scores = [&](int slot, int s, int par) {
+    for_steps<C::kStages>(k, [&](int slot, uint32_t phase, int s, int step, bool fresh, bool, int c0) {
+        const int buf = step % C::kBufs;
+        if (fresh) {
+            if (!wait_warp(su32(&c.x_full[slot]), phase, w)) return false;
+            if (seq_end - c0 < kRows) {
+                zero_rows(smem + C::kOffX1 + (uint32_t)slot * C::kTile, seq_end - c0, kRows, C::kHalves, lane);
+                if (KEYS) zero_rows(smem + C::kOffX2 + (uint32_t)slot * C::kTile, seq_end - c0, kRows, C::kHalves, lane);
+            }
+        }
+        if (!wait_warp(su32(&c.free[buf]), (uint32_t)(((step / C::kBufs) & 1) ^ 1), w)) return false;
         tc_after();
         const uint32_t at = (uint32_t)slot * C::kTile + (uint32_t)s * (kCols * 128u);
         const uint64_t x1 = desc_k(smem + C::kOffX1 + at), x2 = desc_k(smem + C::kOffX2 + at);
 #pragma unroll
         for (int i = 0; i < D / 16; ++i) {
-            const uint64_t step = 2u * (i % 4) + (uint64_t)(i / 4) * (kHalf >> 4);
-            tc_mma_f16_if(tmem + kColS + 64u * par, r1 + step, x1 + step, p.idesc1, i > 0, leader);
+            const uint64_t off = 2u * (i % 4) + (uint64_t)(i / 4) * (kHalf >> 4);
+            tc_mma_f16_if(tmem + C::kColS + 64u * buf, r1 + off, x1 + off, p.idesc1, i > 0, leader);
         }
+        tc_commit_to_if(su32(&c.s_full[buf]), leader);
 #pragma unroll
         for (int i = 0; i < D / 16; ++i) {
-            const uint64_t step = 2u * (i % 4) + (uint64_t)(i / 4) * (kHalf >> 4);
-            tc_mma_f16_if(tmem + kColG + 64u * par, r2 + step, x2 + step, p.idesc1, i > 0, leader);
+            const uint64_t off = 2u * (i % 4) + (uint64_t)(i / 4) * (kHalf >> 4);
+            tc_mma_f16_if(tmem + C::kColG + 64u * buf, r2 + off, x2 + off, p.idesc1, i > 0, leader);
         }
-        tc_commit_to_if(su32(&c.s_full[par]), leader);
-    };
-    auto sums = [&](int slot, int s, int step) {
-        const int par = step & 1;
-        if (!wait_warp(su32(&c.p_ready[par]), (uint32_t)((step >> 1) & 1), w)) return false;
+        tc_commit_to_if(su32(&c.g_full[buf]), leader);
+        return true;
+    });
+}
+
+// acc1 += dS X1 and acc2 += P X2 of every step.
+template <int D, bool KEYS>
+__device__ __forceinline__ void issue_sums(const BwdArgs &p, Ctl &c, uint32_t smem, uint32_t tmem, const Walk &k,
+                                           int lane, const Waiter &w) {
+    using C = Cfg<D>;
+    const uint32_t leader = lane == 0;
+    const bool done = for_steps<C::kStages>(k, [&](int slot, uint32_t, int s, int step, bool, bool last, int) {
+        const int buf = step % C::kBufs;
+        if (!wait_warp(su32(&c.p_ready[buf]), (uint32_t)((step / C::kBufs) & 1), w)) return false;
         tc_after();
         const uint32_t at = (uint32_t)slot * C::kTile + (uint32_t)s * (kCols * 128u);
         const uint64_t x1 = desc_mn(smem + C::kOffX1 + at, kHalf, 1024u), x2 = desc_mn(smem + C::kOffX2 + at, kHalf, 1024u);
         if (KEYS) {
 #pragma unroll
             for (int i = 0; i < kCols / 16; ++i)
-                tc_mma_f16_ts_if(tmem + kColAcc2, tmem + kColS + 64u * par + 8u * i, x2 + 128u * i, p.idesc2,
-                                 step > 0 || i > 0, leader);
+                tc_mma_f16_ts_if(tmem + C::kColAcc2, tmem + C::kColS + 64u * buf + 32u * (i / 2) + 8u * (i % 2),
+                                 x2 + 128u * i, p.idesc2, step > 0 || i > 0, leader);
         }
 #pragma unroll
         for (int i = 0; i < kCols / 16; ++i)
-            tc_mma_f16_ts_if(tmem + kColAcc1, tmem + kColG + 64u * par + 8u * i, x1 + 128u * i, p.idesc2,
-                             step > 0 || i > 0, leader);
+            tc_mma_f16_ts_if(tmem + C::kColAcc1, tmem + C::kColG + 64u * buf + 32u * (i / 2) + 8u * (i % 2),
+                             x1 + 128u * i, p.idesc2, step > 0 || i > 0, leader);
+        tc_commit_to_if(su32(&c.free[buf]), leader);
+        if (last) tc_commit_to_if(su32(&c.x_empty[slot]), leader);
         return true;
-    };
-    const int n = k.copies();
-    int it = 0, step = 0;
-    int old_slot = 0, old_s = 0;
-    bool old_last = false;
-    for (int b = 0; b < n; ++b)
-        for (int r = 0; r < k.heads; ++r, ++it) {
-            const int c0 = k.lo + kRows * b, ns = k.steps(c0), slot = it % C::kStages;
-            if (!wait_warp(su32(&c.x_full[slot]), (uint32_t)((it / C::kStages) & 1), w)) return;
-            if (u.len - c0 < kRows) {
-                zero_rows(smem + C::kOffX1 + (uint32_t)slot * C::kTile, u.len - c0, kRows, C::kHalves, lane);
-                if (KEYS) zero_rows(smem + C::kOffX2 + (uint32_t)slot * C::kTile, u.len - c0, kRows, C::kHalves, lane);
-            }
-            for (int s = 0; s < ns; ++s, ++step) {
-                scores(slot, s, step & 1);
-                if (step > 0) {
-                    if (!sums(old_slot, old_s, step - 1)) return;
-                    if (old_last) tc_commit_to_if(su32(&c.x_empty[old_slot]), leader);
-                }
-                old_slot = slot, old_s = s, old_last = s == ns - 1;
-            }
-        }
-    if (!sums(old_slot, old_s, step - 1)) return;
-    tc_commit_to_if(su32(&c.acc_full), leader);
+    });
+    if (done) tc_commit_to_if(su32(&c.acc_full), leader);
 }
 
 // P and dS of 32 columns.  s, g: this row's scores and dP; columns outside [from, to] are masked when MASK.  With
@@ -344,15 +361,16 @@ __device__ __forceinline__ void grad32(const uint32_t (&s)[32], const uint32_t (
     }
 }
 
-// D columns of 32 rows from tensor memory, times `factor`, through this warp's staging rows to dst (a row every
-// `stride` elements).  Returns whether this lane's row is finite.
-template <int D, bool F16>
+// W columns of 32 rows from tensor memory, times `factor`, through this warp's staging rows to dst (a row every
+// `stride` elements; `cols` of the columns exist).  Returns whether this lane's row is finite.
+template <int W, bool F16>
 __device__ __forceinline__ bool store_acc(uint32_t acc_tm, uint32_t stage, float factor, uint16_t *dst, int64_t stride,
-                                          int live, int hd, int lane) {
-    constexpr int kChunks = D / 8;
+                                          int live, int cols, int lane) {
+    constexpr int kChunks = W / 8;  // 16-byte chunk j of row r lies at j ^ (r & 7), of 64-byte rows at j ^ (r / 2 & 3)
+    auto place = [](int r, int j) { return (uint32_t)((kChunks == 4 ? j ^ ((r >> 1) & 3) : j ^ (r & 7)) << 4); };
     bool good = true;
 #pragma unroll
-    for (int k = 0; k < D / 32; ++k) {
+    for (int k = 0; k < W / 32; ++k) {
         uint32_t o[32];
         tc_ld_32x32(acc_tm + 32 * k, o);
         tc_wait_ld(o);
@@ -364,15 +382,15 @@ __device__ __forceinline__ bool store_acc(uint32_t acc_tm, uint32_t stage, float
         }
 #pragma unroll
         for (int j = 0; j < 4; ++j)
-            sts128(stage + (uint32_t)lane * (2 * D) + (uint32_t)(((4 * k + j) ^ (lane & 7)) << 4),
-                   pack2<F16>(x[8 * j], x[8 * j + 1]), pack2<F16>(x[8 * j + 2], x[8 * j + 3]),
-                   pack2<F16>(x[8 * j + 4], x[8 * j + 5]), pack2<F16>(x[8 * j + 6], x[8 * j + 7]));
+            sts128(stage + (uint32_t)lane * (2 * W) + place(lane, 4 * k + j), pack2<F16>(x[8 * j], x[8 * j + 1]),
+                   pack2<F16>(x[8 * j + 2], x[8 * j + 3]), pack2<F16>(x[8 * j + 4], x[8 * j + 5]),
+                   pack2<F16>(x[8 * j + 6], x[8 * j + 7]));
     }
     __syncwarp();
     const int j = lane % kChunks;
     for (int r = lane / kChunks; r < 32; r += 32 / kChunks) {
-        if (r >= live || 8 * j >= hd) continue;
-        const uint4 x = lds128(stage + (uint32_t)r * (2 * D) + (uint32_t)((j ^ (r & 7)) << 4));
+        if (r >= live || 8 * j >= cols) continue;
+        const uint4 x = lds128(stage + (uint32_t)r * (2 * W) + place(r, j));
         *reinterpret_cast<uint4 *>(dst + (int64_t)r * stride + 8 * j) = x;
     }
     return good;
@@ -383,9 +401,8 @@ __device__ void role_soft(const BwdArgs &p, Ctl &c, uint32_t smem, uint32_t tmem
                           int head, float sigma, int warp, int lane, const Waiter &w) {
     using C = Cfg<D>;
     const Args &a = p.a;
-    const int quad = warp & 3, grp = warp >> 2, row = u.p0 + 32 * quad + lane;
+    const int quad = warp & 3, part = (warp >> 2) & 1, grp = warp >> 3, row = u.p0 + 32 * quad + lane;
     const uint32_t lane_tm = (uint32_t)(32 * quad) << 16;
-    const uint32_t s_tm = tmem + lane_tm + kColS + 64u * grp, g_tm = tmem + lane_tm + kColG + 64u * grp;
     const float cs = a.scale * kLog2e, kappa = F16 ? sigma * 0x1p-13f : 1.f;
     float nl = 0.f, nd = 0.f;
     if (!KEYS && row < u.len) {
@@ -399,7 +416,9 @@ __device__ void role_soft(const BwdArgs &p, Ctl &c, uint32_t smem, uint32_t tmem
         for (int r = 0; r < k.heads; ++r)
             for (int s = 0; s < ns; ++s, ++step) {
                 if ((step & 1) != grp) continue;
-                const int base = c0 + kCols * s, slot = step % kStatSlots;
+                const int base = c0 + kCols * s + 32 * part, slot = step % kStatSlots, buf = step % C::kBufs;
+                const uint32_t phase = (uint32_t)((step / C::kBufs) & 1);
+                const uint32_t s_tm = tmem + lane_tm + C::kColS + 64u * buf, g_tm = tmem + lane_tm + C::kColG + 64u * buf;
                 int from, to;
                 bool whole;
                 if (KEYS) {
@@ -407,51 +426,54 @@ __device__ void role_soft(const BwdArgs &p, Ctl &c, uint32_t smem, uint32_t tmem
                     int end = u.len;
                     if (a.window > 0 && row < u.len - a.window) end = row + a.window;
                     to = end - 1 - base;
-                    whole = base >= u.p0 + kRows - 1 && base + kCols <= u.len &&
-                            (a.window == 0 || base + kCols - 1 < u.p0 + a.window);
+                    whole = base >= u.p0 + kRows - 1 && base + 32 <= u.len &&
+                            (a.window == 0 || base + 31 < u.p0 + a.window);
                     if (!wait_warp(su32(&c.st_full[slot]), (uint32_t)((step / kStatSlots) & 1), w)) return;
                 } else {
                     from = a.window > 0 ? row - a.window + 1 - base : 0;
                     to = row - base;
-                    whole = base + kCols - 1 <= u.p0 && (a.window == 0 || u.p0 + kRows - 1 < base + a.window);
+                    whole = base + 31 <= u.p0 && (a.window == 0 || u.p0 + kRows - 1 < base + a.window);
                 }
-                if (!wait_warp(su32(&c.s_full[grp]), (uint32_t)((step >> 1) & 1), w)) return;
+                uint32_t sv[32], gv[32], pp[16], pd[16];
+                if (!wait_warp(su32(&c.s_full[buf]), phase, w)) return;
                 tc_after();
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    uint32_t sv[32], gv[32], pp[16], pd[16];
-                    tc_ld_32x32(s_tm + 32 * h, sv);
-                    tc_ld_32x32(g_tm + 32 * h, gv);
-                    tc_wait_ld(sv);
-                    tc_wait_ld(gv);
-                    const uint32_t st = smem + 1024u + (uint32_t)slot * kStatBytes + 256u * h;
-                    if (whole)
-                        grad32<F16, KEYS, false>(sv, gv, cs, kappa, st, nl, nd, 0, 0, pp, pd);
-                    else
-                        grad32<F16, KEYS, true>(sv, gv, cs, kappa, st, nl, nd, from - 32 * h, to - 32 * h, pp, pd);
-                    if (KEYS) tc_st_32x16(s_tm + 16 * h, pp);
-                    tc_st_32x16(g_tm + 16 * h, pd);
-                }
+                tc_ld_32x32(s_tm + 32 * part, sv);
+                if (!wait_warp(su32(&c.g_full[buf]), phase, w)) return;
+                tc_after();
+                tc_ld_32x32(g_tm + 32 * part, gv);
+                tc_wait_ld(sv);
+                tc_wait_ld(gv);
+                // The warp of the other 32 columns may still read its half of S and G: P and dS (16 columns) go over
+                // this warp's own half.
+                const uint32_t st = smem + 1024u + (uint32_t)slot * kStatBytes + 256u * part;
+                if (whole)
+                    grad32<F16, KEYS, false>(sv, gv, cs, kappa, st, nl, nd, 0, 0, pp, pd);
+                else
+                    grad32<F16, KEYS, true>(sv, gv, cs, kappa, st, nl, nd, from, to, pp, pd);
+                if (KEYS) tc_st_32x16(s_tm + 32 * part, pp);
+                tc_st_32x16(g_tm + 32 * part, pd);
                 tc_wait_st();
                 tc_before();
                 __syncwarp();
                 if (lane == 0) {
-                    bar_arrive(su32(&c.p_ready[grp]));
+                    bar_arrive(su32(&c.p_ready[buf]));
                     if (KEYS) bar_arrive(su32(&c.st_empty[slot]));
                 }
             }
     }
     if (!wait_warp(su32(&c.acc_full), 0, w)) return;
     tc_after();
-    // The resident tiles are read by now: group 0 stages dK or dQ in R1, group 1 dV in R2.
+    // The resident tiles are read by now: group 0 stages dK or dQ in R1, group 1 dV in R2, half of the columns a warp.
     if (!KEYS && grp == 1) return;
+    constexpr int W = D / 2;
     const int heads = KEYS ? a.nkv : a.nh;
-    const int64_t stride = (int64_t)heads * a.hd, at = (((int64_t)u.begin + u.p0 + 32 * quad) * heads + head) * a.hd;
+    const int64_t stride = (int64_t)heads * a.hd;
+    const int64_t at = (((int64_t)u.begin + u.p0 + 32 * quad) * heads + head) * a.hd + W * part;
     const float factor = grp == 0 ? a.scale / sigma : (F16 ? 0x1p-13f : 1.f);
     uint16_t *dst = static_cast<uint16_t *>(grp == 0 ? (KEYS ? a.dk : a.dq) : a.dv) + at;
-    const uint32_t stage = smem + C::kOffR + (uint32_t)grp * C::kTile + (uint32_t)quad * (C::kTile / 4);
-    const bool good = store_acc<D, F16>(tmem + lane_tm + (grp == 0 ? kColAcc1 : kColAcc2), stage, factor, dst, stride,
-                                        live - 32 * quad, a.hd, lane);
+    const uint32_t stage = smem + C::kOffR + (uint32_t)grp * C::kTile + (uint32_t)(warp & 7) * (C::kTile / 8);
+    const bool good = store_acc<W, F16>(tmem + lane_tm + (grp == 0 ? C::kColAcc1 : C::kColAcc2) + W * part, stage, factor,
+                                        dst, stride, live - 32 * quad, a.hd - W * part, lane);
     if (__any_sync(0xffffffffu, row < u.len && !good) && lane == 0) c.bad = 1;
 }
 
@@ -517,7 +539,7 @@ __device__ __forceinline__ void unit_body(const BwdArgs &p, Ctl &c, uint32_t sme
     using C = Cfg<D>;
     const unsigned heads = KEYS ? p.a.nkv : p.a.nh;
     const int head = (int)(index % heads), g = KEYS ? head : head / p.a.hpk;
-    const Unit u = find_unit(p.a, index / heads, kRows, check, &g_bwd_error_word);
+    const Unit u = find_unit(p.a, index / heads, kRows, !KEYS, check, &g_bwd_error_word);
     if (!u.live) return;
     const int live = u.len - u.p0 < kRows ? u.len - u.p0 : kRows;
     if (u.pad) {
@@ -535,13 +557,19 @@ __device__ __forceinline__ void unit_body(const BwdArgs &p, Ctl &c, uint32_t sme
     const float sigma = ds_scale<F16>(p);
     if (warp < kSoftWarps) {
         role_soft<D, F16, KEYS>(p, c, smem, tmem, u, k, live, head, sigma, warp, lane, w);
-    } else if (warp == kMmaWarp) {
-        issue_products<D, KEYS>(p, c, smem, tmem, u, k, lane, w);
-        tc_commit_to_if(su32(&c.mma_done), lane == 0);  // nothing may still run when tensor memory is released
-        drain(su32(&c.mma_done), 0, w);
+    } else if (warp == kMmaWarp || warp == kMmaWarp + 1) {
+        const int second = warp - kMmaWarp;
+        const uint32_t sm = uniform(smem), tm = uniform(tmem);
+        const Walk ku{uniform(k.lo), uniform(k.hi), uniform(k.heads)};
+        if (second)
+            issue_sums<D, KEYS>(p, c, sm, tm, ku, lane, w);
+        else
+            issue_scores<D, KEYS>(p, c, sm, tm, uniform(u.len), ku, lane, w);
+        tc_commit_to_if(su32(&c.mma_done[second]), lane == 0);  // nothing may still run when tensor memory is released
+        drain(su32(&c.mma_done[second]), 0, w);
         __syncwarp();
     } else if (warp < kStatWarp) {
-        if (lane == 0) role_load<D, KEYS>(p, c, smem, u, k, head, g, warp - kLoadWarp, w);
+        if (lane == 0) role_load<D, KEYS>(p, c, smem, u, k, head, g, w);
         __syncwarp();
     } else if (KEYS) {
         role_stats<F16>(p, c, smem, u, k, g, F16 ? sigma * 0x1p-13f : 1.f, lane, w);
@@ -558,7 +586,7 @@ __global__ void __launch_bounds__(kThreads, 1) backward_tc_kernel(const __grid_c
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     const uint32_t smem = (su32(smem_raw) + 1023u) & ~1023u;
     Ctl &c = *reinterpret_cast<Ctl *>(smem_raw + (smem - su32(smem_raw)));
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = uniform((int)(threadIdx.x >> 5)), lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
         bar_init(su32(&c.r_full), 2);
         for (int s = 0; s < 4; ++s) {
@@ -567,14 +595,17 @@ __global__ void __launch_bounds__(kThreads, 1) backward_tc_kernel(const __grid_c
         }
         for (int s = 0; s < kStatSlots; ++s) {
             bar_init(su32(&c.st_full[s]), 1);
-            bar_init(su32(&c.st_empty[s]), 4);
+            bar_init(su32(&c.st_empty[s]), 8);
         }
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < 3; ++i) {
             bar_init(su32(&c.s_full[i]), 1);
-            bar_init(su32(&c.p_ready[i]), 4);
+            bar_init(su32(&c.g_full[i]), 1);
+            bar_init(su32(&c.p_ready[i]), 8);
+            bar_init(su32(&c.free[i]), 1);
         }
         bar_init(su32(&c.acc_full), 1);
-        bar_init(su32(&c.mma_done), 1);
+        bar_init(su32(&c.mma_done[0]), 1);
+        bar_init(su32(&c.mma_done[1]), 1);
         c.abort_flag = 0;
         c.bad = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");

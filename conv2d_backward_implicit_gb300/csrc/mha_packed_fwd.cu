@@ -119,10 +119,12 @@ __device__ void role_load(const FwdArgs &p, Ctl &c, uint32_t smem, const Unit &u
 
 // All products of the unit; returns early when aborting.
 template <int D>
-__device__ __forceinline__ void issue_products(const FwdArgs &p, Ctl &c, uint32_t smem, uint32_t tmem, const Unit &u,
-                                               const Tile (&t)[2], int lo, int hi, int lane, const Waiter &w) {
+__device__ __forceinline__ void issue_products(const FwdArgs &p, Ctl &c, uint32_t smem_, uint32_t tmem_, int len,
+                                               const Tile (&t)[2], int lo_, int hi_, int lane, const Waiter &w) {
     using C = Cfg<D>;
-    const uint32_t leader = lane == 0;
+    const uint32_t leader = lane == 0, smem = uniform(smem_), tmem = uniform(tmem_);
+    const int lo = uniform(lo_), hi = uniform(hi_), seq_end = uniform(len);
+    const int first[2] = {uniform(t[0].lo), uniform(t[1].lo)}, end[2] = {uniform(t[0].hi), uniform(t[1].hi)};
     int phase[2] = {0, 0};  // products PV issued of each tile
     bool q_seen[2] = {false, false};
     int it = 0;
@@ -133,13 +135,13 @@ __device__ __forceinline__ void issue_products(const FwdArgs &p, Ctl &c, uint32_
         if (more && !wait_warp(su32(&c.k_full[ks]), (uint32_t)((it / C::kStages) & 1), w)) return;
         if (prev) {
             if (!wait_warp(su32(&c.v_full[vs]), (uint32_t)(((it - 1) / C::kStages) & 1), w)) return;
-            const int keys = u.len - kRows * (b + 1);
+            const int keys = seq_end - kRows * (b + 1);
             if (keys < kRows) zero_rows(smem + C::kOffV + (uint32_t)vs * C::kTile, keys, kRows, C::kHalves, lane);
         }
         tc_after();
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-            if (prev && b + 1 >= t[i].lo && b + 1 < t[i].hi) {
+            if (prev && b + 1 >= first[i] && b + 1 < end[i]) {
                 if (!wait_warp(su32(&c.p_ready[i]), (uint32_t)(phase[i] & 1), w)) return;
                 tc_after();
                 const uint64_t vd = desc_mn(smem + C::kOffV + (uint32_t)vs * C::kTile, kHalf, 1024u);
@@ -148,9 +150,9 @@ __device__ __forceinline__ void issue_products(const FwdArgs &p, Ctl &c, uint32_
                     tc_mma_f16_ts_if(tmem + kColO + 128u * i, tmem + kColS + 128u * i + 8u * k, vd + 128u * k, p.idesc2,
                                      phase[i] > 0 || k > 0, leader);
                 ++phase[i];
-                if (b + 1 == t[i].lo) tc_commit_to_if(su32(&c.o_full[i]), leader);
+                if (b + 1 == first[i]) tc_commit_to_if(su32(&c.o_full[i]), leader);
             }
-            if (more && b >= t[i].lo && b < t[i].hi) {
+            if (more && b >= first[i] && b < end[i]) {
                 if (!q_seen[i] && !wait_warp(su32(&c.q_full[i]), 0, w)) return;
                 q_seen[i] = true;
                 const uint64_t qd = desc_k(smem + C::kOffQ + (uint32_t)i * C::kTile);
@@ -171,7 +173,7 @@ __device__ __forceinline__ void issue_products(const FwdArgs &p, Ctl &c, uint32_
 template <int D>
 __device__ void role_mma(const FwdArgs &p, Ctl &c, uint32_t smem, uint32_t tmem, const Unit &u, const Tile (&t)[2],
                          int lo, int hi, int lane, const Waiter &w) {
-    issue_products<D>(p, c, smem, tmem, u, t, lo, hi, lane, w);
+    issue_products<D>(p, c, smem, tmem, u.len, t, lo, hi, lane, w);
     tc_commit_to_if(su32(&c.mma_done), lane == 0);  // nothing may still run when tensor memory is released
     drain(su32(&c.mma_done), 0, w);
     __syncwarp();
@@ -368,7 +370,7 @@ __global__ void __launch_bounds__(kThreads, 1) forward_tc_kernel(const __grid_co
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     const uint32_t smem = (su32(smem_raw) + 1023u) & ~1023u;
     Ctl &c = *reinterpret_cast<Ctl *>(smem_raw + (smem - su32(smem_raw)));
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = uniform((int)(threadIdx.x >> 5)), lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
         for (int s = 0; s < 4; ++s) {
             bar_init(su32(&c.k_full[s]), 1);
@@ -397,8 +399,8 @@ __global__ void __launch_bounds__(kThreads, 1) forward_tc_kernel(const __grid_co
 
     const unsigned pairs = p.pair_heads ? p.a.nh / 2 : p.a.nh;
     const int pair = (int)(blockIdx.x % pairs);
-    const Unit u = find_unit(p.a, blockIdx.x / pairs, p.pair_heads ? kRows : 2 * kRows, blockIdx.x == 0,
-                             &g_fwd_error_word);
+    const Unit u = find_unit(p.a, blockIdx.x / pairs, p.pair_heads ? kRows : 2 * kRows, true,
+                             blockIdx.x == 0, &g_fwd_error_word);
     const Waiter w{&c.abort_flag, &g_fwd_error_word};
     if (u.live) {
         const Tile t[2] = {tile_of(p, u, pair, 0), tile_of(p, u, pair, 1)};

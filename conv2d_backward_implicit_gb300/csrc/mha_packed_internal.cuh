@@ -65,11 +65,12 @@ __device__ __forceinline__ void segment(const Args &a, int i, int &begin, int &l
 
 // Tile `u` of `rows` rows, every thread of the block calling (blockDim.x a
 // multiple of 32, at most 1024).  Segments are numbered as above, the tiles of one
-// in descending order, so that under the causal mask the tiles with the most keys
-// come first.  Each thread adds up the tiles of a run of segments, the block scans
+// in descending order when `down` (queries: those with the most keys come first),
+// else ascending (keys: those with the most queries).  Each thread adds up the tiles of a run of segments, the block scans
 // those sums, and the thread whose run holds `u` walks it: two rounds of loads for
 // any number of sequences.  `check`: raise the error flag where offsets are malformed.
-__device__ __forceinline__ Unit find_unit(const Args &a, int64_t u, int rows, bool check, unsigned *error) {
+__device__ __forceinline__ Unit find_unit(const Args &a, int64_t u, int rows, bool down, bool check,
+                                          unsigned *error) {
     __shared__ int64_t warp_sum[32];
     __shared__ Unit found;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, n = a.seqs + 2;
@@ -104,7 +105,7 @@ __device__ __forceinline__ Unit find_unit(const Args &a, int64_t u, int rows, bo
             if (u < at + tiles) {
                 found.begin = begin;
                 found.len = len;
-                found.p0 = (tiles - 1 - (int)(u - at)) * rows;
+                found.p0 = (down ? tiles - 1 - (int)(u - at) : (int)(u - at)) * rows;
                 found.pad = i >= a.seqs;
                 found.live = true;
                 break;

@@ -77,6 +77,13 @@ __device__ __forceinline__ uint32_t pack2(float a, float b) {
     }
 }
 
+// The same value in every lane, and known to be: what depends on it stays in the warp's uniform registers, from which
+// the tensor-core instructions take their descriptors and addresses.
+template <typename T>
+__device__ __forceinline__ T uniform(T x) {
+    return __shfl_sync(0xffffffffu, x, 0);
+}
+
 __device__ __forceinline__ bool finite(float x) { return fabsf(x) <= 3.402823466e38f; }
 
 // Zero rows [from, rows) of a [rows][D] tile held as D / 64 halves of 128-byte rows: one warp, before the tensor core
