@@ -8,24 +8,27 @@
 //   keys resident (R1 = K, R2 = V; streamed X1 = Q, X2 = dO, over the query blocks that
 //   reach them and the heads of the group):  dK = acc1, dV = acc2;
 //   queries resident (R1 = Q, R2 = dO; streamed X1 = K, X2 = V):  dQ = acc1.
-// For every step of 64 streamed rows (columns below):
-//   S = R1 X1^T, G = R2 X2^T      tcgen05 M128 N64 K16, D / 16 steps each
+// For every step of 128 streamed rows (columns below):
+//   S = R1 X1^T, G = R2 X2^T      tcgen05 M128 N128 K16, D / 16 steps each
 //   P = 2^(S c - stat), dS = P (G - delta), masked, rounded to 16 bits
-//   acc1 += dS X1, acc2 += P X2   tcgen05 M128 N(D) K16, 4 steps each, P and dS from
+//   acc1 += dS X1, acc2 += P X2   tcgen05 M128 N(D) K16, 8 steps each, P and dS from
 //                                 tensor memory, X as the MN-major operand
 // so scores are formed twice (7 products in place of 5), and in return every gradient
 // is one block's sum in a fixed order: no atomics, nothing to zero or convert after.
-// Tensor memory: acc1 and acc2 (D columns each), and a ring of two (D = 128) or three
-// buffers of S and G (64 columns each, P and dS over the first 16 of each 32).
-//   * warps 0-7 and 8-15: P and dS of the even and the odd steps, half a resident row
-//     (32 columns) per thread; at the end dK / dQ and dV;
-//   * warp 16 (converged, lane 0 issuing): S and G of each step, as far ahead as the ring
-//     has buffers; warp 17: acc of each step whose P and dS are written.  Two warps,
-//     because a warp's waits and commits (about 750 cycles a step) otherwise stand
-//     between its products;
-//   * warp 18 (one thread): TMA copies of X1 and X2 (128 rows a copy, two steps) and of R1
-//     and R2;
-//   * warp 19: with keys resident, the statistics of each step's 64 queries.
+// Tensor memory: acc1 and acc2 (D columns each), one buffer of S (two at D = 64) and one
+// of G, 128 columns each, with P and dS over the first 16 of each 32.  Steps of 128
+// columns because a product of N = 64 takes nearly as long as one of N = 128 (65 against
+// 75 cycles); what overlaps is then not two steps but the two halves of one: while P of a
+// step goes through acc2 and the next S, its dS is formed, and while dS goes through
+// acc1 and the next G, the next P is.
+//   * warps 0-15: P, then dS, 32 columns of one resident row per thread; at the end dK /
+//     dQ (warps 0-7) and dV (8-15);
+//   * warp 16 (converged, lane 0 issuing): acc2 of a step, then S of a later one; warp 17:
+//     acc1 of a step, then G of the next.  A warp's products run in order, so the scores
+//     may follow the product that reads what they overwrite without a wait; two warps,
+//     because a warp's waits and commits otherwise stand between its products;
+//   * warp 18 (one thread): TMA copies of X1, X2, R1 and R2;
+//   * warp 19: with keys resident, the statistics of each step's 128 queries.
 // fp16 has 5 exponent bits: P is scaled by 2^13 (P <= 1) and dS by the power of two
 // that brings 2 max|dO| max|V| (row norms; |dP - delta| cannot be larger) to 2^15 at
 // most, both taken out of the sums at the end; the two maxima come from the first launch.
@@ -49,13 +52,12 @@ unsigned take_bwd_error(cudaError_t &e) {
 
 namespace {
 
-constexpr int kRows = 128;           // resident rows, rows of a streamed copy
-constexpr int kCols = 64;            // streamed rows of a step
+constexpr int kRows = 128;           // resident rows, streamed rows of a step
 constexpr uint32_t kHalf = kRows * 128;
-constexpr int kSoftWarps = 16, kMmaWarp = 16, kLoadWarp = 18, kStatWarp = 19;
+constexpr int kSoftWarps = 16, kMmaWarp = 16, kStatWarp = 19;  // 18: the loads
 constexpr int kThreads = 32 * 20;
-constexpr int kStatSlots = 4;
-constexpr uint32_t kStatBytes = kCols * 8;
+constexpr int kStatSlots = 2;
+constexpr uint32_t kStatBytes = kRows * 8;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kPShift = 13.0f;     // log2 of fp16's scale of P
 
@@ -63,13 +65,14 @@ template <int D>
 struct Cfg {
     static constexpr int kHalves = D / 64;
     static constexpr uint32_t kTile = kHalf * kHalves;
-    static constexpr int kStages = D == 64 ? 4 : 2;
-    static constexpr int kBufs = D == 64 ? 3 : 2;  // of S and G
-    static constexpr uint32_t kColAcc1 = 0, kColAcc2 = D, kColS = 2 * D, kColG = kColS + 64 * kBufs;  // + 64 per buffer
+    static constexpr int kX1 = D == 64 ? 5 : 2, kX2 = D == 64 ? 4 : 2;  // ring slots of X1 and X2
+    static constexpr int kBufs = D == 64 ? 2 : 1;                       // buffers of S
+    static constexpr uint32_t kColAcc1 = 0, kColAcc2 = D, kColG = 2 * D, kColS = kColG + 128;  // S: + 128 per buffer
     static constexpr uint32_t kOffStat = 1024, kOffR = kOffStat + kStatSlots * kStatBytes + 1024;
-    static constexpr uint32_t kOffX1 = kOffR + 2 * kTile, kOffX2 = kOffX1 + kStages * kTile;
-    static constexpr uint32_t kSmem = 1024 + kOffX2 + kStages * kTile;  // + 1 KB alignment slack
+    static constexpr uint32_t kOffX1 = kOffR + 2 * kTile, kOffX2 = kOffX1 + kX1 * kTile;
+    static constexpr uint32_t kSmem = 1024 + kOffX2 + kX2 * kTile;  // + 1 KB alignment slack
     static_assert(kOffR % 1024 == 0, "operand tiles must be 1 KB aligned");
+    static_assert(kColS + 128 * kBufs <= 512, "tensor memory");
     static_assert(kSmem + 1024 <= 232448, "shared memory over the per-block limit");
 };
 
@@ -77,23 +80,39 @@ struct BwdArgs {
     Args a;
     CUtensorMap q_map, k_map, v_map, go_map;
     const unsigned *norms;  // fp16: bits of max |dO row|^2, max |V row|^2
-    int64_t key_units;      // blocks [0, key_units) have keys resident
+    unsigned key_units;     // blocks [0, key_units) have keys resident
     uint32_t idesc1, idesc2;
 };
 
 struct Ctl {
-    uint64_t r_full, x_full[4], x_empty[4], st_full[kStatSlots], st_empty[kStatSlots];
-    uint64_t s_full[3], g_full[3], p_ready[3], free[3], acc_full, mma_done[2];
+    uint64_t r_full, x1_full[5], x1_empty[5], x2_full[4], x2_empty[4], st_full[kStatSlots], st_empty[kStatSlots];
+    uint64_t s_full[2], p_ready[2], g_full, d_ready, acc_full, mma_done[2];
     uint32_t tmem_base;
     int abort_flag, bad;
 };
 static_assert(sizeof(Ctl) <= 1024, "control block too large");
 
-// The streamed rows [lo, hi) of a unit, in copies of 128 and steps of 64; `heads`: query heads per copy position.
+// The streamed rows [lo, hi) of a unit in steps of 128, each for `heads` query heads: step j is rows lo + 128 (j / heads)
+// of head j % heads.
 struct Walk {
     int lo, hi, heads;
-    __device__ __forceinline__ int copies() const { return (hi - lo + kRows - 1) / kRows; }
-    __device__ __forceinline__ int steps(int c0) const { return hi - c0 > kCols ? 2 : 1; }
+    __device__ __forceinline__ int steps() const { return (hi - lo + kRows - 1) / kRows * heads; }
+};
+// Walks the steps without a division each.
+struct Cursor {
+    int row, r;  // first row of the step, head of the group
+    __device__ __forceinline__ void next(const Walk &k) {
+        if (++r == k.heads) r = 0, row += kRows;
+    }
+};
+// Slot and phase of a ring of N.
+template <int N>
+struct Ring {
+    int slot = 0;
+    uint32_t phase = 0;
+    __device__ __forceinline__ void next() {
+        if (++slot == N) slot = 0, phase ^= 1u;
+    }
 };
 
 template <bool KEYS>
@@ -105,7 +124,7 @@ __device__ __forceinline__ Walk walk_of(const Args &a, const Unit &u, int live) 
         if (a.window > 0 && u.p0 + live - 1 < u.len - a.window) w.hi = u.p0 + live - 1 + a.window;
         w.heads = a.hpk;
     } else {
-        w.lo = a.window > 0 && u.p0 - a.window + 1 > 0 ? (u.p0 - a.window + 1) / kCols * kCols : 0;
+        w.lo = a.window > 0 && u.p0 - a.window + 1 > 0 ? (u.p0 - a.window + 1) / 64 * 64 : 0;
         w.hi = u.p0 + live;
         w.heads = 1;
     }
@@ -126,81 +145,103 @@ __device__ __forceinline__ float ds_scale(const BwdArgs &p) {
 }
 
 // ------------------------------------------------------------ first launch
-// One warp per head and run of 32 positions: G = hd / 8 lanes (a power of two at least that) take a row's 16-byte pieces.
-template <typename T>
-__global__ void __launch_bounds__(256) stats_kernel(const Args a, unsigned *norms, int group) {
+// Sums over the G lanes that share a row, for G rows at once: v[i] is this lane's part of the row of turn i; returns the
+// whole sum of the row of turn `piece` (this lane's place among the G).  Each shuffle halves what a lane carries: G - 1
+// of them in place of G log2(G).
+template <int G>
+__device__ __forceinline__ float transpose_sum(float (&v)[G], int piece) {
+#pragma unroll
+    for (int o = G / 2; o > 0; o >>= 1) {
+        const bool up = piece & o;
+#pragma unroll
+        for (int i = 0; i < o; ++i) {
+            const float keep = up ? v[i + o] : v[i], send = up ? v[i] : v[i + o];
+            v[i] = keep + __shfl_xor_sync(0xffffffffu, send, o);
+        }
+    }
+    return v[0];
+}
+
+// One warp per head and run of 32 positions: G lanes take a row's 16-byte pieces, 32 / G rows a turn, G turns.
+template <typename T, int G>
+__global__ void __launch_bounds__(256) stats_kernel(const Args a, unsigned *norms) {
     if (threadIdx.x == 0) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
     constexpr bool F16 = std::is_same<T, __half>::value;
-    const int lane = threadIdx.x & 31;
-    const int64_t w = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
-    const int runs = (a.tokens + 31) / 32;
-    const int64_t own = (int64_t)runs * a.nh;
-    const int piece = lane % group, sub = lane / group, per = 32 / group;
+    constexpr int PER = 32 / G, BATCH = G < 8 ? G : 8;  // rows a turn; turns whose loads are in flight together
+    const int lane = threadIdx.x & 31, piece = lane % G, sub = lane / G;
+    const unsigned w = blockIdx.x * 8u + (threadIdx.x >> 5), runs = ((unsigned)a.tokens + 31u) / 32u;
+    const unsigned own = runs * (unsigned)a.nh;
     const bool has = piece * 8 < a.hd;
-    const int first = F16 ? clamp_row(a.off[0], a.tokens) : 0, last = F16 ? clamp_row(a.off[a.seqs], a.tokens) : 0;
+    int first = 0, last = 0;  // the rows of sequences
+    if (F16) first = clamp_row(__ldg(a.off), a.tokens), last = clamp_row(__ldg(a.off + a.seqs), a.tokens);
+    float norm = 0.f;
     if (w < own) {
-        const int h = (int)(w % a.nh), t0 = (int)(w / a.nh) * 32;
-        float mine = 0.f, norm = 0.f;
-#pragma unroll 4
-        for (int r = 0; r < 32; r += per) {
-            const int t = t0 + r + sub;
-            float s = 0.f, n = 0.f;
-            if (has && t < a.tokens) {
-                const int64_t at = ((int64_t)t * a.nh + h) * a.hd + piece * 8;
-                const uint4 x = __ldg(reinterpret_cast<const uint4 *>(static_cast<const T *>(a.o) + at));
-                const uint4 y = __ldg(reinterpret_cast<const uint4 *>(static_cast<const T *>(a.go) + at));
-                const T *xs = reinterpret_cast<const T *>(&x), *ys = reinterpret_cast<const T *>(&y);
+        const int h = (int)(w % (unsigned)a.nh), t0 = (int)(w / (unsigned)a.nh) * 32;
+        const int64_t step = (int64_t)a.nh * a.hd;
+        const int64_t at = (int64_t)(t0 + sub) * step + (int64_t)h * a.hd + piece * 8;
+        const T *o = static_cast<const T *>(a.o) + at, *go = static_cast<const T *>(a.go) + at;
+        float s[G], n[G];
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    s = fmaf(to_f(xs[i]), to_f(ys[i]), s);
-                    if (F16) n = fmaf(to_f(ys[i]), to_f(ys[i]), n);
+        for (int b = 0; b < G; b += BATCH) {
+            uint4 x[BATCH], y[BATCH];
+#pragma unroll
+            for (int i = 0; i < BATCH; ++i) {
+                x[i] = y[i] = make_uint4(0, 0, 0, 0);
+                if (has && t0 + sub + (b + i) * PER < a.tokens) {
+                    x[i] = __ldg(reinterpret_cast<const uint4 *>(o + (b + i) * PER * step));
+                    y[i] = __ldg(reinterpret_cast<const uint4 *>(go + (b + i) * PER * step));
                 }
             }
-            for (int o = group / 2; o > 0; o >>= 1) {
-                s += __shfl_xor_sync(0xffffffffu, s, o);
-                if (F16) n += __shfl_xor_sync(0xffffffffu, n, o);
+#pragma unroll
+            for (int i = 0; i < BATCH; ++i) {
+                const T *xs = reinterpret_cast<const T *>(&x[i]), *ys = reinterpret_cast<const T *>(&y[i]);
+                s[b + i] = n[b + i] = 0.f;
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    s[b + i] = fmaf(to_f(xs[e]), to_f(ys[e]), s[b + i]);
+                    if (F16) n[b + i] = fmaf(to_f(ys[e]), to_f(ys[e]), n[b + i]);
+                }
             }
-            const float got = __shfl_sync(0xffffffffu, s, ((lane - r) & (per - 1)) * group);
-            if (lane >= r && lane < r + per) mine = got;
-            if (F16 && t >= first && t < last && finite(n)) norm = fmaxf(norm, n);
         }
-        const int t = t0 + lane;
+        const float delta = transpose_sum<G>(s, piece);
+        const int t = t0 + piece * PER + sub;  // the row whose sum this lane holds
+        if (F16) {
+            const float x = transpose_sum<G>(n, piece);
+            if (t >= first && t < last && finite(x)) norm = x;
+        }
         if (t < a.tokens) {
             const float *l = a.lse_in + ((int64_t)t * a.nh + h) * 2;
-            a.stats[(int64_t)h * a.tokens + t] = make_float2((l[0] + l[1]) * kLog2e, mine);
+            a.stats[(int64_t)h * a.tokens + t] = make_float2((l[0] + l[1]) * kLog2e, delta);
         }
-        if (F16) {
-            for (int o = 16; o > 0; o >>= 1) norm = fmaxf(norm, __shfl_xor_sync(0xffffffffu, norm, o));
-            if (lane == 0) atomicMax(norms, __float_as_uint(norm));
-        }
-    } else if (F16) {  // V's rows, for their largest norm
-        const int64_t x = w - own;
-        const int g = (int)(x % a.nkv);
-        if (x / a.nkv >= runs) return;
-        const int t0 = (int)(x / a.nkv) * 32;
-        float norm = 0.f;
-#pragma unroll 4
-        for (int r = 0; r < 32; r += per) {
-            const int t = t0 + r + sub;
-            float n = 0.f;
-            if (has && t < a.tokens) {
-                const uint4 y = __ldg(reinterpret_cast<const uint4 *>(static_cast<const T *>(a.v) + (int64_t)t * a.vs +
-                                                                      (int64_t)g * a.hd + piece * 8));
+    } else if (F16 && w < own + runs * (unsigned)a.nkv) {  // V's rows, for their largest norm
+        const unsigned x = w - own;
+        const int g = (int)(x % (unsigned)a.nkv), t0 = (int)(x / (unsigned)a.nkv) * 32;
+        const T *v = static_cast<const T *>(a.v) + (int64_t)(t0 + sub) * a.vs + (int64_t)g * a.hd + piece * 8;
+        float n[G];
+#pragma unroll
+        for (int i = 0; i < G; ++i) {
+            n[i] = 0.f;
+            if (has && t0 + sub + i * PER < a.tokens) {
+                const uint4 y = __ldg(reinterpret_cast<const uint4 *>(v + i * PER * a.vs));
                 const T *ys = reinterpret_cast<const T *>(&y);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) n = fmaf(to_f(ys[i]), to_f(ys[i]), n);
+                for (int e = 0; e < 8; ++e) n[i] = fmaf(to_f(ys[e]), to_f(ys[e]), n[i]);
             }
-            for (int o = group / 2; o > 0; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
-            if (t >= first && t < last && finite(n)) norm = fmaxf(norm, n);
         }
+        const float sum = transpose_sum<G>(n, piece);
+        const int t = t0 + piece * PER + sub;
+        if (t >= first && t < last && finite(sum)) norm = sum;
+    }
+    if (F16) {
         for (int o = 16; o > 0; o >>= 1) norm = fmaxf(norm, __shfl_xor_sync(0xffffffffu, norm, o));
-        if (lane == 0) atomicMax(norms + 1, __float_as_uint(norm));
+        // A maximum of non-negative floats, as unsigned integers: the same in any order.
+        if (lane == 0 && norm > 0.f) atomicMax(norms + (w < own ? 0 : 1), __float_as_uint(norm));
     }
 }
 
 // ----------------------------------------------------------- second launch
-// The loading thread: R1 and R2, then X1 and X2 of every ring slot.
+// The loading thread: R1 and R2, then X1 and X2 of every step.
 template <int D, bool KEYS>
 __device__ void role_load(const BwdArgs &p, Ctl &c, uint32_t smem, const Unit &u, const Walk &k, int head, int g,
                           const Waiter &w) {
@@ -209,154 +250,193 @@ __device__ void role_load(const BwdArgs &p, Ctl &c, uint32_t smem, const Unit &u
     const CUtensorMap *x1 = KEYS ? &p.q_map : &p.k_map, *x2 = KEYS ? &p.go_map : &p.v_map;
     load_rows<D>(smem + C::kOffR, r1, p.a.hd, head, u.begin + u.p0, kRows, su32(&c.r_full));
     load_rows<D>(smem + C::kOffR + C::kTile, r2, p.a.hd, head, u.begin + u.p0, kRows, su32(&c.r_full));
-    const int n = k.copies();
-    int it = 0;
-    bool ok = true;
-    for (int b = 0; b < n && ok; ++b)
-        for (int r = 0; r < k.heads; ++r, ++it) {
-            const int s = it % C::kStages, h = KEYS ? g * p.a.hpk + r : g, row = u.begin + k.lo + kRows * b;
-            if (!wait(su32(&c.x_empty[s]), (uint32_t)(((it / C::kStages) & 1) ^ 1), w)) {
-                ok = false;
-                break;
-            }
-            load_rows<D>(smem + C::kOffX1 + (uint32_t)s * C::kTile, x1, p.a.hd, h, row, kRows, su32(&c.x_full[s]));
-            load_rows<D>(smem + C::kOffX2 + (uint32_t)s * C::kTile, x2, p.a.hd, h, row, kRows, su32(&c.x_full[s]));
-        }
+    const int n = k.steps();
+    Ring<C::kX1> a;
+    Ring<C::kX2> b;
+    Cursor at{k.lo, 0};
+    int n1 = 0, n2 = 0;
+    for (int j = 0; j < n; ++j, at.next(k)) {
+        const int h = KEYS ? g * p.a.hpk + at.r : g, row = u.begin + at.row;
+        auto load1 = [&] {
+            if (!wait(su32(&c.x1_empty[a.slot]), a.phase ^ 1u, w)) return false;
+            load_rows<D>(smem + C::kOffX1 + (uint32_t)a.slot * C::kTile, x1, p.a.hd, h, row, kRows,
+                         su32(&c.x1_full[a.slot]));
+            a.next(), ++n1;
+            return true;
+        };
+        auto load2 = [&] {
+            if (!wait(su32(&c.x2_empty[b.slot]), b.phase ^ 1u, w)) return false;
+            load_rows<D>(smem + C::kOffX2 + (uint32_t)b.slot * C::kTile, x2, p.a.hd, h, row, kRows,
+                         su32(&c.x2_full[b.slot]));
+            b.next(), ++n2;
+            return true;
+        };
+        // X1 is wanted first; once the rings are full, X2's slot is the one that comes free first.
+        if (j < C::kX1 ? !load1() || !load2() : !load2() || !load1()) break;
+    }
     // Copies still landing must finish before the block exits.
     drain(su32(&c.r_full), 0, w);
-    for (int q = it > C::kStages ? it - C::kStages : 0; q < it; ++q)
-        drain(su32(&c.x_full[q % C::kStages]), (uint32_t)((q / C::kStages) & 1), w);
+    for (int q = n1 > C::kX1 ? n1 - C::kX1 : 0; q < n1; ++q)
+        drain(su32(&c.x1_full[q % C::kX1]), (uint32_t)((q / C::kX1) & 1), w);
+    for (int q = n2 > C::kX2 ? n2 - C::kX2 : 0; q < n2; ++q)
+        drain(su32(&c.x2_full[q % C::kX2]), (uint32_t)((q / C::kX2) & 1), w);
 }
 
-// Statistics of each step's 64 queries: per pair of columns (-stat, -stat, -delta, -delta).
+// Statistics of each step's 128 queries: per pair of columns (-stat, -stat, -delta, -delta).
 template <bool F16>
 __device__ void role_stats(const BwdArgs &p, Ctl &c, uint32_t smem, const Unit &u, const Walk &k, int g, float kappa,
                            int lane, const Waiter &w) {
-    const int n = k.copies();
-    int step = 0;
-    for (int b = 0; b < n; ++b)
-        for (int r = 0; r < k.heads; ++r) {
-            const int c0 = k.lo + kRows * b, ns = k.steps(c0);
-            const float2 *st = p.a.stats + (int64_t)(g * p.a.hpk + r) * p.a.tokens + u.begin;
-            for (int s = 0; s < ns; ++s, ++step) {
-                const int slot = step % kStatSlots, col = c0 + kCols * s + 2 * lane;
-                const float2 x = col < u.len ? __ldg(st + col) : make_float2(0.f, 0.f);
-                const float2 y = col + 1 < u.len ? __ldg(st + col + 1) : make_float2(0.f, 0.f);
-                if (!wait_warp(su32(&c.st_empty[slot]), (uint32_t)(((step / kStatSlots) & 1) ^ 1), w)) return;
-                const float shift = F16 ? kPShift : 0.f;
-                sts128(smem + 1024u + (uint32_t)slot * kStatBytes + (uint32_t)lane * 16u, __float_as_uint(shift - x.x),
-                       __float_as_uint(shift - y.x), __float_as_uint(-x.y * kappa), __float_as_uint(-y.y * kappa));
-                __syncwarp();
-                if (lane == 0) bar_arrive(su32(&c.st_full[slot]));
-            }
+    const int n = k.steps();
+    const float shift = F16 ? kPShift : 0.f;
+    Ring<kStatSlots> ring;
+    Cursor at{k.lo, 0};
+    for (int j = 0; j < n; ++j, at.next(k), ring.next()) {
+        const float2 *st = p.a.stats + (int64_t)(g * p.a.hpk + at.r) * p.a.tokens + u.begin;
+        float2 x[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int col = at.row + 64 * (i >> 1) + 2 * lane + (i & 1);
+            x[i] = col < u.len ? __ldg(st + col) : make_float2(0.f, 0.f);
         }
+        if (!wait_warp(su32(&c.st_empty[ring.slot]), ring.phase ^ 1u, w)) return;
+#pragma unroll
+        for (int i = 0; i < 4; i += 2)
+            sts128(smem + 1024u + (uint32_t)ring.slot * kStatBytes + (uint32_t)i * 256u + (uint32_t)lane * 16u,
+                   __float_as_uint(shift - x[i].x), __float_as_uint(shift - x[i + 1].x),
+                   __float_as_uint(-x[i].y * kappa), __float_as_uint(-x[i + 1].y * kappa));
+        __syncwarp();
+        if (lane == 0) bar_arrive(su32(&c.st_full[ring.slot]));
+    }
 }
 
-// The ring walk of one product warp: visit(slot, half, step, first use of the slot, last use, first row of the copy)
-// for every step, until it returns false.
-template <int STAGES, typename F>
-__device__ __forceinline__ bool for_steps(const Walk &k, F visit) {
-    const int n = k.copies();
-    int it = 0, step = 0;
-    for (int b = 0; b < n; ++b)
-        for (int r = 0; r < k.heads; ++r, ++it) {
-            const int c0 = k.lo + kRows * b, ns = k.steps(c0);
-            for (int s = 0; s < ns; ++s, ++step)
-                if (!visit(it % STAGES, (uint32_t)((it / STAGES) & 1), s, step, s == 0, s == ns - 1, c0)) return false;
-        }
-    return true;
+// D / 16 products a . b^T of [128][D] tiles (K-major) into 128 columns at `d`.
+template <int D>
+__device__ __forceinline__ void scores(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t leader) {
+#pragma unroll
+    for (int i = 0; i < D / 16; ++i) {  // +32 bytes of each row, then the next half
+        const uint64_t off = 2u * (i % 4) + (uint64_t)(i / 4) * (kHalf >> 4);
+        tc_mma_f16_if(d, a + off, b + off, idesc, i > 0, leader);
+    }
+}
+// 8 products of P or dS (16 columns at every 32 from `a`) and 128 rows of X, added to D columns at `d`.
+__device__ __forceinline__ void sums(uint32_t d, uint32_t a, uint64_t x, uint32_t idesc, bool first, uint32_t leader) {
+#pragma unroll
+    for (int i = 0; i < kRows / 16; ++i)
+        tc_mma_f16_ts_if(d, a + 32u * (i / 2) + 8u * (i % 2), x + 128u * i, idesc, !first || i > 0, leader);
 }
 
-// S and G of every step, into the next buffer once the sums have read what it held.
+// acc2 of every step and S of the step kBufs later.  With queries resident there is no acc2: p_ready then only says
+// that S is read.
 template <int D, bool KEYS>
-__device__ __forceinline__ void issue_scores(const BwdArgs &p, Ctl &c, uint32_t smem, uint32_t tmem, int seq_end,
-                                             const Walk &k, int lane, const Waiter &w) {
+__device__ __forceinline__ void issue_s(const BwdArgs &p, Ctl &c, uint32_t smem, uint32_t tmem, int seq_end,
+                                        const Walk &k, int lane, const Waiter &w) {
     using C = Cfg<D>;
     const uint32_t leader = lane == 0;
-    const uint64_t r1 = desc_k(smem + C::kOffR), r2 = desc_k(smem + C::kOffR + C::kTile);
+    const uint64_t r1 = desc_k(smem + C::kOffR);
+    const int n = k.steps();
+    Ring<C::kX1> x1;
+    Ring<C::kX2> x2;
+    Ring<C::kBufs> buf, ahead;
+    Cursor at{k.lo, 0};
+    auto next_s = [&] {
+        if (!wait_warp(su32(&c.x1_full[x1.slot]), x1.phase, w)) return false;
+        tc_after();
+        scores<D>(tmem + C::kColS + 128u * ahead.slot, r1, desc_k(smem + C::kOffX1 + (uint32_t)x1.slot * C::kTile), p.idesc1,
+                  leader);
+        tc_commit_to_if(su32(&c.s_full[ahead.slot]), leader);
+        x1.next(), ahead.next();
+        return true;
+    };
     if (!wait_warp(su32(&c.r_full), 0, w)) return;
-    for_steps<C::kStages>(k, [&](int slot, uint32_t phase, int s, int step, bool fresh, bool, int c0) {
-        const int buf = step % C::kBufs;
-        if (fresh) {
-            if (!wait_warp(su32(&c.x_full[slot]), phase, w)) return false;
-            if (seq_end - c0 < kRows) {
-                zero_rows(smem + C::kOffX1 + (uint32_t)slot * C::kTile, seq_end - c0, kRows, C::kHalves, lane);
-                if (KEYS) zero_rows(smem + C::kOffX2 + (uint32_t)slot * C::kTile, seq_end - c0, kRows, C::kHalves, lane);
-            }
+    for (int j = 0; j < C::kBufs && j < n; ++j)
+        if (!next_s()) return;
+    for (int j = 0; j < n; ++j, at.next(k), buf.next(), x2.next()) {
+        if (!wait_warp(su32(&c.p_ready[buf.slot]), buf.phase, w)) return;
+        if (KEYS) {
+            if (!wait_warp(su32(&c.x2_full[x2.slot]), x2.phase, w)) return;
+            const uint32_t x = smem + C::kOffX2 + (uint32_t)x2.slot * C::kTile;
+            if (seq_end - at.row < kRows) zero_rows(x, seq_end - at.row, kRows, C::kHalves, lane);
+            tc_after();
+            sums(tmem + C::kColAcc2, tmem + C::kColS + 128u * buf.slot, desc_mn(x, kHalf, 1024u), p.idesc2, j == 0, leader);
         }
-        if (!wait_warp(su32(&c.free[buf]), (uint32_t)(((step / C::kBufs) & 1) ^ 1), w)) return false;
-        tc_after();
-        const uint32_t at = (uint32_t)slot * C::kTile + (uint32_t)s * (kCols * 128u);
-        const uint64_t x1 = desc_k(smem + C::kOffX1 + at), x2 = desc_k(smem + C::kOffX2 + at);
-#pragma unroll
-        for (int i = 0; i < D / 16; ++i) {
-            const uint64_t off = 2u * (i % 4) + (uint64_t)(i / 4) * (kHalf >> 4);
-            tc_mma_f16_if(tmem + C::kColS + 64u * buf, r1 + off, x1 + off, p.idesc1, i > 0, leader);
-        }
-        tc_commit_to_if(su32(&c.s_full[buf]), leader);
-#pragma unroll
-        for (int i = 0; i < D / 16; ++i) {
-            const uint64_t off = 2u * (i % 4) + (uint64_t)(i / 4) * (kHalf >> 4);
-            tc_mma_f16_if(tmem + C::kColG + 64u * buf, r2 + off, x2 + off, p.idesc1, i > 0, leader);
-        }
-        tc_commit_to_if(su32(&c.g_full[buf]), leader);
-        return true;
-    });
+        tc_commit_to_if(su32(&c.x2_empty[x2.slot]), leader);
+        if (j + C::kBufs < n && !next_s()) return;
+    }
+    tc_commit_to_if(su32(&c.acc_full), leader);
 }
 
-// acc1 += dS X1 and acc2 += P X2 of every step.
-template <int D, bool KEYS>
-__device__ __forceinline__ void issue_sums(const BwdArgs &p, Ctl &c, uint32_t smem, uint32_t tmem, const Walk &k,
-                                           int lane, const Waiter &w) {
+// acc1 of every step and G of the next.
+template <int D>
+__device__ __forceinline__ void issue_g(const BwdArgs &p, Ctl &c, uint32_t smem, uint32_t tmem, int seq_end,
+                                        const Walk &k, int lane, const Waiter &w) {
     using C = Cfg<D>;
     const uint32_t leader = lane == 0;
-    const bool done = for_steps<C::kStages>(k, [&](int slot, uint32_t, int s, int step, bool, bool last, int) {
-        const int buf = step % C::kBufs;
-        if (!wait_warp(su32(&c.p_ready[buf]), (uint32_t)((step / C::kBufs) & 1), w)) return false;
+    const uint64_t r2 = desc_k(smem + C::kOffR + C::kTile);
+    const int n = k.steps();
+    Ring<C::kX1> x1;
+    Ring<C::kX2> x2;
+    Cursor at{k.lo, 0};
+    auto next_g = [&] {
+        if (!wait_warp(su32(&c.x2_full[x2.slot]), x2.phase, w)) return false;
         tc_after();
-        const uint32_t at = (uint32_t)slot * C::kTile + (uint32_t)s * (kCols * 128u);
-        const uint64_t x1 = desc_mn(smem + C::kOffX1 + at, kHalf, 1024u), x2 = desc_mn(smem + C::kOffX2 + at, kHalf, 1024u);
-        if (KEYS) {
-#pragma unroll
-            for (int i = 0; i < kCols / 16; ++i)
-                tc_mma_f16_ts_if(tmem + C::kColAcc2, tmem + C::kColS + 64u * buf + 32u * (i / 2) + 8u * (i % 2),
-                                 x2 + 128u * i, p.idesc2, step > 0 || i > 0, leader);
-        }
-#pragma unroll
-        for (int i = 0; i < kCols / 16; ++i)
-            tc_mma_f16_ts_if(tmem + C::kColAcc1, tmem + C::kColG + 64u * buf + 32u * (i / 2) + 8u * (i % 2),
-                             x1 + 128u * i, p.idesc2, step > 0 || i > 0, leader);
-        tc_commit_to_if(su32(&c.free[buf]), leader);
-        if (last) tc_commit_to_if(su32(&c.x_empty[slot]), leader);
+        scores<D>(tmem + C::kColG, r2, desc_k(smem + C::kOffX2 + (uint32_t)x2.slot * C::kTile), p.idesc1, leader);
+        tc_commit_to_if(su32(&c.g_full), leader);
+        tc_commit_to_if(su32(&c.x2_empty[x2.slot]), leader);
+        x2.next();
         return true;
-    });
-    if (done) tc_commit_to_if(su32(&c.acc_full), leader);
+    };
+    if (!wait_warp(su32(&c.r_full), 0, w)) return;
+    if (!next_g()) return;
+    for (int j = 0; j < n; ++j, at.next(k), x1.next()) {
+        if (!wait_warp(su32(&c.d_ready), (uint32_t)(j & 1), w)) return;
+        if (!wait_warp(su32(&c.x1_full[x1.slot]), x1.phase, w)) return;
+        const uint32_t x = smem + C::kOffX1 + (uint32_t)x1.slot * C::kTile;
+        if (seq_end - at.row < kRows) zero_rows(x, seq_end - at.row, kRows, C::kHalves, lane);
+        tc_after();
+        sums(tmem + C::kColAcc1, tmem + C::kColG, desc_mn(x, kHalf, 1024u), p.idesc2, j == 0, leader);
+        tc_commit_to_if(su32(&c.x1_empty[x1.slot]), leader);
+        if (j + 1 < n && !next_g()) return;
+    }
+    tc_commit_to_if(su32(&c.acc_full), leader);
 }
 
-// P and dS of 32 columns.  s, g: this row's scores and dP; columns outside [from, to] are masked when MASK.  With
-// KEYS the statistics are per column at shared address `st`, else (nl, nd) of the row.
+// P of 32 columns from this row's scores; columns outside [from, to] are masked when MASK.  With KEYS the statistic is
+// per column at shared address `st`, else nl of the row.
 template <bool F16, bool KEYS, bool MASK>
-__device__ __forceinline__ void grad32(const uint32_t (&s)[32], const uint32_t (&g)[32], float cs, float kappa,
-                                       uint32_t st, float nl, float nd, int from, int to, uint32_t (&pp)[16],
-                                       uint32_t (&pd)[16]) {
-    const float2 c2 = make_float2(cs, cs), k2 = make_float2(kappa, kappa);
-    float2 l2 = make_float2(nl, nl), d2 = make_float2(nd, nd);
+__device__ __forceinline__ void probs32(uint32_t (&s)[32], float cs, uint32_t st, float nl, int from, int to,
+                                        uint32_t (&pp)[16]) {
+    const float2 c2 = make_float2(cs, cs);
+    float2 l2 = make_float2(nl, nl);
 #pragma unroll
     for (int e = 0; e < 32; e += 2) {
-        if (KEYS) {
-            const uint4 x = lds128(st + (uint32_t)e * 8u);
-            l2 = make_float2(__uint_as_float(x.x), __uint_as_float(x.y));
-            d2 = make_float2(__uint_as_float(x.z), __uint_as_float(x.w));
-        }
+        if (KEYS)
+            asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(l2.x), "=f"(l2.y) : "r"(st + (uint32_t)e * 8u) : "memory");
         const float2 x = __ffma2_rn(make_float2(__uint_as_float(s[e]), __uint_as_float(s[e + 1])), c2, l2);
         float2 y = make_float2(fast_exp2(x.x), fast_exp2(x.y));
-        const float2 z = __ffma2_rn(make_float2(__uint_as_float(g[e]), __uint_as_float(g[e + 1])), k2, d2);
-        float2 d = __fmul2_rn(y, z);
         if (MASK) {
-            if (e < from || e > to) y.x = 0.f, d.x = 0.f;
-            if (e + 1 < from || e + 1 > to) y.y = 0.f, d.y = 0.f;
+            if (e < from || e > to) y.x = 0.f;
+            if (e + 1 < from || e + 1 > to) y.y = 0.f;
         }
         if (KEYS) pp[e >> 1] = pack2<F16>(y.x, y.y);
+        s[e] = __float_as_uint(y.x), s[e + 1] = __float_as_uint(y.y);
+    }
+}
+// dS = P (G - delta) of 32 columns: p as probs32 leaves it.  A masked column's P is 0, its G may be anything.
+template <bool F16, bool KEYS, bool MASK>
+__device__ __forceinline__ void grads32(const uint32_t (&p)[32], const uint32_t (&g)[32], float kappa, uint32_t st,
+                                        float nd, int from, int to, uint32_t (&pd)[16]) {
+    const float2 k2 = make_float2(kappa, kappa);
+    float2 d2 = make_float2(nd, nd);
+#pragma unroll
+    for (int e = 0; e < 32; e += 2) {
+        if (KEYS)
+            asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(d2.x), "=f"(d2.y) : "r"(st + (uint32_t)e * 8u + 8u) : "memory");
+        const float2 z = __ffma2_rn(make_float2(__uint_as_float(g[e]), __uint_as_float(g[e + 1])), k2, d2);
+        float2 d = __fmul2_rn(make_float2(__uint_as_float(p[e]), __uint_as_float(p[e + 1])), z);
+        if (MASK) {
+            if (e < from || e > to) d.x = 0.f;
+            if (e + 1 < from || e + 1 > to) d.y = 0.f;
+        }
         pd[e >> 1] = pack2<F16>(d.x, d.y);
     }
 }
@@ -401,69 +481,68 @@ __device__ void role_soft(const BwdArgs &p, Ctl &c, uint32_t smem, uint32_t tmem
                           int head, float sigma, int warp, int lane, const Waiter &w) {
     using C = Cfg<D>;
     const Args &a = p.a;
-    const int quad = warp & 3, part = (warp >> 2) & 1, grp = warp >> 3, row = u.p0 + 32 * quad + lane;
+    const int quad = warp & 3, cols = 32 * (warp >> 2), row = u.p0 + 32 * quad + lane;
     const uint32_t lane_tm = (uint32_t)(32 * quad) << 16;
+    const uint32_t g_tm = tmem + lane_tm + C::kColG + (uint32_t)cols;
     const float cs = a.scale * kLog2e, kappa = F16 ? sigma * 0x1p-13f : 1.f;
     float nl = 0.f, nd = 0.f;
     if (!KEYS && row < u.len) {
         const float2 st = __ldg(a.stats + (int64_t)head * a.tokens + u.begin + row);
         nl = (F16 ? kPShift : 0.f) - st.x, nd = -st.y * kappa;
     }
-    const int n = k.copies();
-    int step = 0;
-    for (int b = 0; b < n; ++b) {
-        const int c0 = k.lo + kRows * b, ns = k.steps(c0);
-        for (int r = 0; r < k.heads; ++r)
-            for (int s = 0; s < ns; ++s, ++step) {
-                if ((step & 1) != grp) continue;
-                const int base = c0 + kCols * s + 32 * part, slot = step % kStatSlots, buf = step % C::kBufs;
-                const uint32_t phase = (uint32_t)((step / C::kBufs) & 1);
-                const uint32_t s_tm = tmem + lane_tm + C::kColS + 64u * buf, g_tm = tmem + lane_tm + C::kColG + 64u * buf;
-                int from, to;
-                bool whole;
-                if (KEYS) {
-                    from = row - base;
-                    int end = u.len;
-                    if (a.window > 0 && row < u.len - a.window) end = row + a.window;
-                    to = end - 1 - base;
-                    whole = base >= u.p0 + kRows - 1 && base + 32 <= u.len &&
-                            (a.window == 0 || base + 31 < u.p0 + a.window);
-                    if (!wait_warp(su32(&c.st_full[slot]), (uint32_t)((step / kStatSlots) & 1), w)) return;
-                } else {
-                    from = a.window > 0 ? row - a.window + 1 - base : 0;
-                    to = row - base;
-                    whole = base + 31 <= u.p0 && (a.window == 0 || u.p0 + kRows - 1 < base + a.window);
-                }
-                uint32_t sv[32], gv[32], pp[16], pd[16];
-                if (!wait_warp(su32(&c.s_full[buf]), phase, w)) return;
-                tc_after();
-                tc_ld_32x32(s_tm + 32 * part, sv);
-                if (!wait_warp(su32(&c.g_full[buf]), phase, w)) return;
-                tc_after();
-                tc_ld_32x32(g_tm + 32 * part, gv);
-                tc_wait_ld(sv);
-                tc_wait_ld(gv);
-                // The warp of the other 32 columns may still read its half of S and G: P and dS (16 columns) go over
-                // this warp's own half.
-                const uint32_t st = smem + 1024u + (uint32_t)slot * kStatBytes + 256u * part;
-                if (whole)
-                    grad32<F16, KEYS, false>(sv, gv, cs, kappa, st, nl, nd, 0, 0, pp, pd);
-                else
-                    grad32<F16, KEYS, true>(sv, gv, cs, kappa, st, nl, nd, from, to, pp, pd);
-                if (KEYS) tc_st_32x16(s_tm + 32 * part, pp);
-                tc_st_32x16(g_tm + 32 * part, pd);
-                tc_wait_st();
-                tc_before();
-                __syncwarp();
-                if (lane == 0) {
-                    bar_arrive(su32(&c.p_ready[buf]));
-                    if (KEYS) bar_arrive(su32(&c.st_empty[slot]));
-                }
-            }
+    // The rows that this one meets: queries [row, end) with keys resident, else keys [first, row].
+    const int first = a.window > 0 ? row - a.window + 1 : 0;
+    const int end = a.window > 0 && row < u.len - a.window ? row + a.window : u.len;
+    const int n = k.steps();
+    Ring<C::kBufs> buf;
+    Ring<kStatSlots> stat;
+    Cursor cur{k.lo, 0};
+    for (int j = 0; j < n; ++j, cur.next(k), buf.next(), stat.next()) {
+        const int base = cur.row + cols;
+        const int from = (KEYS ? row : first) - base, to = (KEYS ? end - 1 : row) - base;
+        const bool whole = KEYS ? base >= u.p0 + kRows - 1 && base + 32 <= u.len &&
+                                      (a.window == 0 || base + 31 < u.p0 + a.window)
+                                : base + 31 <= u.p0 && (a.window == 0 || u.p0 + kRows - 1 < base + a.window);
+        const uint32_t st = smem + 1024u + (uint32_t)stat.slot * kStatBytes + 8u * (uint32_t)cols;
+        const uint32_t s_tm = tmem + lane_tm + C::kColS + 128u * (uint32_t)buf.slot + (uint32_t)cols;
+        uint32_t pv[32], gv[32], pk[16];
+        if (KEYS && !wait_warp(su32(&c.st_full[stat.slot]), stat.phase, w)) return;
+        if (!wait_warp(su32(&c.s_full[buf.slot]), buf.phase, w)) return;
+        tc_after();
+        tc_ld_32x32(s_tm, pv);
+        tc_wait_ld(pv);
+        if (whole)
+            probs32<F16, KEYS, false>(pv, cs, st, nl, 0, 0, pk);
+        else
+            probs32<F16, KEYS, true>(pv, cs, st, nl, from, to, pk);
+        if (KEYS) {
+            tc_st_32x16(s_tm, pk);
+            tc_wait_st();
+        }
+        tc_before();
+        __syncwarp();
+        if (lane == 0) bar_arrive(su32(&c.p_ready[buf.slot]));
+        if (!wait_warp(su32(&c.g_full), (uint32_t)(j & 1), w)) return;
+        tc_after();
+        tc_ld_32x32(g_tm, gv);
+        tc_wait_ld(gv);
+        if (whole)
+            grads32<F16, KEYS, false>(pv, gv, kappa, st, nd, 0, 0, pk);
+        else
+            grads32<F16, KEYS, true>(pv, gv, kappa, st, nd, from, to, pk);
+        tc_st_32x16(g_tm, pk);
+        tc_wait_st();
+        tc_before();
+        __syncwarp();
+        if (lane == 0) {
+            bar_arrive(su32(&c.d_ready));
+            if (KEYS) bar_arrive(su32(&c.st_empty[stat.slot]));
+        }
     }
     if (!wait_warp(su32(&c.acc_full), 0, w)) return;
     tc_after();
     // The resident tiles are read by now: group 0 stages dK or dQ in R1, group 1 dV in R2, half of the columns a warp.
+    const int grp = warp >> 3, part = (warp >> 2) & 1;
     if (!KEYS && grp == 1) return;
     constexpr int W = D / 2;
     const int heads = KEYS ? a.nkv : a.nh;
@@ -534,7 +613,7 @@ __device__ __noinline__ void recompute(const Args &a, const Unit &u, int live, i
 }
 
 template <int D, bool F16, bool KEYS>
-__device__ __forceinline__ void unit_body(const BwdArgs &p, Ctl &c, uint32_t smem, uint32_t tmem, int64_t index,
+__device__ __forceinline__ void unit_body(const BwdArgs &p, Ctl &c, uint32_t smem, uint32_t tmem, unsigned index,
                                           bool check, int warp, int lane) {
     using C = Cfg<D>;
     const unsigned heads = KEYS ? p.a.nkv : p.a.nh;
@@ -562,9 +641,9 @@ __device__ __forceinline__ void unit_body(const BwdArgs &p, Ctl &c, uint32_t sme
         const uint32_t sm = uniform(smem), tm = uniform(tmem);
         const Walk ku{uniform(k.lo), uniform(k.hi), uniform(k.heads)};
         if (second)
-            issue_sums<D, KEYS>(p, c, sm, tm, ku, lane, w);
+            issue_g<D>(p, c, sm, tm, uniform(u.len), ku, lane, w);
         else
-            issue_scores<D, KEYS>(p, c, sm, tm, uniform(u.len), ku, lane, w);
+            issue_s<D, KEYS>(p, c, sm, tm, uniform(u.len), ku, lane, w);
         tc_commit_to_if(su32(&c.mma_done[second]), lane == 0);  // nothing may still run when tensor memory is released
         drain(su32(&c.mma_done[second]), 0, w);
         __syncwarp();
@@ -589,21 +668,25 @@ __global__ void __launch_bounds__(kThreads, 1) backward_tc_kernel(const __grid_c
     const int warp = uniform((int)(threadIdx.x >> 5)), lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
         bar_init(su32(&c.r_full), 2);
+        for (int s = 0; s < 5; ++s) {
+            bar_init(su32(&c.x1_full[s]), 1);
+            bar_init(su32(&c.x1_empty[s]), 1);
+        }
         for (int s = 0; s < 4; ++s) {
-            bar_init(su32(&c.x_full[s]), 2);
-            bar_init(su32(&c.x_empty[s]), 1);
+            bar_init(su32(&c.x2_full[s]), 1);
+            bar_init(su32(&c.x2_empty[s]), 2);  // G and acc2
         }
         for (int s = 0; s < kStatSlots; ++s) {
             bar_init(su32(&c.st_full[s]), 1);
-            bar_init(su32(&c.st_empty[s]), 8);
+            bar_init(su32(&c.st_empty[s]), kSoftWarps);
         }
-        for (int i = 0; i < 3; ++i) {
+        for (int i = 0; i < 2; ++i) {
             bar_init(su32(&c.s_full[i]), 1);
-            bar_init(su32(&c.g_full[i]), 1);
-            bar_init(su32(&c.p_ready[i]), 8);
-            bar_init(su32(&c.free[i]), 1);
+            bar_init(su32(&c.p_ready[i]), kSoftWarps);
         }
-        bar_init(su32(&c.acc_full), 1);
+        bar_init(su32(&c.g_full), 1);
+        bar_init(su32(&c.d_ready), kSoftWarps);
+        bar_init(su32(&c.acc_full), 2);
         bar_init(su32(&c.mma_done[0]), 1);
         bar_init(su32(&c.mma_done[1]), 1);
         c.abort_flag = 0;
@@ -615,12 +698,16 @@ __global__ void __launch_bounds__(kThreads, 1) backward_tc_kernel(const __grid_c
     __syncthreads();
     tc_after();
     const uint32_t tmem = c.tmem_base;
+    if (threadIdx.x < 4) {
+        const CUtensorMap *m = threadIdx.x == 0 ? &p.q_map : threadIdx.x == 1 ? &p.k_map : threadIdx.x == 2 ? &p.v_map : &p.go_map;
+        asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(m)) : "memory");
+    }
     if (threadIdx.x == 0) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    if ((int64_t)blockIdx.x < p.key_units)
+    if (blockIdx.x < p.key_units)
         unit_body<D, F16, true>(p, c, smem, tmem, blockIdx.x, blockIdx.x == 0, warp, lane);
     else
-        unit_body<D, F16, false>(p, c, smem, tmem, (int64_t)blockIdx.x - p.key_units, false, warp, lane);
+        unit_body<D, F16, false>(p, c, smem, tmem, blockIdx.x - p.key_units, false, warp, lane);
     __syncthreads();
     if (warp == kMmaWarp) tc_dealloc(tmem, 512);
 }
@@ -633,11 +720,9 @@ int launch(const BwdArgs &q, int64_t blocks, cudaStream_t st) {
 
 template <typename T>
 int launch_stats(const Args &a, unsigned *norms, cudaStream_t st) {
-    int group = 1;
-    while (group * 8 < a.hd) group *= 2;
-    const int64_t runs = (a.tokens + 31) / 32, warps = runs * (a.nh + (std::is_same<T, __half>::value ? a.nkv : 0));
-    if (std::is_same<T, __half>::value && cudaMemsetAsync(norms, 0, 2 * sizeof(unsigned), st) != cudaSuccess)
-        return DGRAD_ERR_CUDA;
+    constexpr bool F16 = std::is_same<T, __half>::value;
+    if (F16 && cudaMemsetAsync(norms, 0, 2 * sizeof(unsigned), st) != cudaSuccess) return DGRAD_ERR_CUDA;
+    const int64_t warps = ((int64_t)a.tokens + 31) / 32 * (a.nh + (F16 ? a.nkv : 0));
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((unsigned)((warps + 7) / 8));
     cfg.blockDim = dim3(256);
@@ -647,7 +732,13 @@ int launch_stats(const Args &a, unsigned *norms, cudaStream_t st) {
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, stats_kernel<T>, a, norms, group) == cudaSuccess ? DGRAD_OK : DGRAD_ERR_CUDA;
+    const int pieces = (a.hd + 7) / 8;
+    auto kern = pieces <= 1 ? stats_kernel<T, 1>
+                : pieces <= 2 ? stats_kernel<T, 2>
+                : pieces <= 4 ? stats_kernel<T, 4>
+                : pieces <= 8 ? stats_kernel<T, 8>
+                              : stats_kernel<T, 16>;
+    return cudaLaunchKernelEx(&cfg, kern, a, norms) == cudaSuccess ? DGRAD_OK : DGRAD_ERR_CUDA;
 }
 
 }  // namespace
@@ -657,7 +748,7 @@ int backward_tc(const Args &a, unsigned *norms, const mha_packed_params *p, int 
     q.a = a;
     q.norms = norms;
     const int D = a.hd <= 64 ? 64 : 128;
-    q.idesc1 = instr_desc(dtype, kRows, kCols, false);
+    q.idesc1 = instr_desc(dtype, kRows, kRows, false);
     q.idesc2 = instr_desc(dtype, kRows, D, true);
     const int64_t dense = (int64_t)a.nh * a.hd;
     if (!encode_rows(&q.q_map, a.q, a.tokens, a.nh, a.hd, a.qs, kRows) ||
@@ -669,8 +760,9 @@ int backward_tc(const Args &a, unsigned *norms, const mha_packed_params *p, int 
     const int rc = f16 ? launch_stats<__half>(a, norms, st) : launch_stats<__nv_bfloat16>(a, norms, st);
     if (rc != DGRAD_OK) return rc;
     const int64_t units = unit_bound(p, kRows);
-    q.key_units = units * a.nkv;
-    const int64_t blocks = q.key_units + units * a.nh;
+    const int64_t blocks = units * (a.nkv + a.nh);
+    if (blocks > INT32_MAX) return DGRAD_ERR_UNSUPPORTED;
+    q.key_units = (unsigned)(units * a.nkv);
     if (D == 64) return f16 ? launch<64, true>(q, blocks, st) : launch<64, false>(q, blocks, st);
     return f16 ? launch<128, true>(q, blocks, st) : launch<128, false>(q, blocks, st);
 }

@@ -69,43 +69,43 @@ __device__ __forceinline__ void segment(const Args &a, int i, int &begin, int &l
 // else ascending (keys: those with the most queries).  Each thread adds up the tiles of a run of segments, the block scans
 // those sums, and the thread whose run holds `u` walks it: two rounds of loads for
 // any number of sequences.  `check`: raise the error flag where offsets are malformed.
-__device__ __forceinline__ Unit find_unit(const Args &a, int64_t u, int rows, bool down, bool check,
+__device__ __forceinline__ Unit find_unit(const Args &a, unsigned u, int rows, bool down, bool check,
                                           unsigned *error) {
-    __shared__ int64_t warp_sum[32];
+    __shared__ unsigned warp_sum[32];
     __shared__ Unit found;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, n = a.seqs + 2;
-    const int per = (n + (int)blockDim.x - 1) / (int)blockDim.x;
+    const int per = a.seqs + 2 <= (int)blockDim.x ? 1 : (n + (int)blockDim.x - 1) / (int)blockDim.x;
     const int i0 = tid * per < n ? tid * per : n, i1 = i0 + per < n ? i0 + per : n;
-    int64_t sum = 0;
+    unsigned sum = 0;
+    int begin = 0, len = 0;  // of the last segment of the run
     for (int i = i0; i < i1; ++i) {
-        int begin, len;
         segment(a, i, begin, len);
-        sum += (len + rows - 1) / rows;
+        sum += (unsigned)((len + rows - 1) / rows);
         if (check && i < a.seqs) {
             const int lo = __ldg(a.off + i), hi = __ldg(a.off + i + 1);
             if (lo < 0 || hi < lo || hi > a.tokens) atomicOr(error, kErrOffsets);
         }
     }
-    int64_t incl = sum;
+    unsigned incl = sum;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const int64_t x = __shfl_up_sync(0xffffffffu, incl, o);
+        const unsigned x = __shfl_up_sync(0xffffffffu, incl, o);
         if (lane >= o) incl += x;
     }
     if (lane == 31) warp_sum[warp] = incl;
     if (tid == 0) found.live = false;
     __syncthreads();
-    for (int w = 0; w < warp; ++w) incl += warp_sum[w];
-    int64_t at = incl - sum;
-    if (u >= at && u < incl)
+    if (n > 32 * per)  // else the first warp holds every segment
+        for (int w = 0; w < warp; ++w) incl += warp_sum[w];
+    unsigned at = incl - sum;
+    if (u >= at && u < incl && i0 < i1)
         for (int i = i0; i < i1; ++i) {
-            int begin, len;
-            segment(a, i, begin, len);
-            const int tiles = (len + rows - 1) / rows;
+            if (per > 1) segment(a, i, begin, len);
+            const unsigned tiles = (unsigned)((len + rows - 1) / rows);
             if (u < at + tiles) {
                 found.begin = begin;
                 found.len = len;
-                found.p0 = (down ? tiles - 1 - (int)(u - at) : (int)(u - at)) * rows;
+                found.p0 = (int)(down ? tiles - 1 - (u - at) : u - at) * rows;
                 found.pad = i >= a.seqs;
                 found.live = true;
                 break;
