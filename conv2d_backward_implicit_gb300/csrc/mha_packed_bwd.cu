@@ -15,18 +15,20 @@
 //                                 tensor memory, X as the MN-major operand
 // so scores are formed twice (7 products in place of 5), and in return every gradient
 // is one block's sum in a fixed order: no atomics, nothing to zero or convert after.
-// Tensor memory: acc1 and acc2 (D columns each), one buffer of S (two at D = 64) and one
-// of G, 128 columns each, with P and dS over the first 16 of each 32.  Steps of 128
-// columns because a product of N = 64 takes nearly as long as one of N = 128 (65 against
-// 75 cycles); what overlaps is then not two steps but the two halves of one: while P of a
-// step goes through acc2 and the next S, its dS is formed, and while dS goes through
-// acc1 and the next G, the next P is.
+// Tensor memory: acc1 and acc2 (D columns each), and a ring of two (D = 128) or three
+// regions of 128 columns that takes S and G of step after step in turn, with P and dS
+// over the first 16 of each 32.  Steps of 128 columns because a product of N = 64 takes
+// nearly as long as one of N = 128 (65 against 75 cycles); what overlaps is then not two
+// steps but the two halves of one: while P of a step goes through acc2 and the region's
+// next scores, its dS is formed, and the other way round.
 //   * warps 0-15: P, then dS, 32 columns of one resident row per thread; at the end dK /
 //     dQ (warps 0-7) and dV (8-15);
-//   * warp 16 (converged, lane 0 issuing): acc2 of a step, then S of a later one; warp 17:
-//     acc1 of a step, then G of the next.  A warp's products run in order, so the scores
-//     may follow the product that reads what they overwrite without a wait; two warps,
-//     because a warp's waits and commits otherwise stand between its products;
+//   * warp 16 (converged, lane 0 issuing): acc2 of a step, then the scores that take its
+//     P's region; warp 17: acc1 of a step, then the scores that take its dS's region.  A
+//     warp's products run in order, so those scores need no wait; two warps, because a
+//     warp's waits and commits otherwise stand between its products.  With two regions
+//     the one takes S of the next step, the other G; with three, the one G of the next,
+//     the other S of the step after;
 //   * warp 18 (one thread): TMA copies of X1, X2, R1 and R2;
 //   * warp 19: with keys resident, the statistics of each step's 128 queries.
 // fp16 has 5 exponent bits: P is scaled by 2^13 (P <= 1) and dS by the power of two
@@ -66,13 +68,13 @@ struct Cfg {
     static constexpr int kHalves = D / 64;
     static constexpr uint32_t kTile = kHalf * kHalves;
     static constexpr int kX1 = D == 64 ? 5 : 2, kX2 = D == 64 ? 4 : 2;  // ring slots of X1 and X2
-    static constexpr int kBufs = D == 64 ? 2 : 1;                       // buffers of S
-    static constexpr uint32_t kColAcc1 = 0, kColAcc2 = D, kColG = 2 * D, kColS = kColG + 128;  // S: + 128 per buffer
+    static constexpr int kRegions = D == 64 ? 3 : 2;  // S of step j is use 2 j of the ring, G use 2 j + 1
+    static constexpr uint32_t kColAcc1 = 0, kColAcc2 = D, kColR = 2 * D;  // regions: + 128 each
     static constexpr uint32_t kOffStat = 1024, kOffR = kOffStat + kStatSlots * kStatBytes + 1024;
     static constexpr uint32_t kOffX1 = kOffR + 2 * kTile, kOffX2 = kOffX1 + kX1 * kTile;
     static constexpr uint32_t kSmem = 1024 + kOffX2 + kX2 * kTile;  // + 1 KB alignment slack
     static_assert(kOffR % 1024 == 0, "operand tiles must be 1 KB aligned");
-    static_assert(kColS + 128 * kBufs <= 512, "tensor memory");
+    static_assert(kColR + 128 * kRegions <= 512, "tensor memory");
     static_assert(kSmem + 1024 <= 232448, "shared memory over the per-block limit");
 };
 
@@ -86,7 +88,7 @@ struct BwdArgs {
 
 struct Ctl {
     uint64_t r_full, x1_full[5], x1_empty[5], x2_full[4], x2_empty[4], st_full[kStatSlots], st_empty[kStatSlots];
-    uint64_t s_full[2], p_ready[2], g_full, d_ready, acc_full, mma_done[2];
+    uint64_t full[3], p_ready[2], d_ready[2], acc_full, mma_done[2];
     uint32_t tmem_base;
     int abort_flag, bad;
 };
@@ -325,77 +327,53 @@ __device__ __forceinline__ void sums(uint32_t d, uint32_t a, uint64_t x, uint32_
         tc_mma_f16_ts_if(d, a + 32u * (i / 2) + 8u * (i % 2), x + 128u * i, idesc, !first || i > 0, leader);
 }
 
-// acc2 of every step and S of the step kBufs later.  With queries resident there is no acc2: p_ready then only says
-// that S is read.
-template <int D, bool KEYS>
-__device__ __forceinline__ void issue_s(const BwdArgs &p, Ctl &c, uint32_t smem, uint32_t tmem, int seq_end,
-                                        const Walk &k, int lane, const Waiter &w) {
+// One of the two product warps.  FIRST: acc2 of every step (with queries resident there is none: p_ready then only says
+// that S is read) and the scores that follow in P's region; else acc1 and those that follow in dS's.
+template <int D, bool KEYS, bool FIRST>
+__device__ __forceinline__ void issue(const BwdArgs &p, Ctl &c, uint32_t smem, uint32_t tmem, int seq_end, const Walk &k,
+                                      int lane, const Waiter &w) {
     using C = Cfg<D>;
+    constexpr int R = C::kRegions;
+    constexpr bool IS_S = (R == 2) == FIRST;       // which scores this warp issues
+    constexpr int AHEAD = R == 3 && !FIRST ? 2 : 1;  // how many steps ahead of its sums
+    constexpr int NA = FIRST ? C::kX2 : C::kX1, NS = IS_S ? C::kX1 : C::kX2;
+    constexpr uint32_t ACC_X = FIRST ? C::kOffX2 : C::kOffX1, SCORE_X = IS_S ? C::kOffX1 : C::kOffX2;
+    uint64_t *acc_full = FIRST ? c.x2_full : c.x1_full, *acc_empty = FIRST ? c.x2_empty : c.x1_empty;
+    uint64_t *score_full = IS_S ? c.x1_full : c.x2_full;
+    uint64_t *ready = FIRST ? c.p_ready : c.d_ready;
     const uint32_t leader = lane == 0;
-    const uint64_t r1 = desc_k(smem + C::kOffR);
+    const uint64_t res = desc_k(smem + C::kOffR + (IS_S ? 0u : C::kTile));
     const int n = k.steps();
-    Ring<C::kX1> x1;
-    Ring<C::kX2> x2;
-    Ring<C::kBufs> buf, ahead;
+    Ring<NS> xs;  // scores' operand
+    Ring<NA> xa;  // sums' operand
     Cursor at{k.lo, 0};
-    auto next_s = [&] {
-        if (!wait_warp(su32(&c.x1_full[x1.slot]), x1.phase, w)) return false;
+    int use = IS_S ? 0 : 1, mine = FIRST ? 0 : 1;  // ring uses of the next scores and of the next sums
+    auto next_scores = [&] {
+        if (!wait_warp(su32(&score_full[xs.slot]), xs.phase, w)) return false;
         tc_after();
-        scores<D>(tmem + C::kColS + 128u * ahead.slot, r1, desc_k(smem + C::kOffX1 + (uint32_t)x1.slot * C::kTile), p.idesc1,
-                  leader);
-        tc_commit_to_if(su32(&c.s_full[ahead.slot]), leader);
-        x1.next(), ahead.next();
+        scores<D>(tmem + C::kColR + 128u * (uint32_t)(use % R), res, desc_k(smem + SCORE_X + (uint32_t)xs.slot * C::kTile),
+                  p.idesc1, leader);
+        tc_commit_to_if(su32(&c.full[use % R]), leader);
+        if (R == 2 && !IS_S) tc_commit_to_if(su32(&c.x2_empty[xs.slot]), leader);
+        xs.next();
+        use += 2;
         return true;
     };
     if (!wait_warp(su32(&c.r_full), 0, w)) return;
-    for (int j = 0; j < C::kBufs && j < n; ++j)
-        if (!next_s()) return;
-    for (int j = 0; j < n; ++j, at.next(k), buf.next(), x2.next()) {
-        if (!wait_warp(su32(&c.p_ready[buf.slot]), buf.phase, w)) return;
-        if (KEYS) {
-            if (!wait_warp(su32(&c.x2_full[x2.slot]), x2.phase, w)) return;
-            const uint32_t x = smem + C::kOffX2 + (uint32_t)x2.slot * C::kTile;
+    for (int j = 0; j < AHEAD && j < n; ++j)
+        if (!next_scores()) return;
+    for (int j = 0; j < n; ++j, at.next(k), xa.next(), mine += 2) {
+        if (!wait_warp(su32(&ready[j & 1]), (uint32_t)((j >> 1) & 1), w)) return;
+        if (KEYS || !FIRST) {
+            if (!wait_warp(su32(&acc_full[xa.slot]), xa.phase, w)) return;
+            const uint32_t x = smem + ACC_X + (uint32_t)xa.slot * C::kTile;
             if (seq_end - at.row < kRows) zero_rows(x, seq_end - at.row, kRows, C::kHalves, lane);
             tc_after();
-            sums(tmem + C::kColAcc2, tmem + C::kColS + 128u * buf.slot, desc_mn(x, kHalf, 1024u), p.idesc2, j == 0, leader);
+            sums(tmem + (FIRST ? C::kColAcc2 : C::kColAcc1), tmem + C::kColR + 128u * (uint32_t)(mine % R),
+                 desc_mn(x, kHalf, 1024u), p.idesc2, j == 0, leader);
         }
-        tc_commit_to_if(su32(&c.x2_empty[x2.slot]), leader);
-        if (j + C::kBufs < n && !next_s()) return;
-    }
-    tc_commit_to_if(su32(&c.acc_full), leader);
-}
-
-// acc1 of every step and G of the next.
-template <int D>
-__device__ __forceinline__ void issue_g(const BwdArgs &p, Ctl &c, uint32_t smem, uint32_t tmem, int seq_end,
-                                        const Walk &k, int lane, const Waiter &w) {
-    using C = Cfg<D>;
-    const uint32_t leader = lane == 0;
-    const uint64_t r2 = desc_k(smem + C::kOffR + C::kTile);
-    const int n = k.steps();
-    Ring<C::kX1> x1;
-    Ring<C::kX2> x2;
-    Cursor at{k.lo, 0};
-    auto next_g = [&] {
-        if (!wait_warp(su32(&c.x2_full[x2.slot]), x2.phase, w)) return false;
-        tc_after();
-        scores<D>(tmem + C::kColG, r2, desc_k(smem + C::kOffX2 + (uint32_t)x2.slot * C::kTile), p.idesc1, leader);
-        tc_commit_to_if(su32(&c.g_full), leader);
-        tc_commit_to_if(su32(&c.x2_empty[x2.slot]), leader);
-        x2.next();
-        return true;
-    };
-    if (!wait_warp(su32(&c.r_full), 0, w)) return;
-    if (!next_g()) return;
-    for (int j = 0; j < n; ++j, at.next(k), x1.next()) {
-        if (!wait_warp(su32(&c.d_ready), (uint32_t)(j & 1), w)) return;
-        if (!wait_warp(su32(&c.x1_full[x1.slot]), x1.phase, w)) return;
-        const uint32_t x = smem + C::kOffX1 + (uint32_t)x1.slot * C::kTile;
-        if (seq_end - at.row < kRows) zero_rows(x, seq_end - at.row, kRows, C::kHalves, lane);
-        tc_after();
-        sums(tmem + C::kColAcc1, tmem + C::kColG, desc_mn(x, kHalf, 1024u), p.idesc2, j == 0, leader);
-        tc_commit_to_if(su32(&c.x1_empty[x1.slot]), leader);
-        if (j + 1 < n && !next_g()) return;
+        tc_commit_to_if(su32(&acc_empty[xa.slot]), leader);
+        if (j + AHEAD < n && !next_scores()) return;
     }
     tc_commit_to_if(su32(&c.acc_full), leader);
 }
@@ -483,7 +461,8 @@ __device__ void role_soft(const BwdArgs &p, Ctl &c, uint32_t smem, uint32_t tmem
     const Args &a = p.a;
     const int quad = warp & 3, cols = 32 * (warp >> 2), row = u.p0 + 32 * quad + lane;
     const uint32_t lane_tm = (uint32_t)(32 * quad) << 16;
-    const uint32_t g_tm = tmem + lane_tm + C::kColG + (uint32_t)cols;
+    constexpr int R = C::kRegions;
+    const uint32_t r_tm = tmem + lane_tm + C::kColR + (uint32_t)cols;
     const float cs = a.scale * kLog2e, kappa = F16 ? sigma * 0x1p-13f : 1.f;
     float nl = 0.f, nd = 0.f;
     if (!KEYS && row < u.len) {
@@ -494,23 +473,29 @@ __device__ void role_soft(const BwdArgs &p, Ctl &c, uint32_t smem, uint32_t tmem
     const int first = a.window > 0 ? row - a.window + 1 : 0;
     const int end = a.window > 0 && row < u.len - a.window ? row + a.window : u.len;
     const int n = k.steps();
-    Ring<C::kBufs> buf;
+    Ring<R> ring;
     Ring<kStatSlots> stat;
     Cursor cur{k.lo, 0};
-    for (int j = 0; j < n; ++j, cur.next(k), buf.next(), stat.next()) {
+    for (int j = 0; j < n; ++j, cur.next(k), stat.next()) {
         const int base = cur.row + cols;
         const int from = (KEYS ? row : first) - base, to = (KEYS ? end - 1 : row) - base;
         const bool whole = KEYS ? base >= u.p0 + kRows - 1 && base + 32 <= u.len &&
                                       (a.window == 0 || base + 31 < u.p0 + a.window)
                                 : base + 31 <= u.p0 && (a.window == 0 || u.p0 + kRows - 1 < base + a.window);
         const uint32_t st = smem + 1024u + (uint32_t)stat.slot * kStatBytes + 8u * (uint32_t)cols;
-        const uint32_t s_tm = tmem + lane_tm + C::kColS + 128u * (uint32_t)buf.slot + (uint32_t)cols;
         uint32_t pv[32], gv[32], pk[16];
         if (KEYS && !wait_warp(su32(&c.st_full[stat.slot]), stat.phase, w)) return;
-        if (!wait_warp(su32(&c.s_full[buf.slot]), buf.phase, w)) return;
+        if (!wait_warp(su32(&c.full[ring.slot]), ring.phase, w)) return;
         tc_after();
+        const uint32_t s_tm = r_tm + 128u * (uint32_t)ring.slot;
+        ring.next();
         tc_ld_32x32(s_tm, pv);
         tc_wait_ld(pv);
+        if (!KEYS) {  // S is read, and no P goes in its place
+            tc_before();
+            __syncwarp();
+            if (lane == 0) bar_arrive(su32(&c.p_ready[j & 1]));
+        }
         if (whole)
             probs32<F16, KEYS, false>(pv, cs, st, nl, 0, 0, pk);
         else
@@ -518,12 +503,14 @@ __device__ void role_soft(const BwdArgs &p, Ctl &c, uint32_t smem, uint32_t tmem
         if (KEYS) {
             tc_st_32x16(s_tm, pk);
             tc_wait_st();
+            tc_before();
+            __syncwarp();
+            if (lane == 0) bar_arrive(su32(&c.p_ready[j & 1]));
         }
-        tc_before();
-        __syncwarp();
-        if (lane == 0) bar_arrive(su32(&c.p_ready[buf.slot]));
-        if (!wait_warp(su32(&c.g_full), (uint32_t)(j & 1), w)) return;
+        if (!wait_warp(su32(&c.full[ring.slot]), ring.phase, w)) return;
         tc_after();
+        const uint32_t g_tm = r_tm + 128u * (uint32_t)ring.slot;
+        ring.next();
         tc_ld_32x32(g_tm, gv);
         tc_wait_ld(gv);
         if (whole)
@@ -535,7 +522,7 @@ __device__ void role_soft(const BwdArgs &p, Ctl &c, uint32_t smem, uint32_t tmem
         tc_before();
         __syncwarp();
         if (lane == 0) {
-            bar_arrive(su32(&c.d_ready));
+            bar_arrive(su32(&c.d_ready[j & 1]));
             if (KEYS) bar_arrive(su32(&c.st_empty[stat.slot]));
         }
     }
@@ -641,9 +628,9 @@ __device__ __forceinline__ void unit_body(const BwdArgs &p, Ctl &c, uint32_t sme
         const uint32_t sm = uniform(smem), tm = uniform(tmem);
         const Walk ku{uniform(k.lo), uniform(k.hi), uniform(k.heads)};
         if (second)
-            issue_g<D>(p, c, sm, tm, uniform(u.len), ku, lane, w);
+            issue<D, KEYS, false>(p, c, sm, tm, uniform(u.len), ku, lane, w);
         else
-            issue_s<D, KEYS>(p, c, sm, tm, uniform(u.len), ku, lane, w);
+            issue<D, KEYS, true>(p, c, sm, tm, uniform(u.len), ku, lane, w);
         tc_commit_to_if(su32(&c.mma_done[second]), lane == 0);  // nothing may still run when tensor memory is released
         drain(su32(&c.mma_done[second]), 0, w);
         __syncwarp();
@@ -674,18 +661,17 @@ __global__ void __launch_bounds__(kThreads, 1) backward_tc_kernel(const __grid_c
         }
         for (int s = 0; s < 4; ++s) {
             bar_init(su32(&c.x2_full[s]), 1);
-            bar_init(su32(&c.x2_empty[s]), 2);  // G and acc2
+            bar_init(su32(&c.x2_empty[s]), C::kRegions == 2 ? 2 : 1);  // G and acc2, of two warps or of one
         }
         for (int s = 0; s < kStatSlots; ++s) {
             bar_init(su32(&c.st_full[s]), 1);
             bar_init(su32(&c.st_empty[s]), kSoftWarps);
         }
+        for (int i = 0; i < 3; ++i) bar_init(su32(&c.full[i]), 1);
         for (int i = 0; i < 2; ++i) {
-            bar_init(su32(&c.s_full[i]), 1);
             bar_init(su32(&c.p_ready[i]), kSoftWarps);
+            bar_init(su32(&c.d_ready[i]), kSoftWarps);
         }
-        bar_init(su32(&c.g_full), 1);
-        bar_init(su32(&c.d_ready), kSoftWarps);
         bar_init(su32(&c.acc_full), 2);
         bar_init(su32(&c.mma_done[0]), 1);
         bar_init(su32(&c.mma_done[1]), 1);
