@@ -23,7 +23,7 @@
 // next scores, its dS is formed, and the other way round.
 //   * warps 0-15: P, then dS, 32 columns of one resident row per thread; at the end dK /
 //     dQ (warps 0-7) and dV (8-15);
-//   * warp 16 (converged, lane 0 issuing): acc2 of a step, then the scores that take its
+//   * warp 16 (one lane issuing): acc2 of a step, then the scores that take its
 //     P's region; warp 17: acc1 of a step, then the scores that take its dS's region.  A
 //     warp's products run in order, so those scores need no wait; two warps, because a
 //     warp's waits and commits otherwise stand between its products.  With two regions
@@ -311,20 +311,20 @@ __device__ void role_stats(const BwdArgs &p, Ctl &c, uint32_t smem, const Unit &
     }
 }
 
-// D / 16 products a . b^T of [128][D] tiles (K-major) into 128 columns at `d`.
+// D / 16 products a . b^T of [128][D] tiles (K-major) into 128 columns at `d`: one lane.
 template <int D>
-__device__ __forceinline__ void scores(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t leader) {
+__device__ __forceinline__ void scores(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc) {
 #pragma unroll
     for (int i = 0; i < D / 16; ++i) {  // +32 bytes of each row, then the next half
         const uint64_t off = 2u * (i % 4) + (uint64_t)(i / 4) * (kHalf >> 4);
-        tc_mma_f16_if(d, a + off, b + off, idesc, i > 0, leader);
+        tc_mma_f16(d, a + off, b + off, idesc, i > 0);
     }
 }
-// 8 products of P or dS (16 columns at every 32 from `a`) and 128 rows of X, added to D columns at `d`.
-__device__ __forceinline__ void sums(uint32_t d, uint32_t a, uint64_t x, uint32_t idesc, bool first, uint32_t leader) {
+// 8 products of P or dS (16 columns at every 32 from `a`) and 128 rows of X, added to D columns at `d`: one lane.
+__device__ __forceinline__ void sums(uint32_t d, uint32_t a, uint64_t x, uint32_t idesc, bool first) {
 #pragma unroll
     for (int i = 0; i < kRows / 16; ++i)
-        tc_mma_f16_ts_if(d, a + 32u * (i / 2) + 8u * (i % 2), x + 128u * i, idesc, !first || i > 0, leader);
+        tc_mma_f16_ts(d, a + 32u * (i / 2) + 8u * (i % 2), x + 128u * i, idesc, !first || i > 0);
 }
 
 // One of the two product warps.  FIRST: acc2 of every step (with queries resident there is none: p_ready then only says
@@ -341,7 +341,6 @@ __device__ __forceinline__ void issue(const BwdArgs &p, Ctl &c, uint32_t smem, u
     uint64_t *acc_full = FIRST ? c.x2_full : c.x1_full, *acc_empty = FIRST ? c.x2_empty : c.x1_empty;
     uint64_t *score_full = IS_S ? c.x1_full : c.x2_full;
     uint64_t *ready = FIRST ? c.p_ready : c.d_ready;
-    const uint32_t leader = lane == 0;
     const uint64_t res = desc_k(smem + C::kOffR + (IS_S ? 0u : C::kTile));
     const int n = k.steps();
     Ring<NS> xs;  // scores' operand
@@ -351,10 +350,12 @@ __device__ __forceinline__ void issue(const BwdArgs &p, Ctl &c, uint32_t smem, u
     auto next_scores = [&] {
         if (!wait_warp(su32(&score_full[xs.slot]), xs.phase, w)) return false;
         tc_after();
-        scores<D>(tmem + C::kColR + 128u * (uint32_t)(use % R), res, desc_k(smem + SCORE_X + (uint32_t)xs.slot * C::kTile),
-                  p.idesc1, leader);
-        tc_commit_to_if(su32(&c.full[use % R]), leader);
-        if (R == 2 && !IS_S) tc_commit_to_if(su32(&c.x2_empty[xs.slot]), leader);
+        if (elect_one()) {
+            scores<D>(tmem + C::kColR + 128u * (uint32_t)(use % R), res,
+                      desc_k(smem + SCORE_X + (uint32_t)xs.slot * C::kTile), p.idesc1);
+            tc_commit_to(su32(&c.full[use % R]));
+            if (R == 2 && !IS_S) tc_commit_to(su32(&c.x2_empty[xs.slot]));
+        }
         xs.next();
         use += 2;
         return true;
@@ -369,13 +370,14 @@ __device__ __forceinline__ void issue(const BwdArgs &p, Ctl &c, uint32_t smem, u
             const uint32_t x = smem + ACC_X + (uint32_t)xa.slot * C::kTile;
             if (seq_end - at.row < kRows) zero_rows(x, seq_end - at.row, kRows, C::kHalves, lane);
             tc_after();
-            sums(tmem + (FIRST ? C::kColAcc2 : C::kColAcc1), tmem + C::kColR + 128u * (uint32_t)(mine % R),
-                 desc_mn(x, kHalf, 1024u), p.idesc2, j == 0, leader);
+            if (elect_one())
+                sums(tmem + (FIRST ? C::kColAcc2 : C::kColAcc1), tmem + C::kColR + 128u * (uint32_t)(mine % R),
+                     desc_mn(x, kHalf, 1024u), p.idesc2, j == 0);
         }
-        tc_commit_to_if(su32(&acc_empty[xa.slot]), leader);
+        if (elect_one()) tc_commit_to(su32(&acc_empty[xa.slot]));
         if (j + AHEAD < n && !next_scores()) return;
     }
-    tc_commit_to_if(su32(&c.acc_full), leader);
+    if (elect_one()) tc_commit_to(su32(&c.acc_full));
 }
 
 // P of 32 columns from this row's scores; columns outside [from, to] are masked when MASK.  With KEYS the statistic is
@@ -631,7 +633,7 @@ __device__ __forceinline__ void unit_body(const BwdArgs &p, Ctl &c, uint32_t sme
             issue<D, KEYS, false>(p, c, sm, tm, uniform(u.len), ku, lane, w);
         else
             issue<D, KEYS, true>(p, c, sm, tm, uniform(u.len), ku, lane, w);
-        tc_commit_to_if(su32(&c.mma_done[second]), lane == 0);  // nothing may still run when tensor memory is released
+        if (elect_one()) tc_commit_to(su32(&c.mma_done[second]));  // nothing may still run when tensor memory is released
         drain(su32(&c.mma_done[second]), 0, w);
         __syncwarp();
     } else if (warp < kStatWarp) {

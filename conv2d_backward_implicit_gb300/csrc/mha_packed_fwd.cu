@@ -17,7 +17,7 @@
 //     maximum m_i that scales P and O may lag the true one: O and the sum are rescaled
 //     only when it grew by more than 2^8 (P stays below 2^8, far from fp16's limit), so
 //     most blocks skip the pass over O.  The true maximum is kept beside it for LSE.
-//   * warp 8 (converged, lane 0 issuing): per key block PV_0, S_0 of the next block,
+//   * warp 8 (one lane issuing): per key block PV_0, S_0 of the next block,
 //     PV_1, S_1 of the next: while one tile's products run, the other's softmax does.
 //     The products of one thread run in order, so S_i may overwrite P_i behind PV_i.
 //   * warps 9 and 10 (one thread each): TMA copies of K (and Q tile 0) and V (and Q
@@ -122,7 +122,7 @@ template <int D>
 __device__ __forceinline__ void issue_products(const FwdArgs &p, Ctl &c, uint32_t smem_, uint32_t tmem_, int len,
                                                const Tile (&t)[2], int lo_, int hi_, int lane, const Waiter &w) {
     using C = Cfg<D>;
-    const uint32_t leader = lane == 0, smem = uniform(smem_), tmem = uniform(tmem_);
+    const uint32_t smem = uniform(smem_), tmem = uniform(tmem_);
     const int lo = uniform(lo_), hi = uniform(hi_), seq_end = uniform(len);
     const int first[2] = {uniform(t[0].lo), uniform(t[1].lo)}, end[2] = {uniform(t[0].hi), uniform(t[1].hi)};
     int phase[2] = {0, 0};  // products PV issued of each tile
@@ -145,28 +145,34 @@ __device__ __forceinline__ void issue_products(const FwdArgs &p, Ctl &c, uint32_
                 if (!wait_warp(su32(&c.p_ready[i]), (uint32_t)(phase[i] & 1), w)) return;
                 tc_after();
                 const uint64_t vd = desc_mn(smem + C::kOffV + (uint32_t)vs * C::kTile, kHalf, 1024u);
+                if (elect_one()) {
 #pragma unroll
-                for (int k = 0; k < 8; ++k)  // A: 8 columns (16 keys) per step; B: two groups of 8 keys (2 KB)
-                    tc_mma_f16_ts_if(tmem + kColO + 128u * i, tmem + kColS + 128u * i + 8u * k, vd + 128u * k, p.idesc2,
-                                     phase[i] > 0 || k > 0, leader);
+                    for (int k = 0; k < 8; ++k)  // A: 8 columns (16 keys) per step; B: two groups of 8 keys (2 KB)
+                        tc_mma_f16_ts(tmem + kColO + 128u * i, tmem + kColS + 128u * i + 8u * k, vd + 128u * k, p.idesc2,
+                                      phase[i] > 0 || k > 0);
+                    if (b + 1 == first[i]) tc_commit_to(su32(&c.o_full[i]));
+                }
                 ++phase[i];
-                if (b + 1 == first[i]) tc_commit_to_if(su32(&c.o_full[i]), leader);
             }
             if (more && b >= first[i] && b < end[i]) {
                 if (!q_seen[i] && !wait_warp(su32(&c.q_full[i]), 0, w)) return;
                 q_seen[i] = true;
                 const uint64_t qd = desc_k(smem + C::kOffQ + (uint32_t)i * C::kTile);
                 const uint64_t kd = desc_k(smem + C::kOffK + (uint32_t)ks * C::kTile);
+                if (elect_one()) {
 #pragma unroll
-                for (int k = 0; k < D / 16; ++k) {  // +32 bytes of each row, then the next half
-                    const uint64_t step = 2u * (k % 4) + (uint64_t)(k / 4) * (kHalf >> 4);
-                    tc_mma_f16_if(tmem + kColS + 128u * i, qd + step, kd + step, p.idesc1, k > 0, leader);
+                    for (int k = 0; k < D / 16; ++k) {  // +32 bytes of each row, then the next half
+                        const uint64_t step = 2u * (k % 4) + (uint64_t)(k / 4) * (kHalf >> 4);
+                        tc_mma_f16(tmem + kColS + 128u * i, qd + step, kd + step, p.idesc1, k > 0);
+                    }
+                    tc_commit_to(su32(&c.s_full[i]));
                 }
-                tc_commit_to_if(su32(&c.s_full[i]), leader);
             }
         }
-        if (prev) tc_commit_to_if(su32(&c.v_empty[vs]), leader);
-        if (more) tc_commit_to_if(su32(&c.k_empty[ks]), leader);
+        if (elect_one()) {
+            if (prev) tc_commit_to(su32(&c.v_empty[vs]));
+            if (more) tc_commit_to(su32(&c.k_empty[ks]));
+        }
     }
 }
 
@@ -174,7 +180,7 @@ template <int D>
 __device__ void role_mma(const FwdArgs &p, Ctl &c, uint32_t smem, uint32_t tmem, const Unit &u, const Tile (&t)[2],
                          int lo, int hi, int lane, const Waiter &w) {
     issue_products<D>(p, c, smem, tmem, u.len, t, lo, hi, lane, w);
-    tc_commit_to_if(su32(&c.mma_done), lane == 0);  // nothing may still run when tensor memory is released
+    if (elect_one()) tc_commit_to(su32(&c.mma_done));  // nothing may still run when tensor memory is released
     drain(su32(&c.mma_done), 0, w);
     __syncwarp();
 }

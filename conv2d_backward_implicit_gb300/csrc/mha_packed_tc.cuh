@@ -77,11 +77,18 @@ __device__ __forceinline__ uint32_t pack2(float a, float b) {
     }
 }
 
-// The same value in every lane, and known to be: what depends on it stays in the warp's uniform registers, from which
-// the tensor-core instructions take their descriptors and addresses.
-template <typename T>
-__device__ __forceinline__ T uniform(T x) {
-    return __shfl_sync(0xffffffffu, x, 0);
+// The same value in every lane, and known to be: a warp reduction's result lies in a uniform register, and what
+// depends on it can stay there, where the tensor-core instructions take their descriptors and addresses from.
+__device__ __forceinline__ uint32_t uniform(uint32_t x) { return __reduce_max_sync(0xffffffffu, x); }
+__device__ __forceinline__ int uniform(int x) { return (int)__reduce_max_sync(0xffffffffu, (unsigned)x); }
+
+// True in one lane of a converged warp, the same one each time.  Products and commits are issued under this branch: it is
+// the form in which one takes its execution time (M128 K16, operands in shared memory: N128 65, N64 50 cycles; A in
+// tensor memory: 63, 33), where a predicate on the lane number costs 76 at least.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+    return p != 0;
 }
 
 __device__ __forceinline__ bool finite(float x) { return fabsf(x) <= 3.402823466e38f; }
