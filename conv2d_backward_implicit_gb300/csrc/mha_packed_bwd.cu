@@ -15,7 +15,8 @@
 //                                 tensor memory, X as the MN-major operand
 // so scores are formed twice (7 products in place of 5), and in return every gradient
 // is one block's sum in a fixed order: no atomics, nothing to zero or convert after.
-// Tensor memory: acc1 and acc2 (D columns each), and a ring of two (D = 128) or three
+// Tensor memory: acc1 and acc2 (D columns each; with queries resident, R1 and R2 in
+// acc2's place, the scores' A operand), and a ring of two (D = 128) or three
 // regions of 128 columns that takes S and G of step after step in turn, with P and dS
 // over the first 16 of each 32.  Steps of 128 columns because a product of N = 64 takes
 // nearly as long as one of N = 128 (65 against 75 cycles); what overlaps is then not two
@@ -87,7 +88,7 @@ struct BwdArgs {
 };
 
 struct Ctl {
-    uint64_t r_full, x1_full[5], x1_empty[5], x2_full[4], x2_empty[4], st_full[kStatSlots], st_empty[kStatSlots];
+    uint64_t r_full, r_ready, x1_full[5], x1_empty[5], x2_full[4], x2_empty[4], st_full[kStatSlots], st_empty[kStatSlots];
     uint64_t full[3], p_ready[2], d_ready[2], acc_full, mma_done[2];
     uint32_t tmem_base;
     int abort_flag, bad;
@@ -284,7 +285,7 @@ __device__ void role_load(const BwdArgs &p, Ctl &c, uint32_t smem, const Unit &u
         drain(su32(&c.x2_full[q % C::kX2]), (uint32_t)((q / C::kX2) & 1), w);
 }
 
-// Statistics of each step's 128 queries: per pair of columns (-stat, -stat, -delta, -delta).
+// Statistics of each step's 128 queries: -stat of all, then -delta of all.
 template <bool F16>
 __device__ void role_stats(const BwdArgs &p, Ctl &c, uint32_t smem, const Unit &u, const Walk &k, int g, float kappa,
                            int lane, const Waiter &w) {
@@ -297,27 +298,31 @@ __device__ void role_stats(const BwdArgs &p, Ctl &c, uint32_t smem, const Unit &
         float2 x[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const int col = at.row + 64 * (i >> 1) + 2 * lane + (i & 1);
+            const int col = at.row + 4 * lane + i;
             x[i] = col < u.len ? __ldg(st + col) : make_float2(0.f, 0.f);
         }
         if (!wait_warp(su32(&c.st_empty[ring.slot]), ring.phase ^ 1u, w)) return;
-#pragma unroll
-        for (int i = 0; i < 4; i += 2)
-            sts128(smem + 1024u + (uint32_t)ring.slot * kStatBytes + (uint32_t)i * 256u + (uint32_t)lane * 16u,
-                   __float_as_uint(shift - x[i].x), __float_as_uint(shift - x[i + 1].x),
-                   __float_as_uint(-x[i].y * kappa), __float_as_uint(-x[i + 1].y * kappa));
+        const uint32_t dst = smem + 1024u + (uint32_t)ring.slot * kStatBytes + (uint32_t)lane * 16u;
+        sts128(dst, __float_as_uint(shift - x[0].x), __float_as_uint(shift - x[1].x), __float_as_uint(shift - x[2].x),
+               __float_as_uint(shift - x[3].x));
+        sts128(dst + 512u, __float_as_uint(-x[0].y * kappa), __float_as_uint(-x[1].y * kappa),
+               __float_as_uint(-x[2].y * kappa), __float_as_uint(-x[3].y * kappa));
         __syncwarp();
         if (lane == 0) bar_arrive(su32(&c.st_full[ring.slot]));
     }
 }
 
-// D / 16 products a . b^T of [128][D] tiles (K-major) into 128 columns at `d`: one lane.
-template <int D>
+// D / 16 products a . b^T of [128][D] tiles (b K-major in shared memory; a the same, or TM: in tensor memory) into 128
+// columns at `d`: one lane.
+template <int D, bool TM>
 __device__ __forceinline__ void scores(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc) {
 #pragma unroll
     for (int i = 0; i < D / 16; ++i) {  // +32 bytes of each row, then the next half
         const uint64_t off = 2u * (i % 4) + (uint64_t)(i / 4) * (kHalf >> 4);
-        tc_mma_f16(d, a + off, b + off, idesc, i > 0);
+        if (TM)
+            tc_mma_f16_ts(d, (uint32_t)a + 8u * i, b + off, idesc, i > 0);
+        else
+            tc_mma_f16(d, a + off, b + off, idesc, i > 0);
     }
 }
 // 8 products of P or dS (16 columns at every 32 from `a`) and 128 rows of X, added to D columns at `d`: one lane.
@@ -341,7 +346,8 @@ __device__ __forceinline__ void issue(const BwdArgs &p, Ctl &c, uint32_t smem, u
     uint64_t *acc_full = FIRST ? c.x2_full : c.x1_full, *acc_empty = FIRST ? c.x2_empty : c.x1_empty;
     uint64_t *score_full = IS_S ? c.x1_full : c.x2_full;
     uint64_t *ready = FIRST ? c.p_ready : c.d_ready;
-    const uint64_t res = desc_k(smem + C::kOffR + (IS_S ? 0u : C::kTile));
+    const uint64_t res = KEYS ? desc_k(smem + C::kOffR + (IS_S ? 0u : C::kTile))
+                              : (uint64_t)(tmem + C::kColAcc2 + (IS_S ? 0u : D / 2u));
     const int n = k.steps();
     Ring<NS> xs;  // scores' operand
     Ring<NA> xa;  // sums' operand
@@ -351,7 +357,7 @@ __device__ __forceinline__ void issue(const BwdArgs &p, Ctl &c, uint32_t smem, u
         if (!wait_warp(su32(&score_full[xs.slot]), xs.phase, w)) return false;
         tc_after();
         if (elect_one()) {
-            scores<D>(tmem + C::kColR + 128u * (uint32_t)(use % R), res,
+            scores<D, !KEYS>(tmem + C::kColR + 128u * (uint32_t)(use % R), res,
                       desc_k(smem + SCORE_X + (uint32_t)xs.slot * C::kTile), p.idesc1);
             tc_commit_to(su32(&c.full[use % R]));
             if (R == 2 && !IS_S) tc_commit_to(su32(&c.x2_empty[xs.slot]));
@@ -360,7 +366,7 @@ __device__ __forceinline__ void issue(const BwdArgs &p, Ctl &c, uint32_t smem, u
         use += 2;
         return true;
     };
-    if (!wait_warp(su32(&c.r_full), 0, w)) return;
+    if (!wait_warp(su32(KEYS ? &c.r_full : &c.r_ready), 0, w)) return;
     for (int j = 0; j < AHEAD && j < n; ++j)
         if (!next_scores()) return;
     for (int j = 0; j < n; ++j, at.next(k), xa.next(), mine += 2) {
@@ -380,44 +386,60 @@ __device__ __forceinline__ void issue(const BwdArgs &p, Ctl &c, uint32_t smem, u
     if (elect_one()) tc_commit_to(su32(&c.acc_full));
 }
 
-// P of 32 columns from this row's scores; columns outside [from, to] are masked when MASK.  With KEYS the statistic is
-// per column at shared address `st`, else nl of the row.
+// P of 32 columns from this row's scores; with MASK, columns whose bit of `keep` is 0 are masked.  With KEYS the
+// statistics are per column at shared address `st`, else nl of the row.
 template <bool F16, bool KEYS, bool MASK>
-__device__ __forceinline__ void probs32(uint32_t (&s)[32], float cs, uint32_t st, float nl, int from, int to,
+__device__ __forceinline__ void probs32(uint32_t (&s)[32], float cs, uint32_t st, float nl, uint32_t keep,
                                         uint32_t (&pp)[16]) {
     const float2 c2 = make_float2(cs, cs);
-    float2 l2 = make_float2(nl, nl);
 #pragma unroll
-    for (int e = 0; e < 32; e += 2) {
-        if (KEYS)
-            asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(l2.x), "=f"(l2.y) : "r"(st + (uint32_t)e * 8u) : "memory");
-        const float2 x = __ffma2_rn(make_float2(__uint_as_float(s[e]), __uint_as_float(s[e + 1])), c2, l2);
-        float2 y = make_float2(fast_exp2(x.x), fast_exp2(x.y));
-        if (MASK) {
-            if (e < from || e > to) y.x = 0.f;
-            if (e + 1 < from || e + 1 > to) y.y = 0.f;
+    for (int e = 0; e < 32; e += 4) {
+        float2 l2[2] = {make_float2(nl, nl), make_float2(nl, nl)};
+        if (KEYS) {
+            const uint4 x = lds128(st + (uint32_t)e * 4u);
+            l2[0] = make_float2(__uint_as_float(x.x), __uint_as_float(x.y));
+            l2[1] = make_float2(__uint_as_float(x.z), __uint_as_float(x.w));
         }
-        if (KEYS) pp[e >> 1] = pack2<F16>(y.x, y.y);
-        s[e] = __float_as_uint(y.x), s[e + 1] = __float_as_uint(y.y);
+#pragma unroll
+        for (int z = 0; z < 2; ++z) {
+            const int i = e + 2 * z;
+            const float2 x = __ffma2_rn(make_float2(__uint_as_float(s[i]), __uint_as_float(s[i + 1])), c2, l2[z]);
+            float2 y = make_float2(fast_exp2(x.x), fast_exp2(x.y));
+            if (MASK) {
+                if (!(keep >> i & 1u)) y.x = 0.f;
+                if (!(keep >> (i + 1) & 1u)) y.y = 0.f;
+            }
+            if (KEYS) pp[i >> 1] = pack2<F16>(y.x, y.y);
+            s[i] = __float_as_uint(y.x), s[i + 1] = __float_as_uint(y.y);
+        }
     }
 }
-// dS = P (G - delta) of 32 columns: p as probs32 leaves it.  A masked column's P is 0, its G may be anything.
+// dS = P (G - delta) of 32 columns: p as probs32 leaves it, 0 where masked.  With MASK, columns whose bit of `keep` is 0
+// get 0 whatever their G: those past the sequence's end, which hold other sequences' rows.  (A masked column inside the
+// sequence whose G is not finite makes a NaN, and its tile is recomputed.)
 template <bool F16, bool KEYS, bool MASK>
 __device__ __forceinline__ void grads32(const uint32_t (&p)[32], const uint32_t (&g)[32], float kappa, uint32_t st,
-                                        float nd, int from, int to, uint32_t (&pd)[16]) {
+                                        float nd, uint32_t keep, uint32_t (&pd)[16]) {
     const float2 k2 = make_float2(kappa, kappa);
-    float2 d2 = make_float2(nd, nd);
 #pragma unroll
-    for (int e = 0; e < 32; e += 2) {
-        if (KEYS)
-            asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(d2.x), "=f"(d2.y) : "r"(st + (uint32_t)e * 8u + 8u) : "memory");
-        const float2 z = __ffma2_rn(make_float2(__uint_as_float(g[e]), __uint_as_float(g[e + 1])), k2, d2);
-        float2 d = __fmul2_rn(make_float2(__uint_as_float(p[e]), __uint_as_float(p[e + 1])), z);
-        if (MASK) {
-            if (e < from || e > to) d.x = 0.f;
-            if (e + 1 < from || e + 1 > to) d.y = 0.f;
+    for (int e = 0; e < 32; e += 4) {
+        float2 d2[2] = {make_float2(nd, nd), make_float2(nd, nd)};
+        if (KEYS) {
+            const uint4 x = lds128(st + 512u + (uint32_t)e * 4u);
+            d2[0] = make_float2(__uint_as_float(x.x), __uint_as_float(x.y));
+            d2[1] = make_float2(__uint_as_float(x.z), __uint_as_float(x.w));
         }
-        pd[e >> 1] = pack2<F16>(d.x, d.y);
+#pragma unroll
+        for (int z = 0; z < 2; ++z) {
+            const int i = e + 2 * z;
+            const float2 x = __ffma2_rn(make_float2(__uint_as_float(g[i]), __uint_as_float(g[i + 1])), k2, d2[z]);
+            float2 d = __fmul2_rn(make_float2(__uint_as_float(p[i]), __uint_as_float(p[i + 1])), x);
+            if (MASK) {
+                if (!(keep >> i & 1u)) d.x = 0.f;
+                if (!(keep >> (i + 1) & 1u)) d.y = 0.f;
+            }
+            pd[i >> 1] = pack2<F16>(d.x, d.y);
+        }
     }
 }
 
@@ -471,6 +493,30 @@ __device__ void role_soft(const BwdArgs &p, Ctl &c, uint32_t smem, uint32_t tmem
         const float2 st = __ldg(a.stats + (int64_t)head * a.tokens + u.begin + row);
         nl = (F16 ? kPShift : 0.f) - st.x, nd = -st.y * kappa;
     }
+    if (!KEYS) {
+        // Q and dO of this thread's row go to tensor memory, where acc2 would be: as the A operand they then cost shared
+        // memory no reads (the scores' operands in shared memory alone would keep it busy for as long as the products).
+        const int which = warp >> 3, part = (warp >> 2) & 1;  // R1 or R2, half of its columns
+        if (!wait_warp(su32(&c.r_full), 0, w)) return;
+        const uint32_t r = (uint32_t)(32 * quad + lane);
+        const uint32_t src = smem + C::kOffR + (uint32_t)which * C::kTile + (D == 128 ? (uint32_t)part * kHalf : 0u) + r * 128u;
+        const uint32_t dst = tmem + lane_tm + C::kColAcc2 + (uint32_t)(which * (D / 2) + part * (D / 4));
+#pragma unroll
+        for (int b = 0; b < D / 64; ++b) {
+            uint32_t v[16];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const uint32_t chunk = (uint32_t)(4 * b + i + (D == 64 ? 4 * part : 0));
+                const uint4 x = lds128(src + ((chunk ^ (r & 7u)) << 4));
+                v[4 * i] = x.x, v[4 * i + 1] = x.y, v[4 * i + 2] = x.z, v[4 * i + 3] = x.w;
+            }
+            tc_st_32x16(dst + 16 * b, v);
+        }
+        tc_wait_st();
+        tc_before();
+        __syncwarp();
+        if (lane == 0) bar_arrive(su32(&c.r_ready));
+    }
     // The rows that this one meets: queries [row, end) with keys resident, else keys [first, row].
     const int first = a.window > 0 ? row - a.window + 1 : 0;
     const int end = a.window > 0 && row < u.len - a.window ? row + a.window : u.len;
@@ -484,7 +530,7 @@ __device__ void role_soft(const BwdArgs &p, Ctl &c, uint32_t smem, uint32_t tmem
         const bool whole = KEYS ? base >= u.p0 + kRows - 1 && base + 32 <= u.len &&
                                       (a.window == 0 || base + 31 < u.p0 + a.window)
                                 : base + 31 <= u.p0 && (a.window == 0 || u.p0 + kRows - 1 < base + a.window);
-        const uint32_t st = smem + 1024u + (uint32_t)stat.slot * kStatBytes + 8u * (uint32_t)cols;
+        const uint32_t keep = bits_between(from, to), st = smem + 1024u + (uint32_t)stat.slot * kStatBytes + 4u * (uint32_t)cols;
         uint32_t pv[32], gv[32], pk[16];
         if (KEYS && !wait_warp(su32(&c.st_full[stat.slot]), stat.phase, w)) return;
         if (!wait_warp(su32(&c.full[ring.slot]), ring.phase, w)) return;
@@ -499,9 +545,9 @@ __device__ void role_soft(const BwdArgs &p, Ctl &c, uint32_t smem, uint32_t tmem
             if (lane == 0) bar_arrive(su32(&c.p_ready[j & 1]));
         }
         if (whole)
-            probs32<F16, KEYS, false>(pv, cs, st, nl, 0, 0, pk);
+            probs32<F16, KEYS, false>(pv, cs, st, nl, keep, pk);
         else
-            probs32<F16, KEYS, true>(pv, cs, st, nl, from, to, pk);
+            probs32<F16, KEYS, true>(pv, cs, st, nl, keep, pk);
         if (KEYS) {
             tc_st_32x16(s_tm, pk);
             tc_wait_st();
@@ -515,10 +561,10 @@ __device__ void role_soft(const BwdArgs &p, Ctl &c, uint32_t smem, uint32_t tmem
         ring.next();
         tc_ld_32x32(g_tm, gv);
         tc_wait_ld(gv);
-        if (whole)
-            grads32<F16, KEYS, false>(pv, gv, kappa, st, nd, 0, 0, pk);
+        if (base + 32 <= u.len)
+            grads32<F16, KEYS, false>(pv, gv, kappa, st, nd, keep, pk);
         else
-            grads32<F16, KEYS, true>(pv, gv, kappa, st, nd, from, to, pk);
+            grads32<F16, KEYS, true>(pv, gv, kappa, st, nd, keep, pk);
         tc_st_32x16(g_tm, pk);
         tc_wait_st();
         tc_before();
@@ -657,6 +703,7 @@ __global__ void __launch_bounds__(kThreads, 1) backward_tc_kernel(const __grid_c
     const int warp = uniform((int)(threadIdx.x >> 5)), lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
         bar_init(su32(&c.r_full), 2);
+        bar_init(su32(&c.r_ready), kSoftWarps);
         for (int s = 0; s < 5; ++s) {
             bar_init(su32(&c.x1_full[s]), 1);
             bar_init(su32(&c.x1_empty[s]), 1);

@@ -187,9 +187,10 @@ __device__ void role_mma(const FwdArgs &p, Ctl &c, uint32_t smem, uint32_t tmem,
 
 // 32 scores of one row, keys base .. base + 31: those outside [from, to] (relative to base) become -inf.
 __device__ __forceinline__ void mask32(uint32_t (&v)[32], int from, int to) {
+    const uint32_t keep = bits_between(from, to);
 #pragma unroll
     for (int e = 0; e < 32; ++e)
-        if (e < from || e > to) v[e] = 0xFF800000u;
+        if (!(keep >> e & 1u)) v[e] = 0xFF800000u;
 }
 __device__ __forceinline__ float max32(const uint32_t (&v)[32], float m) {
 #pragma unroll

@@ -65,6 +65,13 @@ __device__ __forceinline__ float fast_exp2(float x) {  // the SFU's 2^x
     return y;
 }
 
+// Bits e of 32 with from <= e <= to.
+__device__ __forceinline__ uint32_t bits_between(int from, int to) {
+    const uint32_t above = from <= 0 ? 0xffffffffu : (from > 31 ? 0u : 0xffffffffu << from);
+    const uint32_t below = to >= 31 ? 0xffffffffu : (to < 0 ? 0u : 0xffffffffu >> (31 - to));
+    return above & below;
+}
+
 // Two floats rounded to a pair of the input type (low half first).
 template <bool F16>
 __device__ __forceinline__ uint32_t pack2(float a, float b) {
