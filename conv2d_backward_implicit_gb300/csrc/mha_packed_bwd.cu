@@ -28,8 +28,10 @@
 //     P's region; warp 17: acc1 of a step, then the scores that take its dS's region.  A
 //     warp's products run in order, so those scores need no wait; two warps, because a
 //     warp's waits and commits otherwise stand between its products.  With two regions
-//     the one takes S of the next step, the other G; with three, the one G of the next,
-//     the other S of the step after;
+//     the one takes S of the next step, the other G, and the second warp lets the first
+//     go ahead: products of two warps share the tensor core evenly, and both scores would
+//     come at the end of the step, with nothing to overlap the next P.  With three, the
+//     one takes G of the next step, the other S of the step after;
 //   * warp 18 (one thread): TMA copies of X1, X2, R1 and R2;
 //   * warp 19: with keys resident, the statistics of each step's 128 queries.
 // fp16 has 5 exponent bits: P is scaled by 2^13 (P <= 1) and dS by the power of two
@@ -68,15 +70,17 @@ template <int D>
 struct Cfg {
     static constexpr int kHalves = D / 64;
     static constexpr uint32_t kTile = kHalf * kHalves;
-    static constexpr int kX1 = D == 64 ? 5 : 2, kX2 = D == 64 ? 4 : 2;  // ring slots of X1 and X2
+    // Ring slots of X1 and X2.  X1 has the shorter way from its last reader (acc1) to its next (S, two products later), so
+    // at D = 128, where one tile beyond two and two fits, it is X1's.
+    static constexpr int kX1 = D == 64 ? 5 : 3, kX2 = D == 64 ? 4 : 2;
     static constexpr int kRegions = D == 64 ? 3 : 2;  // S of step j is use 2 j of the ring, G use 2 j + 1
     static constexpr uint32_t kColAcc1 = 0, kColAcc2 = D, kColR = 2 * D;  // regions: + 128 each
-    static constexpr uint32_t kOffStat = 1024, kOffR = kOffStat + kStatSlots * kStatBytes + 1024;
-    static constexpr uint32_t kOffX1 = kOffR + 2 * kTile, kOffX2 = kOffX1 + kX1 * kTile;
-    static constexpr uint32_t kSmem = 1024 + kOffX2 + kX2 * kTile;  // + 1 KB alignment slack
-    static_assert(kOffR % 1024 == 0, "operand tiles must be 1 KB aligned");
+    // The tiles (1 KB aligned), the control block and the statistics: at D = 128 all of the 227 KB a block may have.
+    static constexpr uint32_t kOffR = 0, kOffX1 = kOffR + 2 * kTile, kOffX2 = kOffX1 + kX1 * kTile;
+    static constexpr uint32_t kOffCtl = kOffX2 + kX2 * kTile, kOffStat = kOffCtl + 1024;
+    static constexpr uint32_t kSmem = kOffStat + kStatSlots * kStatBytes;
     static_assert(kColR + 128 * kRegions <= 512, "tensor memory");
-    static_assert(kSmem + 1024 <= 232448, "shared memory over the per-block limit");
+    static_assert(kSmem <= 232448, "shared memory over the per-block limit");
 };
 
 struct BwdArgs {
@@ -89,9 +93,10 @@ struct BwdArgs {
 
 struct Ctl {
     uint64_t r_full, r_ready, x1_full[5], x1_empty[5], x2_full[4], x2_empty[4], st_full[kStatSlots], st_empty[kStatSlots];
-    uint64_t full[3], p_ready[2], d_ready[2], acc_full, mma_done[2];
+    uint64_t full[3], p_ready[2], d_ready[2], turn[2], acc_full, mma_done[2];
     uint32_t tmem_base;
     int abort_flag, bad;
+    Lookup lookup;
 };
 static_assert(sizeof(Ctl) <= 1024, "control block too large");
 
@@ -286,7 +291,7 @@ __device__ void role_load(const BwdArgs &p, Ctl &c, uint32_t smem, const Unit &u
 }
 
 // Statistics of each step's 128 queries: -stat of all, then -delta of all.
-template <bool F16>
+template <int D, bool F16>
 __device__ void role_stats(const BwdArgs &p, Ctl &c, uint32_t smem, const Unit &u, const Walk &k, int g, float kappa,
                            int lane, const Waiter &w) {
     const int n = k.steps();
@@ -302,7 +307,7 @@ __device__ void role_stats(const BwdArgs &p, Ctl &c, uint32_t smem, const Unit &
             x[i] = col < u.len ? __ldg(st + col) : make_float2(0.f, 0.f);
         }
         if (!wait_warp(su32(&c.st_empty[ring.slot]), ring.phase ^ 1u, w)) return;
-        const uint32_t dst = smem + 1024u + (uint32_t)ring.slot * kStatBytes + (uint32_t)lane * 16u;
+        const uint32_t dst = smem + Cfg<D>::kOffStat + (uint32_t)ring.slot * kStatBytes + (uint32_t)lane * 16u;
         sts128(dst, __float_as_uint(shift - x[0].x), __float_as_uint(shift - x[1].x), __float_as_uint(shift - x[2].x),
                __float_as_uint(shift - x[3].x));
         sts128(dst + 512u, __float_as_uint(-x[0].y * kappa), __float_as_uint(-x[1].y * kappa),
@@ -371,6 +376,7 @@ __device__ __forceinline__ void issue(const BwdArgs &p, Ctl &c, uint32_t smem, u
         if (!next_scores()) return;
     for (int j = 0; j < n; ++j, at.next(k), xa.next(), mine += 2) {
         if (!wait_warp(su32(&ready[j & 1]), (uint32_t)((j >> 1) & 1), w)) return;
+        if (R == 2 && !FIRST && !wait_warp(su32(&c.turn[j & 1]), (uint32_t)((j >> 1) & 1), w)) return;
         if (KEYS || !FIRST) {
             if (!wait_warp(su32(&acc_full[xa.slot]), xa.phase, w)) return;
             const uint32_t x = smem + ACC_X + (uint32_t)xa.slot * C::kTile;
@@ -382,6 +388,7 @@ __device__ __forceinline__ void issue(const BwdArgs &p, Ctl &c, uint32_t smem, u
         }
         if (elect_one()) tc_commit_to(su32(&acc_empty[xa.slot]));
         if (j + AHEAD < n && !next_scores()) return;
+        if (R == 2 && FIRST && lane == 0) bar_arrive(su32(&c.turn[j & 1]));
     }
     if (elect_one()) tc_commit_to(su32(&c.acc_full));
 }
@@ -530,7 +537,7 @@ __device__ void role_soft(const BwdArgs &p, Ctl &c, uint32_t smem, uint32_t tmem
         const bool whole = KEYS ? base >= u.p0 + kRows - 1 && base + 32 <= u.len &&
                                       (a.window == 0 || base + 31 < u.p0 + a.window)
                                 : base + 31 <= u.p0 && (a.window == 0 || u.p0 + kRows - 1 < base + a.window);
-        const uint32_t keep = bits_between(from, to), st = smem + 1024u + (uint32_t)stat.slot * kStatBytes + 4u * (uint32_t)cols;
+        const uint32_t keep = bits_between(from, to), st = smem + C::kOffStat + (uint32_t)stat.slot * kStatBytes + 4u * (uint32_t)cols;
         uint32_t pv[32], gv[32], pk[16];
         if (KEYS && !wait_warp(su32(&c.st_full[stat.slot]), stat.phase, w)) return;
         if (!wait_warp(su32(&c.full[ring.slot]), ring.phase, w)) return;
@@ -653,7 +660,7 @@ __device__ __forceinline__ void unit_body(const BwdArgs &p, Ctl &c, uint32_t sme
     using C = Cfg<D>;
     const unsigned heads = KEYS ? p.a.nkv : p.a.nh;
     const int head = (int)(index % heads), g = KEYS ? head : head / p.a.hpk;
-    const Unit u = find_unit(p.a, index / heads, kRows, !KEYS, check, &g_bwd_error_word);
+    const Unit u = find_unit(p.a, index / heads, kRows, !KEYS, check, &g_bwd_error_word, c.lookup);
     if (!u.live) return;
     const int live = u.len - u.p0 < kRows ? u.len - u.p0 : kRows;
     if (u.pad) {
@@ -686,7 +693,7 @@ __device__ __forceinline__ void unit_body(const BwdArgs &p, Ctl &c, uint32_t sme
         if (lane == 0) role_load<D, KEYS>(p, c, smem, u, k, head, g, w);
         __syncwarp();
     } else if (KEYS) {
-        role_stats<F16>(p, c, smem, u, k, g, F16 ? sigma * 0x1p-13f : 1.f, lane, w);
+        role_stats<D, F16>(p, c, smem, u, k, g, F16 ? sigma * 0x1p-13f : 1.f, lane, w);
     }
     tc_before();
     __syncthreads();
@@ -698,8 +705,12 @@ template <int D, bool F16>
 __global__ void __launch_bounds__(kThreads, 1) backward_tc_kernel(const __grid_constant__ BwdArgs p) {
     using C = Cfg<D>;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
-    const uint32_t smem = (su32(smem_raw) + 1023u) & ~1023u;
-    Ctl &c = *reinterpret_cast<Ctl *>(smem_raw + (smem - su32(smem_raw)));
+    const uint32_t smem = su32(smem_raw);
+    Ctl &c = *reinterpret_cast<Ctl *>(smem_raw + C::kOffCtl);
+    if (smem & 1023u) {  // there is no room to align it here; the kernel has no other shared memory, so it is aligned
+        if (threadIdx.x == 0) atomicOr(&g_bwd_error_word, kErrTimeout);
+        return;
+    }
     const int warp = uniform((int)(threadIdx.x >> 5)), lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
         bar_init(su32(&c.r_full), 2);
@@ -720,6 +731,7 @@ __global__ void __launch_bounds__(kThreads, 1) backward_tc_kernel(const __grid_c
         for (int i = 0; i < 2; ++i) {
             bar_init(su32(&c.p_ready[i]), kSoftWarps);
             bar_init(su32(&c.d_ready[i]), kSoftWarps);
+            bar_init(su32(&c.turn[i]), 1);
         }
         bar_init(su32(&c.acc_full), 2);
         bar_init(su32(&c.mma_done[0]), 1);

@@ -69,10 +69,14 @@ __device__ __forceinline__ void segment(const Args &a, int i, int &begin, int &l
 // else ascending (keys: those with the most queries).  Each thread adds up the tiles of a run of segments, the block scans
 // those sums, and the thread whose run holds `u` walks it: two rounds of loads for
 // any number of sequences.  `check`: raise the error flag where offsets are malformed.
-__device__ __forceinline__ Unit find_unit(const Args &a, unsigned u, int rows, bool down, bool check,
-                                          unsigned *error) {
-    __shared__ unsigned warp_sum[32];
-    __shared__ Unit found;
+struct Lookup {  // its shared memory
+    unsigned warp_sum[32];
+    Unit found;
+};
+__device__ __forceinline__ Unit find_unit(const Args &a, unsigned u, int rows, bool down, bool check, unsigned *error,
+                                          Lookup &s) {
+    unsigned *warp_sum = s.warp_sum;
+    Unit &found = s.found;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, n = a.seqs + 2;
     const int per = a.seqs + 2 <= (int)blockDim.x ? 1 : (n + (int)blockDim.x - 1) / (int)blockDim.x;
     const int i0 = tid * per < n ? tid * per : n, i1 = i0 + per < n ? i0 + per : n;
@@ -114,6 +118,11 @@ __device__ __forceinline__ Unit find_unit(const Args &a, unsigned u, int rows, b
         }
     __syncthreads();
     return found;
+}
+__device__ __forceinline__ Unit find_unit(const Args &a, unsigned u, int rows, bool down, bool check,
+                                          unsigned *error) {
+    __shared__ Lookup s;
+    return find_unit(a, u, rows, down, check, error, s);
 }
 
 template <typename T>
