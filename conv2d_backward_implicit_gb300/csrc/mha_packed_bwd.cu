@@ -358,8 +358,8 @@ __device__ __forceinline__ void issue(const BwdArgs &p, Ctl &c, uint32_t smem, u
     Ring<NA> xa;  // sums' operand
     Cursor at{k.lo, 0};
     int use = IS_S ? 0 : 1, mine = FIRST ? 0 : 1;  // ring uses of the next scores and of the next sums
+    auto operand = [&] { return wait_warp(su32(&score_full[xs.slot]), xs.phase, w); };  // of the next scores
     auto next_scores = [&] {
-        if (!wait_warp(su32(&score_full[xs.slot]), xs.phase, w)) return false;
         tc_after();
         if (elect_one()) {
             scores<D, !KEYS>(tmem + C::kColR + 128u * (uint32_t)(use % R), res,
@@ -369,25 +369,32 @@ __device__ __forceinline__ void issue(const BwdArgs &p, Ctl &c, uint32_t smem, u
         }
         xs.next();
         use += 2;
-        return true;
     };
     if (!wait_warp(su32(KEYS ? &c.r_full : &c.r_ready), 0, w)) return;
-    for (int j = 0; j < AHEAD && j < n; ++j)
-        if (!next_scores()) return;
+    for (int j = 0; j < AHEAD && j < n; ++j) {
+        if (!operand()) return;
+        next_scores();
+    }
     for (int j = 0; j < n; ++j, at.next(k), xa.next(), mine += 2) {
+        // The operands first: a wait costs over 100 cycles even for what is there, and this one passes while the softmax
+        // still works.
+        const bool more = j + AHEAD < n;
+        if (more && !operand()) return;
+        const uint32_t x = smem + ACC_X + (uint32_t)xa.slot * C::kTile;
+        if (KEYS || !FIRST) {
+            if (!wait_warp(su32(&acc_full[xa.slot]), xa.phase, w)) return;
+            if (seq_end - at.row < kRows) zero_rows(x, seq_end - at.row, kRows, C::kHalves, lane);
+        }
         if (!wait_warp(su32(&ready[j & 1]), (uint32_t)((j >> 1) & 1), w)) return;
         if (R == 2 && !FIRST && !wait_warp(su32(&c.turn[j & 1]), (uint32_t)((j >> 1) & 1), w)) return;
         if (KEYS || !FIRST) {
-            if (!wait_warp(su32(&acc_full[xa.slot]), xa.phase, w)) return;
-            const uint32_t x = smem + ACC_X + (uint32_t)xa.slot * C::kTile;
-            if (seq_end - at.row < kRows) zero_rows(x, seq_end - at.row, kRows, C::kHalves, lane);
             tc_after();
             if (elect_one())
                 sums(tmem + (FIRST ? C::kColAcc2 : C::kColAcc1), tmem + C::kColR + 128u * (uint32_t)(mine % R),
                      desc_mn(x, kHalf, 1024u), p.idesc2, j == 0);
         }
         if (elect_one()) tc_commit_to(su32(&acc_empty[xa.slot]));
-        if (j + AHEAD < n && !next_scores()) return;
+        if (more) next_scores();
         if (R == 2 && FIRST && lane == 0) bar_arrive(su32(&c.turn[j & 1]));
     }
     if (elect_one()) tc_commit_to(su32(&c.acc_full));
