@@ -464,24 +464,19 @@ __device__ __forceinline__ bool store_acc(uint32_t acc_tm, uint32_t stage, float
                                           int live, int cols, int lane) {
     constexpr int kChunks = W / 8;  // 16-byte chunk j of row r lies at j ^ (r & 7), of 64-byte rows at j ^ (r / 2 & 3)
     auto place = [](int r, int j) { return (uint32_t)((kChunks == 4 ? j ^ ((r >> 1) & 3) : j ^ (r & 7)) << 4); };
-    bool good = true;
+    float2 odd = make_float2(0.f, 0.f);  // 0 as long as every value is finite
 #pragma unroll
     for (int k = 0; k < W / 32; ++k) {
         uint32_t o[32];
         tc_ld_32x32(acc_tm + 32 * k, o);
         tc_wait_ld(o);
-        float x[32];
-#pragma unroll
-        for (int e = 0; e < 32; ++e) {
-            x[e] = __uint_as_float(o[e]) * factor;
-            good = good && finite(x[e]);
-        }
+        scale_pack<F16>(o, factor, odd);
 #pragma unroll
         for (int j = 0; j < 4; ++j)
-            sts128(stage + (uint32_t)lane * (2 * W) + place(lane, 4 * k + j), pack2<F16>(x[8 * j], x[8 * j + 1]),
-                   pack2<F16>(x[8 * j + 2], x[8 * j + 3]), pack2<F16>(x[8 * j + 4], x[8 * j + 5]),
-                   pack2<F16>(x[8 * j + 6], x[8 * j + 7]));
+            sts128(stage + (uint32_t)lane * (2 * W) + place(lane, 4 * k + j), o[4 * j], o[4 * j + 1], o[4 * j + 2],
+                   o[4 * j + 3]);
     }
+    const bool good = odd.x + odd.y == 0.f;
     __syncwarp();
     const int j = lane % kChunks;
     for (int r = lane / kChunks; r < 32; r += 32 / kChunks) {
@@ -667,7 +662,7 @@ __device__ __forceinline__ void unit_body(const BwdArgs &p, Ctl &c, uint32_t sme
     using C = Cfg<D>;
     const unsigned heads = KEYS ? p.a.nkv : p.a.nh;
     const int head = (int)(index % heads), g = KEYS ? head : head / p.a.hpk;
-    const Unit u = find_unit(p.a, index / heads, kRows, !KEYS, check, &g_bwd_error_word, c.lookup);
+    const Unit u = find_unit(p.a, index / heads, 7, !KEYS, check, &g_bwd_error_word, c.lookup);
     if (!u.live) return;
     const int live = u.len - u.p0 < kRows ? u.len - u.p0 : kRows;
     if (u.pad) {
@@ -722,40 +717,38 @@ __global__ void __launch_bounds__(kThreads, 1) backward_tc_kernel(const __grid_c
     if (threadIdx.x == 0) {
         bar_init(su32(&c.r_full), 2);
         bar_init(su32(&c.r_ready), kSoftWarps);
-        for (int s = 0; s < 5; ++s) {
-            bar_init(su32(&c.x1_full[s]), 1);
-            bar_init(su32(&c.x1_empty[s]), 1);
-        }
-        for (int s = 0; s < 4; ++s) {
-            bar_init(su32(&c.x2_full[s]), 1);
-            bar_init(su32(&c.x2_empty[s]), C::kRegions == 2 ? 2 : 1);  // G and acc2, of two warps or of one
-        }
-        for (int s = 0; s < kStatSlots; ++s) {
-            bar_init(su32(&c.st_full[s]), 1);
-            bar_init(su32(&c.st_empty[s]), kSoftWarps);
-        }
-        for (int i = 0; i < 3; ++i) bar_init(su32(&c.full[i]), 1);
-        for (int i = 0; i < 2; ++i) {
-            bar_init(su32(&c.p_ready[i]), kSoftWarps);
-            bar_init(su32(&c.d_ready[i]), kSoftWarps);
-            bar_init(su32(&c.turn[i]), 1);
-        }
         bar_init(su32(&c.acc_full), 2);
         bar_init(su32(&c.mma_done[0]), 1);
         bar_init(su32(&c.mma_done[1]), 1);
         c.abort_flag = 0;
         c.bad = 0;
-        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    } else if (warp == 0) {
+        if (lane <= 5) {
+            bar_init(su32(&c.x1_full[lane - 1]), 1);
+            bar_init(su32(&c.x1_empty[lane - 1]), 1);
+        } else if (lane <= 9) {
+            bar_init(su32(&c.x2_full[lane - 6]), 1);
+            bar_init(su32(&c.x2_empty[lane - 6]), C::kRegions == 2 ? 2 : 1);  // G and acc2, of two warps or of one
+        } else if (lane <= 9 + kStatSlots) {
+            bar_init(su32(&c.st_full[lane - 10]), 1);
+            bar_init(su32(&c.st_empty[lane - 10]), kSoftWarps);
+        } else if (lane <= 14) {
+            bar_init(su32(&c.full[lane - 12]), 1);
+        } else if (lane <= 16) {
+            bar_init(su32(&c.p_ready[lane - 15]), kSoftWarps);
+            bar_init(su32(&c.d_ready[lane - 15]), kSoftWarps);
+            bar_init(su32(&c.turn[lane - 15]), 1);
+        }
+    } else if (threadIdx.x < 36) {
+        const CUtensorMap *m = lane == 0 ? &p.q_map : lane == 1 ? &p.k_map : lane == 2 ? &p.v_map : &p.go_map;
+        asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(m)) : "memory");
     }
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     if (warp == kMmaWarp) tc_alloc(su32(&c.tmem_base), 512);
     tc_before();
     __syncthreads();
     tc_after();
     const uint32_t tmem = c.tmem_base;
-    if (threadIdx.x < 4) {
-        const CUtensorMap *m = threadIdx.x == 0 ? &p.q_map : threadIdx.x == 1 ? &p.k_map : threadIdx.x == 2 ? &p.v_map : &p.go_map;
-        asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(m)) : "memory");
-    }
     if (threadIdx.x == 0) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
     if (blockIdx.x < p.key_units)

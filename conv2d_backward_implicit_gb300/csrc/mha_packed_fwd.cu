@@ -10,17 +10,19 @@
 //   S_i[pos][t] = Q_i . K^T                tcgen05 M128 N128 K16, D / 16 steps
 //   P_i = 2^(S_i c - m_i c), c = log2(e) / sqrt(head_dim), masked, rounded to 16 bits
 //   O_i[pos][:] += P_i V                   tcgen05 M128 N(D) K16, 8 steps, P from tensor memory
-// Tensor memory holds S_0, S_1 (128 columns each, P_i over the first 64 of S_i) and
+// Tensor memory holds S_0, S_1 (128 columns each, P_i over the first 32 of each 64) and
 // O_0, O_1 (D each).
-//   * warps 0-3 and 4-7: the softmax of tile 0 and 1, one query per thread.  fp16's P
+//   * warps 0-7 and 8-15: the softmax of tile 0 and 1, 64 of a query's 128 keys per
+//     thread; the two warps that share 32 queries exchange their maxima through shared
+//     memory, 64 threads at a named barrier.  fp16's P
 //     carries a factor 2^7, which cancels in O / sum.  The
 //     maximum m_i that scales P and O may lag the true one: O and the sum are rescaled
 //     only when it grew by more than 2^8 (P stays below 2^8, far from fp16's limit), so
 //     most blocks skip the pass over O.  The true maximum is kept beside it for LSE.
-//   * warp 8 (one lane issuing): per key block PV_0, S_0 of the next block,
+//   * warp 16 (one lane issuing): per key block PV_0, S_0 of the next block,
 //     PV_1, S_1 of the next: while one tile's products run, the other's softmax does.
 //     The products of one thread run in order, so S_i may overwrite P_i behind PV_i.
-//   * warps 9 and 10 (one thread each): TMA copies of K (and Q tile 0) and V (and Q
+//   * warps 17 and 18 (one thread each): TMA copies of K (and Q tile 0) and V (and Q
 //     tile 1).
 // V rows past the sequence's end are zeroed in shared memory (other sequences' rows,
 // possibly with infinities); what is masked inside the sequence has P = 0, and if a
@@ -46,7 +48,7 @@ namespace {
 
 constexpr int kRows = 128;                     // queries per tile, keys per step
 constexpr uint32_t kHalf = kRows * 128;        // bytes of a [128][64] 16-bit half tile
-constexpr int kSoftWarps = 8, kMmaWarp = 8, kLoadWarp = 9;  // K, then V
+constexpr int kSoftWarps = 16, kMmaWarp = 16, kLoadWarp = 17;  // K, then V
 constexpr uint32_t kColS = 0, kColO = 256;     // + 128 i, + 128 i
 constexpr int kThreads = 32 * (kLoadWarp + 2);
 constexpr float kLag = 8.0f;                   // log2 of how far the scaling maximum may lag
@@ -57,8 +59,9 @@ struct Cfg {
     static constexpr int kHalves = D / 64;
     static constexpr uint32_t kTile = kHalf * kHalves;
     static constexpr int kStages = D == 64 ? 4 : 2;
-    static constexpr uint32_t kOffQ = 1024, kOffK = kOffQ + 2 * kTile, kOffV = kOffK + kStages * kTile;
+    static constexpr uint32_t kOffQ = 5120, kOffK = kOffQ + 2 * kTile, kOffV = kOffK + kStages * kTile;
     static constexpr uint32_t kSmem = 1024 + kOffV + kStages * kTile;  // + 1 KB alignment slack
+    static_assert(kOffQ % 1024 == 0, "operand tiles must be 1 KB aligned");
     static_assert(kSmem + 1024 <= 232448, "shared memory over the per-block limit");
 };
 
@@ -147,8 +150,8 @@ __device__ __forceinline__ void issue_products(const FwdArgs &p, Ctl &c, uint32_
                 const uint64_t vd = desc_mn(smem + C::kOffV + (uint32_t)vs * C::kTile, kHalf, 1024u);
                 if (elect_one()) {
 #pragma unroll
-                    for (int k = 0; k < 8; ++k)  // A: 8 columns (16 keys) per step; B: two groups of 8 keys (2 KB)
-                        tc_mma_f16_ts(tmem + kColO + 128u * i, tmem + kColS + 128u * i + 8u * k, vd + 128u * k, p.idesc2,
+                    for (int k = 0; k < 8; ++k)  // A: 8 columns (16 keys) per step, 64 keys every 64; B: two groups of 8 keys
+                        tc_mma_f16_ts(tmem + kColO + 128u * i, tmem + kColS + 128u * i + 64u * (k / 4) + 8u * (k % 4), vd + 128u * k, p.idesc2,
                                       phase[i] > 0 || k > 0);
                     if (b + 1 == first[i]) tc_commit_to(su32(&c.o_full[i]));
                 }
@@ -210,54 +213,53 @@ __device__ __forceinline__ void exp32(const uint32_t (&v)[32], float cs, float m
     }
 }
 
+// The softmax of tile i.  `xch`: shared floats [2][64] of this pair of warps (both halves of a row, two turns).
 template <int D, bool F16>
 __device__ void role_soft(const FwdArgs &p, Ctl &c, uint32_t smem, uint32_t tmem, const Unit &u, const Tile &t, int i,
-                          int warp, int lane, const Waiter &w) {
+                          int warp, int lane, float *xch, const Waiter &w) {
     using C = Cfg<D>;
-    const int quad = warp & 3, pos = t.p0 + 32 * quad + lane;
+    const int quad = warp & 3, part = (warp >> 2) & 1, pair = 4 * i + quad, pos = t.p0 + 32 * quad + lane;
     const uint32_t lane_tm = (uint32_t)(32 * quad) << 16;
-    const uint32_t s_tm = tmem + lane_tm + kColS + 128u * i, o_tm = tmem + lane_tm + kColO + 128u * i;
+    const uint32_t s_tm = tmem + lane_tm + kColS + 128u * i + 64u * part;
+    const uint32_t p_tm = tmem + lane_tm + kColS + 128u * i + 64u * part;  // P: 32 columns over this warp's own scores
+    const uint32_t o_tm = tmem + lane_tm + kColO + 128u * i + (uint32_t)(D / 2) * part;
     const float cs = p.a.scale * 1.4426950408889634f;
     float used = -INFINITY, top = -INFINITY;  // the maximum that scales, the true one
     float2 sum = make_float2(0.f, 0.f);
+    auto meet = [&](float mine, int turn) {  // the other half's value of this row
+        xch[64 * turn + 32 * part + lane] = mine;
+        asm volatile("bar.sync %0, 64;" ::"r"(1 + pair) : "memory");
+        return xch[64 * turn + 32 * (part ^ 1) + lane];
+    };
     int it = 0;
     for (int b = t.hi - 1; b >= t.lo; --b, ++it) {
         if (!wait_warp(su32(&c.s_full[i]), (uint32_t)(it & 1), w)) return;
         tc_after();
-        const int base = kRows * b;
-        const bool whole = base + kRows - 1 <= t.p0 && (p.a.window == 0 || t.p0 + kRows - 1 < base + p.a.window);
-        const int to = pos - base, from = p.a.window > 0 ? pos - p.a.window + 1 - base : 0;
+        const int base = kRows * b + 64 * part;
+        const bool whole = base + 63 <= t.p0 && (p.a.window == 0 || t.p0 + kRows - 1 < base + p.a.window);
         uint32_t v0[32], v1[32];
-        float m = top;
-        // Chunks 2 and 3 for their maximum, then 0 and 1, which stay in registers: their P overwrites columns that
-        // are read, and chunks 2 and 3 are read again afterwards (columns 64 .. 127, which P never covers).
-        tc_ld_32x32(s_tm + 64, v0);
-        tc_ld_32x32(s_tm + 96, v1);
-        tc_wait_ld(v0);
-        tc_wait_ld(v1);
-        if (!whole) mask32(v0, from - 64, to - 64), mask32(v1, from - 96, to - 96);
-        m = max32(v0, m);
-        m = max32(v1, m);
         tc_ld_32x32(s_tm, v0);
         tc_ld_32x32(s_tm + 32, v1);
         tc_wait_ld(v0);
         tc_wait_ld(v1);
-        if (!whole) mask32(v0, from, to), mask32(v1, from - 32, to - 32);
-        m = max32(v0, m);
-        m = max32(v1, m);
+        if (!whole) {
+            const int to = pos - base, from = p.a.window > 0 ? pos - p.a.window + 1 - base : 0;
+            mask32(v0, from, to), mask32(v1, from - 32, to - 32);
+        }
+        float m = max32(v1, max32(v0, top));
+        m = fmaxf(m, meet(m, it & 1));
         top = m;
-        if (__any_sync(0xffffffffu, (m - used) * cs > kLag)) {
+        if (__any_sync(0xffffffffu, (m - used) * cs > kLag)) {  // the same for both halves
             if (it > 0) {  // before the first product O holds nothing
                 const float keep = m == -INFINITY ? 1.f : fast_exp2((used - m) * cs);
                 sum.x *= keep, sum.y *= keep;
+#pragma unroll 1
+                for (int k = 0; k < D / 2; k += 16) {  // S of this block is behind PV of the last: O is complete
+                    uint32_t o[16];
+                    tc_ld_32x16(o_tm + k, o);
 #pragma unroll
-                for (int k = 0; k < D / 32; ++k) {  // S of this block is behind PV of the last: O is complete
-                    uint32_t o[32];
-                    tc_ld_32x32(o_tm + 32 * k, o);
-                    tc_wait_ld(o);
-#pragma unroll
-                    for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * keep);
-                    tc_st_32x32(o_tm + 32 * k, o);
+                    for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * keep);
+                    tc_st_32x16(o_tm + k, o);
                 }
             }
             used = m;
@@ -265,51 +267,38 @@ __device__ void role_soft(const FwdArgs &p, Ctl &c, uint32_t smem, uint32_t tmem
         const float mc = (used == -INFINITY ? 0.f : used * cs) - (F16 ? kShift16 : 0.f);
         uint32_t pk[16];
         exp32<F16>(v0, cs, mc, sum, pk);
-        tc_st_32x16(s_tm, pk);
+        tc_st_32x16(p_tm, pk);
         exp32<F16>(v1, cs, mc, sum, pk);
-        tc_st_32x16(s_tm + 16, pk);
-        tc_ld_32x32(s_tm + 64, v0);
-        tc_ld_32x32(s_tm + 96, v1);
-        tc_wait_ld(v0);
-        tc_wait_ld(v1);
-        if (!whole) mask32(v0, from - 64, to - 64), mask32(v1, from - 96, to - 96);
-        exp32<F16>(v0, cs, mc, sum, pk);
-        tc_st_32x16(s_tm + 32, pk);
-        exp32<F16>(v1, cs, mc, sum, pk);
-        tc_st_32x16(s_tm + 48, pk);
+        tc_st_32x16(p_tm + 16, pk);
         tc_wait_st();
         tc_before();
         __syncwarp();
         if (lane == 0) bar_arrive(su32(&c.p_ready[i]));
     }
+    const float mine = sum.x + sum.y, total = mine + meet(mine, it & 1);
     if (!wait_warp(su32(&c.o_full[i]), 0, w)) return;
     tc_after();
-    // O rows through this warp's part of its Q tile (read by then), 16-byte chunk j of row r at j ^ (r & 7).
-    constexpr int kChunks = D / 8;
-    const float total = sum.x + sum.y, inv = 1.0f / total;
-    const uint32_t stage = smem + C::kOffQ + (uint32_t)i * C::kTile + (uint32_t)quad * (C::kTile / 4);
+    // O rows (this warp's D / 2 columns) through its part of the Q tile, read by then.
+    constexpr int W = D / 2, kChunks = W / 8;  // 16-byte chunk j of row r lies at j ^ (r & 7), of 64-byte rows at j ^ (r / 2 & 3)
+    auto place = [](int r, int j) { return (uint32_t)((kChunks == 4 ? j ^ ((r >> 1) & 3) : j ^ (r & 7)) << 4); };
+    const float inv = 1.0f / total;
+    const uint32_t stage = smem + C::kOffQ + (uint32_t)i * C::kTile + (uint32_t)(warp & 7) * (C::kTile / 8);
     const bool row_live = 32 * quad + lane < t.live;
-    bool good = true;
+    float2 odd = make_float2(0.f, 0.f);  // 0 as long as every value is finite
 #pragma unroll
-    for (int k = 0; k < D / 32; ++k) {
+    for (int k = 0; k < W / 32; ++k) {
         uint32_t o[32];
         tc_ld_32x32(o_tm + 32 * k, o);
         tc_wait_ld(o);
-        float x[32];
-#pragma unroll
-        for (int e = 0; e < 32; ++e) {
-            x[e] = __uint_as_float(o[e]) * inv;
-            good = good && finite(x[e]);
-        }
+        scale_pack<F16>(o, inv, odd);
 #pragma unroll
         for (int j = 0; j < 4; ++j)
-            sts128(stage + (uint32_t)lane * (2 * D) + (uint32_t)(((4 * k + j) ^ (lane & 7)) << 4),
-                   pack2<F16>(x[8 * j], x[8 * j + 1]), pack2<F16>(x[8 * j + 2], x[8 * j + 3]),
-                   pack2<F16>(x[8 * j + 4], x[8 * j + 5]), pack2<F16>(x[8 * j + 6], x[8 * j + 7]));
+            sts128(stage + (uint32_t)lane * (2 * W) + place(lane, 4 * k + j), o[4 * j], o[4 * j + 1], o[4 * j + 2],
+                   o[4 * j + 3]);
     }
-    if (__any_sync(0xffffffffu, row_live && !good) && lane == 0) c.bad[i] = 1;
+    if (__any_sync(0xffffffffu, row_live && !(odd.x + odd.y == 0.f)) && lane == 0) c.bad[i] = 1;
     const int64_t row0 = (int64_t)u.begin + t.p0 + 32 * quad;
-    if (row_live) {
+    if (row_live && part == 0) {
         // The sum is relative to `used`; LSE wants it relative to the true maximum.
         const float ln2 = 0.6931471805599453f;
         const float l = logf(total) - ((top - used) * cs + (F16 ? kShift16 : 0.f)) * ln2;
@@ -317,21 +306,20 @@ __device__ void role_soft(const FwdArgs &p, Ctl &c, uint32_t smem, uint32_t tmem
         st[0] = top * p.a.scale, st[1] = l;
     }
     __syncwarp();
-    uint16_t *out = static_cast<uint16_t *>(p.a.out) + (row0 * p.a.nh + t.head) * p.a.hd;
+    uint16_t *out = static_cast<uint16_t *>(p.a.out) + (row0 * p.a.nh + t.head) * p.a.hd + W * part;
     const int j = lane % kChunks;
     for (int r = lane / kChunks; r < 32; r += 32 / kChunks) {
-        if (32 * quad + r >= t.live || 8 * j >= p.a.hd) continue;
-        const uint4 x = lds128(stage + (uint32_t)r * (2 * D) + (uint32_t)((j ^ (r & 7)) << 4));
+        if (32 * quad + r >= t.live || W * part + 8 * j >= p.a.hd) continue;
+        const uint4 x = lds128(stage + (uint32_t)r * (2 * W) + place(r, j));
         *reinterpret_cast<uint4 *>(out + (int64_t)r * p.a.nh * p.a.hd + 8 * j) = x;
     }
 }
 
 // A tile row by row over the attended keys, one warp per row: for tiles where a masked value is not finite.
 template <int D, bool F16>
-__device__ void recompute(const FwdArgs &p, const Unit &u, const Tile &t, int g) {
+__device__ __noinline__ void recompute(const Args &a, const Unit &u, const Tile &t, int g) {
     using T = typename std::conditional<F16, __half, __nv_bfloat16>::type;
     constexpr int N = D / 32;
-    const Args &a = p.a;
     const int lane = threadIdx.x & 31, warps = blockDim.x >> 5;
     for (int r = threadIdx.x >> 5; r < t.live; r += warps) {
         const int pos = t.p0 + r;
@@ -379,23 +367,27 @@ __global__ void __launch_bounds__(kThreads, 1) forward_tc_kernel(const __grid_co
     Ctl &c = *reinterpret_cast<Ctl *>(smem_raw + (smem - su32(smem_raw)));
     const int warp = uniform((int)(threadIdx.x >> 5)), lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
-        for (int s = 0; s < 4; ++s) {
-            bar_init(su32(&c.k_full[s]), 1);
-            bar_init(su32(&c.v_full[s]), 1);
-            bar_init(su32(&c.k_empty[s]), 1);
-            bar_init(su32(&c.v_empty[s]), 1);
-        }
-        for (int i = 0; i < 2; ++i) {
-            bar_init(su32(&c.q_full[i]), 1);
-            bar_init(su32(&c.s_full[i]), 1);
-            bar_init(su32(&c.p_ready[i]), 4);
-            bar_init(su32(&c.o_full[i]), 1);
-            c.bad[i] = 0;
-        }
         bar_init(su32(&c.mma_done), 1);
         c.abort_flag = 0;
-        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    } else if (warp == 0) {
+        if (lane <= 4) {
+            bar_init(su32(&c.k_full[lane - 1]), 1);
+            bar_init(su32(&c.k_empty[lane - 1]), 1);
+        } else if (lane <= 8) {
+            bar_init(su32(&c.v_full[lane - 5]), 1);
+            bar_init(su32(&c.v_empty[lane - 5]), 1);
+        } else if (lane <= 10) {
+            bar_init(su32(&c.q_full[lane - 9]), 1);
+            bar_init(su32(&c.s_full[lane - 9]), 1);
+            bar_init(su32(&c.p_ready[lane - 9]), 8);
+            bar_init(su32(&c.o_full[lane - 9]), 1);
+            c.bad[lane - 9] = 0;
+        }
+    } else if (threadIdx.x < 35) {
+        const CUtensorMap *m = lane == 0 ? &p.q_map : lane == 1 ? &p.k_map : &p.v_map;
+        asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(m)) : "memory");
     }
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     if (warp == kMmaWarp) tc_alloc(su32(&c.tmem_base), 512);
     tc_before();
     __syncthreads();
@@ -406,8 +398,8 @@ __global__ void __launch_bounds__(kThreads, 1) forward_tc_kernel(const __grid_co
 
     const unsigned pairs = p.pair_heads ? p.a.nh / 2 : p.a.nh;
     const int pair = (int)(blockIdx.x % pairs);
-    const Unit u = find_unit(p.a, blockIdx.x / pairs, p.pair_heads ? kRows : 2 * kRows, true,
-                             blockIdx.x == 0, &g_fwd_error_word);
+    const Unit u = find_unit(p.a, blockIdx.x / pairs, p.pair_heads ? 7 : 8, true, blockIdx.x == 0,
+                             &g_fwd_error_word);
     const Waiter w{&c.abort_flag, &g_fwd_error_word};
     if (u.live) {
         const Tile t[2] = {tile_of(p, u, pair, 0), tile_of(p, u, pair, 1)};
@@ -425,9 +417,10 @@ __global__ void __launch_bounds__(kThreads, 1) forward_tc_kernel(const __grid_co
             const int lo = t[1].live && t[1].lo < t[0].lo ? t[1].lo : t[0].lo;
             const int hi = t[1].hi > t[0].hi ? t[1].hi : t[0].hi;
             if (warp < kSoftWarps) {
-                const int i = warp >> 2;
+                const int i = warp >> 3;
                 const Tile own = i ? t[1] : t[0];
-                if (own.live) role_soft<D, F16>(p, c, smem, tmem, u, own, i, warp, lane, w);
+                float *xch = reinterpret_cast<float *>(reinterpret_cast<uint8_t *>(&c) + 1024) + 128 * (4 * i + (warp & 3));
+                if (own.live) role_soft<D, F16>(p, c, smem, tmem, u, own, i, warp, lane, xch, w);
             } else if (warp == kMmaWarp) {
                 role_mma<D>(p, c, smem, tmem, u, t, lo, hi, lane, w);
             } else {
@@ -439,8 +432,8 @@ __global__ void __launch_bounds__(kThreads, 1) forward_tc_kernel(const __grid_co
             __syncthreads();
             tc_after();
             if (!c.abort_flag) {
-                if (c.bad[0]) recompute<D, F16>(p, u, t[0], g);
-                if (c.bad[1]) recompute<D, F16>(p, u, t[1], g);
+                if (c.bad[0]) recompute<D, F16>(p.a, u, t[0], g);
+                if (c.bad[1]) recompute<D, F16>(p.a, u, t[1], g);
             }
         }
     }

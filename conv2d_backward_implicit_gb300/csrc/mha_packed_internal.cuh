@@ -63,66 +63,85 @@ __device__ __forceinline__ void segment(const Args &a, int i, int &begin, int &l
     len = hi > begin ? hi - begin : 0;
 }
 
-// Tile `u` of `rows` rows, every thread of the block calling (blockDim.x a
+// Tile `u` of 2^shift rows, every thread of the block calling (blockDim.x a
 // multiple of 32, at most 1024).  Segments are numbered as above, the tiles of one
 // in descending order when `down` (queries: those with the most keys come first),
-// else ascending (keys: those with the most queries).  Each thread adds up the tiles of a run of segments, the block scans
-// those sums, and the thread whose run holds `u` walks it: two rounds of loads for
-// any number of sequences.  `check`: raise the error flag where offsets are malformed.
+// else ascending (keys: those with the most queries).  Up to 32 segments: every warp
+// looks them through by itself, one segment per lane, one load's latency.  More: each
+// thread adds up the tiles of a run of segments, the block scans those sums, and the
+// thread whose run holds `u` walks it, two rounds of loads for any number of
+// sequences.  `check`: raise the error flag where offsets are malformed.
 struct Lookup {  // its shared memory
     unsigned warp_sum[32];
     Unit found;
 };
-__device__ __forceinline__ Unit find_unit(const Args &a, unsigned u, int rows, bool down, bool check, unsigned *error,
+__device__ __forceinline__ void check_offsets(const Args &a, int i, unsigned *error) {
+    const int lo = __ldg(a.off + i), hi = __ldg(a.off + i + 1);
+    if (lo < 0 || hi < lo || hi > a.tokens) atomicOr(error, kErrOffsets);
+}
+__device__ __forceinline__ unsigned scan32(unsigned x, int lane) {  // inclusive
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const unsigned y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += y;
+    }
+    return x;
+}
+__device__ __forceinline__ Unit find_unit(const Args &a, unsigned u, int shift, bool down, bool check, unsigned *error,
                                           Lookup &s) {
-    unsigned *warp_sum = s.warp_sum;
-    Unit &found = s.found;
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, n = a.seqs + 2;
-    const int per = a.seqs + 2 <= (int)blockDim.x ? 1 : (n + (int)blockDim.x - 1) / (int)blockDim.x;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, n = a.seqs + 2, round = (1 << shift) - 1;
+    if (n <= 32) {
+        int begin = 0, len = 0;
+        if (lane < n) segment(a, lane, begin, len);
+        if (check && tid < a.seqs) check_offsets(a, tid, error);
+        const unsigned tiles = ((unsigned)len + round) >> shift, incl = scan32(tiles, lane);
+        const unsigned hit = __ballot_sync(0xffffffffu, u >= incl - tiles && u < incl);
+        Unit x;
+        x.live = hit != 0;
+        const int at = hit ? __ffs(hit) - 1 : 0;
+        x.begin = __shfl_sync(0xffffffffu, begin, at);
+        x.len = __shfl_sync(0xffffffffu, len, at);
+        const unsigned k = u - __shfl_sync(0xffffffffu, incl - tiles, at), m = __shfl_sync(0xffffffffu, tiles, at);
+        x.p0 = (int)((down ? m - 1 - k : k) << shift);
+        x.pad = at >= a.seqs;
+        return x;
+    }
+    const int per = n <= (int)blockDim.x ? 1 : (n + (int)blockDim.x - 1) / (int)blockDim.x;
     const int i0 = tid * per < n ? tid * per : n, i1 = i0 + per < n ? i0 + per : n;
     unsigned sum = 0;
     int begin = 0, len = 0;  // of the last segment of the run
     for (int i = i0; i < i1; ++i) {
         segment(a, i, begin, len);
-        sum += (unsigned)((len + rows - 1) / rows);
-        if (check && i < a.seqs) {
-            const int lo = __ldg(a.off + i), hi = __ldg(a.off + i + 1);
-            if (lo < 0 || hi < lo || hi > a.tokens) atomicOr(error, kErrOffsets);
-        }
+        sum += ((unsigned)len + round) >> shift;
+        if (check && i < a.seqs) check_offsets(a, i, error);
     }
-    unsigned incl = sum;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const unsigned x = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane >= o) incl += x;
-    }
-    if (lane == 31) warp_sum[warp] = incl;
-    if (tid == 0) found.live = false;
+    unsigned incl = scan32(sum, lane);
+    if (lane == 31) s.warp_sum[warp] = incl;
+    if (tid == 0) s.found.live = false;
     __syncthreads();
-    if (n > 32 * per)  // else the first warp holds every segment
-        for (int w = 0; w < warp; ++w) incl += warp_sum[w];
+    for (int w = 0; w < warp; ++w) incl += s.warp_sum[w];
     unsigned at = incl - sum;
     if (u >= at && u < incl && i0 < i1)
         for (int i = i0; i < i1; ++i) {
             if (per > 1) segment(a, i, begin, len);
-            const unsigned tiles = (unsigned)((len + rows - 1) / rows);
+            const unsigned tiles = ((unsigned)len + round) >> shift;
             if (u < at + tiles) {
-                found.begin = begin;
-                found.len = len;
-                found.p0 = (int)(down ? tiles - 1 - (u - at) : u - at) * rows;
-                found.pad = i >= a.seqs;
-                found.live = true;
+                s.found.begin = begin;
+                s.found.len = len;
+                s.found.p0 = (int)((down ? tiles - 1 - (u - at) : u - at) << shift);
+                s.found.pad = i >= a.seqs;
+                s.found.live = true;
                 break;
             }
             at += tiles;
         }
     __syncthreads();
-    return found;
+    return s.found;
 }
-__device__ __forceinline__ Unit find_unit(const Args &a, unsigned u, int rows, bool down, bool check,
+__device__ __forceinline__ Unit find_unit(const Args &a, unsigned u, int shift, bool down, bool check,
                                           unsigned *error) {
     __shared__ Lookup s;
-    return find_unit(a, u, rows, down, check, error, s);
+    return find_unit(a, u, shift, down, check, error, s);
 }
 
 template <typename T>

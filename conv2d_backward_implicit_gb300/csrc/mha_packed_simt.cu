@@ -156,7 +156,7 @@ __global__ void __launch_bounds__(kThreads) forward_simt_kernel(const Args a) {
     float *q_s = sm, *x_s = q_s + B * P, *p_s = x_s + B * P;
     const int ty = threadIdx.x >> 4, tx = threadIdx.x & 15;
     const int h = (int)(blockIdx.x % (unsigned)a.nh), g = h / a.hpk;
-    const Unit u = find_unit(a, blockIdx.x / (unsigned)a.nh, B, true, blockIdx.x == 0, &g_simt_error_word);
+    const Unit u = find_unit(a, blockIdx.x / (unsigned)a.nh, 6, true, blockIdx.x == 0, &g_simt_error_word);
     if (!u.live) return;
     const int live = u.len - u.p0 < B ? u.len - u.p0 : B;
     const int64_t row0 = (int64_t)u.begin + u.p0;
@@ -264,7 +264,7 @@ __global__ void __launch_bounds__(kThreads) backward_simt_kernel(const Args a) {
     const int ty = threadIdx.x >> 4, tx = threadIdx.x & 15;
     const unsigned heads = KEYS ? a.nkv : a.nh;
     const int head = (int)(blockIdx.x % heads), g = KEYS ? head : head / a.hpk;
-    const Unit u = find_unit(a, blockIdx.x / heads, B, !KEYS, blockIdx.x == 0 && KEYS, &g_simt_error_word);
+    const Unit u = find_unit(a, blockIdx.x / heads, B == 64 ? 6 : 5, !KEYS, blockIdx.x == 0 && KEYS, &g_simt_error_word);
     if (!u.live) return;
     const int live = u.len - u.p0 < B ? u.len - u.p0 : B;
     const int64_t row0 = (int64_t)u.begin + u.p0;

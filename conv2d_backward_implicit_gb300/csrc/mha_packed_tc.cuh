@@ -48,14 +48,14 @@ __device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity, const W
     return __all_sync(0xffffffffu, wait(bar, parity, w)) != 0;
 }
 
-__device__ __forceinline__ void tc_st_32x32(uint32_t taddr, const uint32_t (&r)[32]) {
+// 32 lanes x 16 consecutive 32-bit columns, complete on return.
+__device__ __forceinline__ void tc_ld_32x16(uint32_t taddr, uint32_t (&r)[16]) {
     asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, "
-        "%14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(taddr),
-        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
-        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
-        "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
-        "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, "
+        "[%16];\n\ttcgen05.wait::ld.sync.aligned;"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr)
         : "memory");
 }
 
@@ -99,6 +99,18 @@ __device__ __forceinline__ bool elect_one() {
 }
 
 __device__ __forceinline__ bool finite(float x) { return fabsf(x) <= 3.402823466e38f; }
+
+// 32 floats times `factor`, rounded in pairs into o[0 .. 15]; `odd` stays 0 unless one is not finite (x * 0 is then NaN).
+template <bool F16>
+__device__ __forceinline__ void scale_pack(uint32_t (&o)[32], float factor, float2 &odd) {
+    const float2 f2 = make_float2(factor, factor), z2 = make_float2(0.f, 0.f);
+#pragma unroll
+    for (int e = 0; e < 32; e += 2) {
+        const float2 x = __fmul2_rn(make_float2(__uint_as_float(o[e]), __uint_as_float(o[e + 1])), f2);
+        odd = __ffma2_rn(x, z2, odd);
+        o[e >> 1] = pack2<F16>(x.x, x.y);
+    }
+}
 
 // Zero rows [from, rows) of a [rows][D] tile held as D / 64 halves of 128-byte rows: one warp, before the tensor core
 // reads it.
