@@ -10,19 +10,23 @@
 //   S_i[pos][t] = Q_i . K^T                tcgen05 M128 N128 K16, D / 16 steps
 //   P_i = 2^(S_i c - m_i c), c = log2(e) / sqrt(head_dim), masked, rounded to 16 bits
 //   O_i[pos][:] += P_i V                   tcgen05 M128 N(D) K16, 8 steps, P from tensor memory
-// Tensor memory holds S_0, S_1 (128 columns each, P_i over the first 32 of each 64) and
+// Tensor memory holds S_0, S_1 (128 columns each, P_i over the first 16 of each 32) and
 // O_0, O_1 (D each).
-//   * warps 0-7 and 8-15: the softmax of tile 0 and 1, 64 of a query's 128 keys per
-//     thread; the two warps that share 32 queries exchange their maxima through shared
-//     memory, 64 threads at a named barrier.  fp16's P
-//     carries a factor 2^7, which cancels in O / sum.  The
+//   * warps 0-15: the softmax of tile 0, then of tile 1, 32 of a query's 128 keys per
+//     thread; the four warps that share 32 queries exchange their maxima through shared
+//     memory, 128 threads at a named barrier.  All sixteen on one tile, because what
+//     counts is the time from a tile's scores to its P: the other tile's products (1024
+//     cycles at D = 128) are all there is to run meanwhile.  fp16's P carries a factor
+//     2^7, which cancels in O / sum.  The
 //     maximum m_i that scales P and O may lag the true one: O and the sum are rescaled
 //     only when it grew by more than 2^8 (P stays below 2^8, far from fp16's limit), so
 //     most blocks skip the pass over O.  The true maximum is kept beside it for LSE.
-//   * warp 16 (one lane issuing): per key block PV_0, S_0 of the next block,
-//     PV_1, S_1 of the next: while one tile's products run, the other's softmax does.
-//     The products of one thread run in order, so S_i may overwrite P_i behind PV_i.
-//   * warps 17 and 18 (one thread each): TMA copies of K (and Q tile 0) and V (and Q
+//   * warps 16 and 17 (one lane issuing): the products of tile 0 and 1, per key block PV,
+//     then S of the next block, in turns: while one tile's products run, the other's
+//     softmax does.  A warp's products run in order, so S may overwrite P behind PV; two
+//     warps, because a warp's waits otherwise stand between its products (2850 cycles per
+//     key block with one warp, of which 850 were waits).
+//   * warps 18 and 19 (one thread each): TMA copies of K (and Q tile 0) and V (and Q
 //     tile 1).
 // V rows past the sequence's end are zeroed in shared memory (other sequences' rows,
 // possibly with infinities); what is masked inside the sequence has P = 0, and if a
@@ -48,7 +52,7 @@ namespace {
 
 constexpr int kRows = 128;                     // queries per tile, keys per step
 constexpr uint32_t kHalf = kRows * 128;        // bytes of a [128][64] 16-bit half tile
-constexpr int kSoftWarps = 16, kMmaWarp = 16, kLoadWarp = 17;  // K, then V
+constexpr int kSoftWarps = 16, kMmaWarp = 16, kLoadWarp = 18;  // one for each tile; K, then V
 constexpr uint32_t kColS = 0, kColO = 256;     // + 128 i, + 128 i
 constexpr int kThreads = 32 * (kLoadWarp + 2);
 constexpr float kLag = 8.0f;                   // log2 of how far the scaling maximum may lag
@@ -74,7 +78,7 @@ struct FwdArgs {
 
 struct Ctl {
     uint64_t q_full[2], k_full[4], k_empty[4], v_full[4], v_empty[4];
-    uint64_t s_full[2], p_ready[2], o_full[2], mma_done;
+    uint64_t s_full[2], p_ready[2], o_full[2], turn[2], mma_done[2];
     uint32_t tmem_base;
     int abort_flag, bad[2];
 };
@@ -120,72 +124,60 @@ __device__ void role_load(const FwdArgs &p, Ctl &c, uint32_t smem, const Unit &u
         drain(su32(&full[q % C::kStages]), (uint32_t)((q / C::kStages) & 1), w);
 }
 
-// All products of the unit; returns early when aborting.
+// The products of tile i; returns early when aborting.  Iteration b: PV of key block b + 1, then S of block b.  The two
+// tiles' warps take turns iteration by iteration: one's products then run while the other's scores are in the softmax,
+// where without turns both would share the tensor core evenly and wait for their scores together.
 template <int D>
-__device__ __forceinline__ void issue_products(const FwdArgs &p, Ctl &c, uint32_t smem_, uint32_t tmem_, int len,
-                                               const Tile (&t)[2], int lo_, int hi_, int lane, const Waiter &w) {
+__device__ __forceinline__ void issue_products(const FwdArgs &p, Ctl &c, uint32_t smem, uint32_t tmem, int seq_end,
+                                               int first, int end, int lo, int hi, int i, int lane, const Waiter &w) {
     using C = Cfg<D>;
-    const uint32_t smem = uniform(smem_), tmem = uniform(tmem_);
-    const int lo = uniform(lo_), hi = uniform(hi_), seq_end = uniform(len);
-    const int first[2] = {uniform(t[0].lo), uniform(t[1].lo)}, end[2] = {uniform(t[0].hi), uniform(t[1].hi)};
-    int phase[2] = {0, 0};  // products PV issued of each tile
-    bool q_seen[2] = {false, false};
-    int it = 0;
-    // Iteration b: PV of block b + 1, then S of block b, tile by tile.
+    int done = 0;  // products PV issued
+    int ks = 0, vs = 0;
+    uint32_t kph = 0, vph = 0;
+    const uint32_t o_col = tmem + kColO + 128u * i, s_col = tmem + kColS + 128u * i;
+    const uint64_t qd = desc_k(smem + C::kOffQ + (uint32_t)i * C::kTile);
+    if (first < end && !wait_warp(su32(&c.q_full[i]), 0, w)) return;
+    uint32_t it = 0;
     for (int b = hi - 1; b >= lo - 1; --b, ++it) {
         const bool more = b >= lo, prev = b + 1 < hi;
-        const int ks = it % C::kStages, vs = (it - 1) % C::kStages;
-        if (more && !wait_warp(su32(&c.k_full[ks]), (uint32_t)((it / C::kStages) & 1), w)) return;
+        const bool pv = b + 1 >= first && b + 1 < end, sc = b >= first && b < end;
+        // The operands first: a wait costs about 100 cycles even for what is there, and these pass while the softmax works.
+        if (more && !wait_warp(su32(&c.k_full[ks]), kph, w)) return;
+        const uint32_t v = smem + C::kOffV + (uint32_t)vs * C::kTile;
         if (prev) {
-            if (!wait_warp(su32(&c.v_full[vs]), (uint32_t)(((it - 1) / C::kStages) & 1), w)) return;
+            if (!wait_warp(su32(&c.v_full[vs]), vph, w)) return;
             const int keys = seq_end - kRows * (b + 1);
-            if (keys < kRows) zero_rows(smem + C::kOffV + (uint32_t)vs * C::kTile, keys, kRows, C::kHalves, lane);
+            if (i == 0 && keys < kRows) zero_rows(v, keys, kRows, C::kHalves, lane);  // before the first turn that reads it
         }
+        if ((i == 1 || it > 0) && !wait_warp(su32(&c.turn[i]), (it + (uint32_t)i - 1u) & 1u, w)) return;
+        if (pv && !wait_warp(su32(&c.p_ready[i]), (uint32_t)(done & 1), w)) return;
         tc_after();
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            if (prev && b + 1 >= first[i] && b + 1 < end[i]) {
-                if (!wait_warp(su32(&c.p_ready[i]), (uint32_t)(phase[i] & 1), w)) return;
-                tc_after();
-                const uint64_t vd = desc_mn(smem + C::kOffV + (uint32_t)vs * C::kTile, kHalf, 1024u);
-                if (elect_one()) {
-#pragma unroll
-                    for (int k = 0; k < 8; ++k)  // A: 8 columns (16 keys) per step, 64 keys every 64; B: two groups of 8 keys
-                        tc_mma_f16_ts(tmem + kColO + 128u * i, tmem + kColS + 128u * i + 64u * (k / 4) + 8u * (k % 4), vd + 128u * k, p.idesc2,
-                                      phase[i] > 0 || k > 0);
-                    if (b + 1 == first[i]) tc_commit_to(su32(&c.o_full[i]));
-                }
-                ++phase[i];
-            }
-            if (more && b >= first[i] && b < end[i]) {
-                if (!q_seen[i] && !wait_warp(su32(&c.q_full[i]), 0, w)) return;
-                q_seen[i] = true;
-                const uint64_t qd = desc_k(smem + C::kOffQ + (uint32_t)i * C::kTile);
-                const uint64_t kd = desc_k(smem + C::kOffK + (uint32_t)ks * C::kTile);
-                if (elect_one()) {
-#pragma unroll
-                    for (int k = 0; k < D / 16; ++k) {  // +32 bytes of each row, then the next half
-                        const uint64_t step = 2u * (k % 4) + (uint64_t)(k / 4) * (kHalf >> 4);
-                        tc_mma_f16(tmem + kColS + 128u * i, qd + step, kd + step, p.idesc1, k > 0);
-                    }
-                    tc_commit_to(su32(&c.s_full[i]));
-                }
-            }
-        }
         if (elect_one()) {
+            if (pv) {
+                const uint64_t vd = desc_mn(v, kHalf, 1024u);
+#pragma unroll
+                for (int k = 0; k < 8; ++k)  // A: 8 columns (16 keys) per step, 32 keys every 32; B: two groups of 8 keys
+                    tc_mma_f16_ts(o_col, s_col + 32u * (k / 2) + 8u * (k % 2), vd + 128u * k, p.idesc2, done > 0 || k > 0);
+                if (b + 1 == first) tc_commit_to(su32(&c.o_full[i]));
+            }
             if (prev) tc_commit_to(su32(&c.v_empty[vs]));
+            if (sc) {
+                const uint64_t kd = desc_k(smem + C::kOffK + (uint32_t)ks * C::kTile);
+#pragma unroll
+                for (int k = 0; k < D / 16; ++k) {  // +32 bytes of each row, then the next half
+                    const uint64_t step = 2u * (k % 4) + (uint64_t)(k / 4) * (kHalf >> 4);
+                    tc_mma_f16(s_col, qd + step, kd + step, p.idesc1, k > 0);
+                }
+                tc_commit_to(su32(&c.s_full[i]));
+            }
             if (more) tc_commit_to(su32(&c.k_empty[ks]));
+            bar_arrive(su32(&c.turn[i ^ 1]));
         }
+        __syncwarp();
+        if (pv) ++done;
+        if (prev && ++vs == C::kStages) vs = 0, vph ^= 1u;
+        if (more && ++ks == C::kStages) ks = 0, kph ^= 1u;
     }
-}
-
-template <int D>
-__device__ void role_mma(const FwdArgs &p, Ctl &c, uint32_t smem, uint32_t tmem, const Unit &u, const Tile (&t)[2],
-                         int lo, int hi, int lane, const Waiter &w) {
-    issue_products<D>(p, c, smem, tmem, u.len, t, lo, hi, lane, w);
-    if (elect_one()) tc_commit_to(su32(&c.mma_done));  // nothing may still run when tensor memory is released
-    drain(su32(&c.mma_done), 0, w);
-    __syncwarp();
 }
 
 // 32 scores of one row, keys base .. base + 31: those outside [from, to] (relative to base) become -inf.
@@ -195,10 +187,14 @@ __device__ __forceinline__ void mask32(uint32_t (&v)[32], int from, int to) {
     for (int e = 0; e < 32; ++e)
         if (!(keep >> e & 1u)) v[e] = 0xFF800000u;
 }
+// The largest of m and 32 scores, in four chains.
 __device__ __forceinline__ float max32(const uint32_t (&v)[32], float m) {
+    float t[4] = {m, m, m, m};
 #pragma unroll
-    for (int e = 0; e < 32; e += 2) m = fmaxf(m, fmaxf(__uint_as_float(v[e]), __uint_as_float(v[e + 1])));
-    return m;
+    for (int e = 0; e < 32; e += 8)
+#pragma unroll
+        for (int z = 0; z < 4; ++z) t[z] = fmaxf(t[z], fmaxf(__uint_as_float(v[e + z]), __uint_as_float(v[e + z + 4])));
+    return fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3]));
 }
 // P of 32 scores: 2^(s c - mc), added to sum and packed two per word.
 template <bool F16>
@@ -213,77 +209,95 @@ __device__ __forceinline__ void exp32(const uint32_t (&v)[32], float cs, float m
     }
 }
 
-// The softmax of tile i.  `xch`: shared floats [2][64] of this pair of warps (both halves of a row, two turns).
+// The softmax of both tiles, one after the other for each key block.  `xch`: shared floats [2][4][32] of this warp's
+// rows (two turns, four quarters of a row).
 template <int D, bool F16>
-__device__ void role_soft(const FwdArgs &p, Ctl &c, uint32_t smem, uint32_t tmem, const Unit &u, const Tile &t, int i,
-                          int warp, int lane, float *xch, const Waiter &w) {
+__device__ void role_soft(const FwdArgs &p, Ctl &c, uint32_t smem, uint32_t tmem, const Unit &u, const Tile (&t)[2],
+                          int lo, int hi, int warp, int lane, float *xch, const Waiter &w) {
     using C = Cfg<D>;
-    const int quad = warp & 3, part = (warp >> 2) & 1, pair = 4 * i + quad, pos = t.p0 + 32 * quad + lane;
+    const int quad = warp & 3, part = warp >> 2;
     const uint32_t lane_tm = (uint32_t)(32 * quad) << 16;
-    const uint32_t s_tm = tmem + lane_tm + kColS + 128u * i + 64u * part;
-    const uint32_t p_tm = tmem + lane_tm + kColS + 128u * i + 64u * part;  // P: 32 columns over this warp's own scores
-    const uint32_t o_tm = tmem + lane_tm + kColO + 128u * i + (uint32_t)(D / 2) * part;
     const float cs = p.a.scale * 1.4426950408889634f;
-    float used = -INFINITY, top = -INFINITY;  // the maximum that scales, the true one
-    float2 sum = make_float2(0.f, 0.f);
-    auto meet = [&](float mine, int turn) {  // the other half's value of this row
-        xch[64 * turn + 32 * part + lane] = mine;
-        asm volatile("bar.sync %0, 64;" ::"r"(1 + pair) : "memory");
-        return xch[64 * turn + 32 * (part ^ 1) + lane];
-    };
-    int it = 0;
-    for (int b = t.hi - 1; b >= t.lo; --b, ++it) {
-        if (!wait_warp(su32(&c.s_full[i]), (uint32_t)(it & 1), w)) return;
-        tc_after();
-        const int base = kRows * b + 64 * part;
-        const bool whole = base + 63 <= t.p0 && (p.a.window == 0 || t.p0 + kRows - 1 < base + p.a.window);
-        uint32_t v0[32], v1[32];
-        tc_ld_32x32(s_tm, v0);
-        tc_ld_32x32(s_tm + 32, v1);
-        tc_wait_ld(v0);
-        tc_wait_ld(v1);
-        if (!whole) {
-            const int to = pos - base, from = p.a.window > 0 ? pos - p.a.window + 1 - base : 0;
-            mask32(v0, from, to), mask32(v1, from - 32, to - 32);
-        }
-        float m = max32(v1, max32(v0, top));
-        m = fmaxf(m, meet(m, it & 1));
-        top = m;
-        if (__any_sync(0xffffffffu, (m - used) * cs > kLag)) {  // the same for both halves
-            if (it > 0) {  // before the first product O holds nothing
-                const float keep = m == -INFINITY ? 1.f : fast_exp2((used - m) * cs);
-                sum.x *= keep, sum.y *= keep;
-#pragma unroll 1
-                for (int k = 0; k < D / 2; k += 16) {  // S of this block is behind PV of the last: O is complete
-                    uint32_t o[16];
-                    tc_ld_32x16(o_tm + k, o);
+    float used[2] = {-INFINITY, -INFINITY}, top[2] = {-INFINITY, -INFINITY};  // the maximum that scales, the true one
+    float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+    int it[2] = {0, 0}, turn = 0;
+    float others[3];
+    auto meet = [&](float mine) {  // the other quarters' values of this row
+        float *x = xch + 128 * turn;
+        turn ^= 1;
+        x[32 * part + lane] = mine;
+        asm volatile("bar.sync %0, 128;" ::"r"(1 + quad) : "memory");
 #pragma unroll
-                    for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * keep);
-                    tc_st_32x16(o_tm + k, o);
-                }
+        for (int z = 0; z < 3; ++z) others[z] = x[32 * ((part + 1 + z) & 3) + lane];
+    };
+    for (int b = hi - 1; b >= lo; --b) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            if (b < t[i].lo || b >= t[i].hi) continue;
+            if (!wait_warp(su32(&c.s_full[i]), (uint32_t)(it[i] & 1), w)) return;
+            tc_after();
+            const uint32_t s_tm = tmem + lane_tm + kColS + 128u * i + 32u * part;  // P: 16 columns over this warp's scores
+            const int base = kRows * b + 32 * part;
+            uint32_t v[32];
+            tc_ld_32x32(s_tm, v);
+            tc_wait_ld(v);
+            if (!(base + 31 <= t[i].p0 && (p.a.window == 0 || t[i].p0 + kRows - 1 < base + p.a.window))) {
+                const int pos = t[i].p0 + 32 * quad + lane;
+                mask32(v, p.a.window > 0 ? pos - p.a.window + 1 - base : 0, pos - base);
             }
-            used = m;
+            float m = max32(v, top[i]);
+            meet(m);
+            m = fmaxf(fmaxf(m, others[0]), fmaxf(others[1], others[2]));
+            top[i] = m;
+            if (__any_sync(0xffffffffu, (m - used[i]) * cs > kLag)) {  // the same in the four warps of these rows
+                if (it[i] > 0) {  // before the first product O holds nothing
+                    const float keep = m == -INFINITY ? 1.f : fast_exp2((used[i] - m) * cs);
+                    const uint32_t o_tm = tmem + lane_tm + kColO + 128u * i + (uint32_t)(D / 4) * part;
+                    sum[i].x *= keep, sum[i].y *= keep;
+#pragma unroll 1
+                    for (int k = 0; k < D / 4; k += 16) {  // S of this block is behind PV of the last: O is complete
+                        uint32_t o[16];
+                        tc_ld_32x16(o_tm + k, o);
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * keep);
+                        tc_st_32x16(o_tm + k, o);
+                    }
+                }
+                used[i] = m;
+            }
+            uint32_t pk[16];
+            exp32<F16>(v, cs, (used[i] == -INFINITY ? 0.f : used[i] * cs) - (F16 ? kShift16 : 0.f), sum[i], pk);
+            tc_st_32x16(s_tm, pk);
+            tc_wait_st();
+            tc_before();
+            __syncwarp();
+            if (lane == 0) bar_arrive(su32(&c.p_ready[i]));
+            ++it[i];
         }
-        const float mc = (used == -INFINITY ? 0.f : used * cs) - (F16 ? kShift16 : 0.f);
-        uint32_t pk[16];
-        exp32<F16>(v0, cs, mc, sum, pk);
-        tc_st_32x16(p_tm, pk);
-        exp32<F16>(v1, cs, mc, sum, pk);
-        tc_st_32x16(p_tm + 16, pk);
-        tc_wait_st();
-        tc_before();
-        __syncwarp();
-        if (lane == 0) bar_arrive(su32(&c.p_ready[i]));
     }
-    const float mine = sum.x + sum.y, total = mine + meet(mine, it & 1);
+    float total[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        total[i] = sum[i].x + sum[i].y;
+        meet(total[i]);
+        // In the quarters' order, whichever this warp has: the four warps get the same sum.
+        const float a[4] = {total[i], others[0], others[1], others[2]};
+        total[i] = (a[(4 - part) & 3] + a[(5 - part) & 3]) + (a[(6 - part) & 3] + a[(7 - part) & 3]);
+    }
+    // Now warps 0-7 finish tile 0 and 8-15 tile 1, D / 2 columns each: O rows through this warp's part of the Q tile,
+    // read by then.
+    const int i = warp >> 3, half = (warp >> 2) & 1;
+    const Tile own = i ? t[1] : t[0];
+    if (!own.live) return;
+    const float all = i ? total[1] : total[0], was = i ? used[1] : used[0], best = i ? top[1] : top[0];
     if (!wait_warp(su32(&c.o_full[i]), 0, w)) return;
     tc_after();
-    // O rows (this warp's D / 2 columns) through its part of the Q tile, read by then.
     constexpr int W = D / 2, kChunks = W / 8;  // 16-byte chunk j of row r lies at j ^ (r & 7), of 64-byte rows at j ^ (r / 2 & 3)
     auto place = [](int r, int j) { return (uint32_t)((kChunks == 4 ? j ^ ((r >> 1) & 3) : j ^ (r & 7)) << 4); };
-    const float inv = 1.0f / total;
+    const float inv = 1.0f / all;
+    const uint32_t o_tm = tmem + lane_tm + kColO + 128u * i + (uint32_t)W * half;
     const uint32_t stage = smem + C::kOffQ + (uint32_t)i * C::kTile + (uint32_t)(warp & 7) * (C::kTile / 8);
-    const bool row_live = 32 * quad + lane < t.live;
+    const bool row_live = 32 * quad + lane < own.live;
     float2 odd = make_float2(0.f, 0.f);  // 0 as long as every value is finite
 #pragma unroll
     for (int k = 0; k < W / 32; ++k) {
@@ -297,19 +311,19 @@ __device__ void role_soft(const FwdArgs &p, Ctl &c, uint32_t smem, uint32_t tmem
                    o[4 * j + 3]);
     }
     if (__any_sync(0xffffffffu, row_live && !(odd.x + odd.y == 0.f)) && lane == 0) c.bad[i] = 1;
-    const int64_t row0 = (int64_t)u.begin + t.p0 + 32 * quad;
-    if (row_live && part == 0) {
-        // The sum is relative to `used`; LSE wants it relative to the true maximum.
+    const int64_t row0 = (int64_t)u.begin + own.p0 + 32 * quad;
+    if (row_live && half == 0) {
+        // The sum is relative to the maximum in use; LSE wants it relative to the true one.
         const float ln2 = 0.6931471805599453f;
-        const float l = logf(total) - ((top - used) * cs + (F16 ? kShift16 : 0.f)) * ln2;
-        float *st = p.a.lse + ((row0 + lane) * p.a.nh + t.head) * 2;
-        st[0] = top * p.a.scale, st[1] = l;
+        const float l = logf(all) - ((best - was) * cs + (F16 ? kShift16 : 0.f)) * ln2;
+        float *st = p.a.lse + ((row0 + lane) * p.a.nh + own.head) * 2;
+        st[0] = best * p.a.scale, st[1] = l;
     }
     __syncwarp();
-    uint16_t *out = static_cast<uint16_t *>(p.a.out) + (row0 * p.a.nh + t.head) * p.a.hd + W * part;
+    uint16_t *out = static_cast<uint16_t *>(p.a.out) + (row0 * p.a.nh + own.head) * p.a.hd + W * half;
     const int j = lane % kChunks;
     for (int r = lane / kChunks; r < 32; r += 32 / kChunks) {
-        if (32 * quad + r >= t.live || W * part + 8 * j >= p.a.hd) continue;
+        if (32 * quad + r >= own.live || W * half + 8 * j >= p.a.hd) continue;
         const uint4 x = lds128(stage + (uint32_t)r * (2 * W) + place(r, j));
         *reinterpret_cast<uint4 *>(out + (int64_t)r * p.a.nh * p.a.hd + 8 * j) = x;
     }
@@ -367,20 +381,21 @@ __global__ void __launch_bounds__(kThreads, 1) forward_tc_kernel(const __grid_co
     Ctl &c = *reinterpret_cast<Ctl *>(smem_raw + (smem - su32(smem_raw)));
     const int warp = uniform((int)(threadIdx.x >> 5)), lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
-        bar_init(su32(&c.mma_done), 1);
         c.abort_flag = 0;
     } else if (warp == 0) {
         if (lane <= 4) {
             bar_init(su32(&c.k_full[lane - 1]), 1);
-            bar_init(su32(&c.k_empty[lane - 1]), 1);
+            bar_init(su32(&c.k_empty[lane - 1]), 2);
         } else if (lane <= 8) {
             bar_init(su32(&c.v_full[lane - 5]), 1);
-            bar_init(su32(&c.v_empty[lane - 5]), 1);
+            bar_init(su32(&c.v_empty[lane - 5]), 2);
         } else if (lane <= 10) {
             bar_init(su32(&c.q_full[lane - 9]), 1);
             bar_init(su32(&c.s_full[lane - 9]), 1);
-            bar_init(su32(&c.p_ready[lane - 9]), 8);
+            bar_init(su32(&c.p_ready[lane - 9]), kSoftWarps);
             bar_init(su32(&c.o_full[lane - 9]), 1);
+            bar_init(su32(&c.turn[lane - 9]), 1);
+            bar_init(su32(&c.mma_done[lane - 9]), 1);
             c.bad[lane - 9] = 0;
         }
     } else if (threadIdx.x < 35) {
@@ -417,12 +432,16 @@ __global__ void __launch_bounds__(kThreads, 1) forward_tc_kernel(const __grid_co
             const int lo = t[1].live && t[1].lo < t[0].lo ? t[1].lo : t[0].lo;
             const int hi = t[1].hi > t[0].hi ? t[1].hi : t[0].hi;
             if (warp < kSoftWarps) {
-                const int i = warp >> 3;
+                float *xch = reinterpret_cast<float *>(reinterpret_cast<uint8_t *>(&c) + 1024) + 256 * (warp & 3);
+                role_soft<D, F16>(p, c, smem, tmem, u, t, lo, hi, warp, lane, xch, w);
+            } else if (warp < kLoadWarp) {
+                const int i = warp - kMmaWarp;
                 const Tile own = i ? t[1] : t[0];
-                float *xch = reinterpret_cast<float *>(reinterpret_cast<uint8_t *>(&c) + 1024) + 128 * (4 * i + (warp & 3));
-                if (own.live) role_soft<D, F16>(p, c, smem, tmem, u, own, i, warp, lane, xch, w);
-            } else if (warp == kMmaWarp) {
-                role_mma<D>(p, c, smem, tmem, u, t, lo, hi, lane, w);
+                issue_products<D>(p, c, uniform(smem), uniform(tmem), uniform(u.len), uniform(own.lo), uniform(own.hi),
+                                  uniform(lo), uniform(hi), i, lane, w);
+                if (elect_one()) tc_commit_to(su32(&c.mma_done[i]));  // nothing may still run when tensor memory is released
+                drain(su32(&c.mma_done[i]), 0, w);
+                __syncwarp();
             } else {
                 const int tensor = warp - kLoadWarp;
                 if (lane == 0) role_load<D>(p, c, smem, u, tensor ? t[1] : t[0], g, lo, hi, tensor, w);
