@@ -13,14 +13,14 @@
 // Tensor memory holds S_0, S_1 (128 columns each, P_i over the first 16 of each 32) and
 // O_0, O_1 (D each).
 //   * warps 0-15: the softmax of tile 0, then of tile 1, 32 of a query's 128 keys per
-//     thread; the four warps that share 32 queries exchange their maxima through shared
-//     memory, 128 threads at a named barrier.  All sixteen on one tile, because what
+//     thread; the four warps that share 32 queries meet at a named barrier.  All sixteen on one tile, because what
 //     counts is the time from a tile's scores to its P: the other tile's products (1024
 //     cycles at D = 128) are all there is to run meanwhile.  fp16's P carries a factor
 //     2^7, which cancels in O / sum.  The
 //     maximum m_i that scales P and O may lag the true one: O and the sum are rescaled
-//     only when it grew by more than 2^8 (P stays below 2^8, far from fp16's limit), so
-//     most blocks skip the pass over O.  The true maximum is kept beside it for LSE.
+//     only when a score is above it by more than 2^8 (P stays below 2^8, far from fp16's
+//     limit), so most blocks skip the pass over O, and P can be formed before the four
+//     warps of a row have compared their maxima.  The true one is kept beside it for LSE.
 //   * warps 16 and 17 (one lane issuing): the products of tile 0 and 1, per key block PV,
 //     then S of the next block, in turns: while one tile's products run, the other's
 //     softmax does.  A warp's products run in order, so S may overwrite P behind PV; two
@@ -209,6 +209,17 @@ __device__ __forceinline__ void exp32(const uint32_t (&v)[32], float cs, float m
     }
 }
 
+// Whether `x` holds in any of the 128 threads that meet at named barrier `id`.
+__device__ __forceinline__ bool any_of_quad(bool x, int id) {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %2, 0;\n\tbar.red.or.pred q, %1, 128, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(r)
+        : "r"(id), "r"((uint32_t)x)
+        : "memory");
+    return r != 0;
+}
+
 // The softmax of both tiles, one after the other for each key block.  `xch`: shared floats [2][4][32] of this warp's
 // rows (two turns, four quarters of a row).
 template <int D, bool F16>
@@ -218,7 +229,7 @@ __device__ void role_soft(const FwdArgs &p, Ctl &c, uint32_t smem, uint32_t tmem
     const int quad = warp & 3, part = warp >> 2;
     const uint32_t lane_tm = (uint32_t)(32 * quad) << 16;
     const float cs = p.a.scale * 1.4426950408889634f;
-    float used[2] = {-INFINITY, -INFINITY}, top[2] = {-INFINITY, -INFINITY};  // the maximum that scales, the true one
+    float used[2] = {-INFINITY, -INFINITY}, top[2] = {-INFINITY, -INFINITY};  // the maximum that scales, this quarter's own
     float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
     int it[2] = {0, 0}, turn = 0;
     float others[3];
@@ -245,13 +256,27 @@ __device__ void role_soft(const FwdArgs &p, Ctl &c, uint32_t smem, uint32_t tmem
                 const int pos = t[i].p0 + 32 * quad + lane;
                 mask32(v, p.a.window > 0 ? pos - p.a.window + 1 - base : 0, pos - base);
             }
-            float m = max32(v, top[i]);
-            meet(m);
-            m = fmaxf(fmaxf(m, others[0]), fmaxf(others[1], others[2]));
-            top[i] = m;
-            if (__any_sync(0xffffffffu, (m - used[i]) * cs > kLag)) {  // the same in the four warps of these rows
+            const float m = max32(v, -INFINITY);
+            top[i] = fmaxf(top[i], m);
+            uint32_t pk[16];
+            float2 part_sum = make_float2(0.f, 0.f);
+            auto probs = [&] {
+                part_sum = make_float2(0.f, 0.f);
+                exp32<F16>(v, cs, (used[i] == -INFINITY ? 0.f : used[i] * cs) - (F16 ? kShift16 : 0.f), part_sum, pk);
+            };
+            // P with the maximum in use, before it is known whether that still does: the four warps' answers then meet
+            // at a barrier that the exponentials have covered.
+            bool far = it[i] == 0;
+            if (!far) {
+                probs();
+                far = any_of_quad((m - used[i]) * cs > kLag, 1 + quad);
+            }
+            if (far) {
+                float now = fmaxf(m, used[i]);
+                meet(now);
+                now = fmaxf(fmaxf(now, others[0]), fmaxf(others[1], others[2]));
                 if (it[i] > 0) {  // before the first product O holds nothing
-                    const float keep = m == -INFINITY ? 1.f : fast_exp2((used[i] - m) * cs);
+                    const float keep = now == -INFINITY ? 1.f : fast_exp2((used[i] - now) * cs);
                     const uint32_t o_tm = tmem + lane_tm + kColO + 128u * i + (uint32_t)(D / 4) * part;
                     sum[i].x *= keep, sum[i].y *= keep;
 #pragma unroll 1
@@ -263,10 +288,10 @@ __device__ void role_soft(const FwdArgs &p, Ctl &c, uint32_t smem, uint32_t tmem
                         tc_st_32x16(o_tm + k, o);
                     }
                 }
-                used[i] = m;
+                used[i] = now;
+                probs();
             }
-            uint32_t pk[16];
-            exp32<F16>(v, cs, (used[i] == -INFINITY ? 0.f : used[i] * cs) - (F16 ? kShift16 : 0.f), sum[i], pk);
+            sum[i] = __fadd2_rn(sum[i], part_sum);
             tc_st_32x16(s_tm, pk);
             tc_wait_st();
             tc_before();
@@ -278,6 +303,8 @@ __device__ void role_soft(const FwdArgs &p, Ctl &c, uint32_t smem, uint32_t tmem
     float total[2];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
+        meet(top[i]);
+        top[i] = fmaxf(fmaxf(top[i], others[0]), fmaxf(others[1], others[2]));
         total[i] = sum[i].x + sum[i].y;
         meet(total[i]);
         // In the quarters' order, whichever this warp has: the four warps get the same sum.
