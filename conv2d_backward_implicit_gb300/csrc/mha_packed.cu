@@ -7,13 +7,29 @@
 
 namespace mhapk {
 
-unsigned take_simt_error(cudaError_t &e);
+__device__ unsigned int g_simt_error_word = 0;
+
 unsigned take_fwd_error(cudaError_t &e);
 unsigned take_bwd_error(cudaError_t &e);
 
 namespace {
 
 std::atomic<int> g_kernel_choice{DGRAD_KERNEL_AUTO};
+
+unsigned take_simt_error(cudaError_t &e) {
+    unsigned int word = 0;
+    const unsigned int zero = 0;
+    if (e == cudaSuccess) e = cudaMemcpyFromSymbol(&word, g_simt_error_word, sizeof(word));
+    if (e == cudaSuccess && word) e = cudaMemcpyToSymbol(g_simt_error_word, &zero, sizeof(zero));
+    return word;
+}
+
+int run_simt(SimtLauncher *f32, SimtLauncher *bf16, SimtLauncher *f16, const Args &a, const mha_packed_params *p,
+             int dtype, cudaStream_t st) {
+    void *error = nullptr;
+    if (cudaGetSymbolAddress(&error, g_simt_error_word) != cudaSuccess) return DGRAD_ERR_CUDA;
+    return (dtype == DGRAD_F32 ? f32 : dtype == DGRAD_BF16 ? bf16 : f16)(a, p, static_cast<unsigned *>(error), st);
+}
 
 bool aligned(const void *ptr, uintptr_t a) { return (reinterpret_cast<uintptr_t>(ptr) & (a - 1)) == 0; }
 
@@ -35,7 +51,7 @@ int validate(const mha_packed_params *p, int dtype) {
         row_of(p->v_stride, p->num_kv_heads, p->head_dim) < kd)
         return DGRAD_ERR_SHAPE;
     // Thread blocks of the smallest tile (32 rows) and most heads; also the warps of the delta kernel.
-    if (unit_bound(p, 32) * p->num_heads > INT32_MAX || (int64_t)p->tokens * p->num_heads / 8 > INT32_MAX)
+    if (unit_bound(p, 32) * (2 * (int64_t)p->num_heads + 8) > INT32_MAX || (int64_t)p->tokens * p->num_heads / 8 > INT32_MAX)
         return DGRAD_ERR_UNSUPPORTED;
     return DGRAD_OK;
 }
@@ -105,7 +121,8 @@ int mha_packed_forward(const void *q, const void *k, const void *v, const int32_
     a.out = o;
     a.lse = lse;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    return kern == DGRAD_KERNEL_TC ? forward_tc(a, p, dtype, st) : forward_simt(a, p, dtype, st);
+    if (kern == DGRAD_KERNEL_TC) return forward_tc(a, p, dtype, st);
+    return run_simt(forward_simt_f32, forward_simt_bf16, forward_simt_f16, a, p, dtype, st);
 }
 
 size_t mha_packed_workspace_size(const mha_packed_params *p, int dtype) {
@@ -130,7 +147,7 @@ int mha_packed_backward(const void *q, const void *k, const void *v, const void 
     a.stats = reinterpret_cast<float2 *>(static_cast<char *>(workspace) + kHeader);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     if (kern == DGRAD_KERNEL_TC) return backward_tc(a, static_cast<unsigned *>(workspace), p, dtype, st);
-    return backward_simt(a, p, dtype, st);
+    return run_simt(backward_simt_f32, backward_simt_bf16, backward_simt_f16, a, p, dtype, st);
 }
 
 int mha_packed_forward_select_kernel(const void *q, const void *k, const void *v, const void *o,

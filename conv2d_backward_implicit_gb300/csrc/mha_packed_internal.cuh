@@ -167,10 +167,12 @@ __device__ __forceinline__ float warp_sum(float x) {
     return x;
 }
 
-// Forward: one launcher per kernel family; all return a dgrad_status.
-int forward_simt(const Args &a, const mha_packed_params *p, int dtype, cudaStream_t st);
+// One launcher per kernel family; all return a dgrad_status.  `error`: the device address of the CUDA-core kernels'
+// error word; the tensor-core translation units have their own.
+using SimtLauncher = int(const Args &a, const mha_packed_params *p, unsigned *error, cudaStream_t st);
+SimtLauncher forward_simt_f32, forward_simt_bf16, forward_simt_f16, backward_simt_f32, backward_simt_bf16,
+    backward_simt_f16;
 int forward_tc(const Args &a, const mha_packed_params *p, int dtype, cudaStream_t st);
-int backward_simt(const Args &a, const mha_packed_params *p, int dtype, cudaStream_t st);
 int backward_tc(const Args &a, unsigned *norms, const mha_packed_params *p, int dtype, cudaStream_t st);
 
 }  // namespace mhapk

@@ -1,0 +1,455 @@
+// mha_packed_simt.cuh -- CUDA-core kernels of causal attention over packed
+// sequences (include/mha_packed.h): every type, any head_dim up to 256, float32
+// throughout.  Included once per element type.
+//
+// Both directions: blocks of 128 threads, 32 resident rows against streamed tiles of 64
+// rows.  Thread (ty, tx) of an 8 x 16 grid owns resident rows 4 ty .. 4 ty + 3 and
+// streamed rows tx + 16 j of the 32 x 64 products, and of the accumulated sums the same
+// resident rows and elements 2 tx + 32 c, 2 tx + 32 c + 1 -- four rows by four, so that
+// shared memory feeds the fused multiply-adds (packed two by two) at their rate.  32
+// rows a block, because these kernels serve small problems and odd shapes, where the
+// number of blocks is what there is least of.
+//
+// Forward: queries resident; K and V pass through; a query's statistics live in the 16
+// lanes of a half-warp, and the running maximum and sum of the softmax make it one pass.
+//
+// Backward, one kernel for both directions of the pair of products:
+//   s = R1 X1^T, dp = R2 X2^T, p and ds from the statistics,
+//   acc1 += ds X1, and with keys resident also acc2 += p X2;
+// queries resident (R = Q, dO; X = K, V) give dQ, keys resident (R = K, V; X = Q, dO)
+// give dK and dV.  Scores are formed twice, which costs 7 products in place of 5 but
+// needs no atomics: results do not change from run to run.  With keys resident the heads
+// of a group are dealt to the blocks of a cluster (up to 8), which add up their sums
+// through distributed shared memory in the heads' order.
+//
+// A masked pair has p = ds = 0, and in tiles that the mask crosses its products are
+// left out instead of multiplied by zero: infinities and NaN in rows that a query does
+// not attend stay out of its results.
+#pragma once
+
+#include <cooperative_groups.h>
+
+#include "mha_packed_internal.cuh"
+
+namespace mhapk {
+namespace {
+
+constexpr int kThreads = 128, kRes = 32, kStr = 64;  // threads, resident rows, streamed rows
+constexpr int kP = kStr + 4;                         // pitch of the 32 x 64 products
+
+// rows [0, ROWS) of a head into shared memory as float32, zero past `live` rows and past hd.
+template <typename T, int ROWS, int D>
+__device__ __forceinline__ void load_tile(float *dst, const T *src, int64_t stride, int live, int hd) {
+    constexpr int P = D + 4;
+    constexpr int V = 16 / sizeof(T);  // elements of a 16-byte load
+    if (hd % V == 0 && stride % V == 0 && (reinterpret_cast<uintptr_t>(src) & 15u) == 0) {
+#pragma unroll 4
+        for (int e = threadIdx.x; e < ROWS * (D / V); e += kThreads) {
+            const int r = e / (D / V), d = (e - r * (D / V)) * V;
+            uint4 w = make_uint4(0, 0, 0, 0);
+            if (r < live && d < hd) w = __ldg(reinterpret_cast<const uint4 *>(src + (int64_t)r * stride + d));
+            const T *h = reinterpret_cast<const T *>(&w);
+#pragma unroll
+            for (int i = 0; i < V; i += 4)
+                *reinterpret_cast<float4 *>(dst + r * P + d + i) =
+                    make_float4(to_f(h[i]), to_f(h[i + 1]), to_f(h[i + 2]), to_f(h[i + 3]));
+        }
+    } else {
+#pragma unroll 4
+        for (int e = threadIdx.x; e < ROWS * D; e += kThreads) {
+            const int r = e / D, d = e - r * D;
+            dst[r * P + d] = r < live && d < hd ? to_f(src[(int64_t)r * stride + d]) : 0.f;
+        }
+    }
+}
+
+// out[i][j] = sum over d of a[4 ty + i][d] b[tx + 16 j][d].
+template <int D>
+__device__ __forceinline__ void score_tile(const float *a, const float *b, int ty, int tx, float (&out)[4][4]) {
+    constexpr int P = D + 4;
+    float2 acc[4][4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) acc[i][j] = make_float2(0.f, 0.f);
+#pragma unroll 2
+    for (int d = 0; d < D; d += 4) {
+        float4 x[4], y[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[i] = *reinterpret_cast<const float4 *>(a + (4 * ty + i) * P + d);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) y[j] = *reinterpret_cast<const float4 *>(b + (tx + 16 * j) * P + d);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                acc[i][j] = __ffma2_rn(make_float2(x[i].x, x[i].y), make_float2(y[j].x, y[j].y), acc[i][j]);
+                acc[i][j] = __ffma2_rn(make_float2(x[i].z, x[i].w), make_float2(y[j].z, y[j].w), acc[i][j]);
+            }
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) out[i][j] = acc[i][j].x + acc[i][j].y;
+}
+
+// acc[i][c] += sum over t of p[4 ty + i][t] x[t][2 tx + 32 c ..]; SKIP leaves out terms with p = 0.
+template <int D, bool SKIP>
+__device__ __forceinline__ void add_tile(const float *p, const float *x, int ty, int tx, float2 (&acc)[4][D / 32]) {
+    constexpr int P = D + 4;
+#pragma unroll 2
+    for (int t = 0; t < kStr; t += 4) {
+        float4 w[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w[i] = *reinterpret_cast<const float4 *>(p + (4 * ty + i) * kP + t);
+#pragma unroll
+        for (int z = 0; z < 4; ++z)
+#pragma unroll
+            for (int c = 0; c < D / 32; ++c) {
+                const float2 y = *reinterpret_cast<const float2 *>(x + (t + z) * P + 2 * tx + 32 * c);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float f = z == 0 ? w[i].x : z == 1 ? w[i].y : z == 2 ? w[i].z : w[i].w;
+                    if (!SKIP || f != 0.f) acc[i][c] = __ffma2_rn(make_float2(f, f), y, acc[i][c]);
+                }
+            }
+    }
+}
+
+template <typename T, int D>
+__device__ __forceinline__ void store_rows(T *dst, int64_t stride, int ty, int tx, int live, int hd,
+                                           const float2 (&acc)[4][D / 32], const float (&factor)[4]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int r = 4 * ty + i;
+        if (r >= live) continue;
+#pragma unroll
+        for (int c = 0; c < D / 32; ++c) {
+            const int d = 2 * tx + 32 * c;
+            if (d < hd) dst[(int64_t)r * stride + d] = from_f<T>(acc[i][c].x * factor[i]);
+            if (d + 1 < hd) dst[(int64_t)r * stride + d + 1] = from_f<T>(acc[i][c].y * factor[i]);
+        }
+    }
+}
+
+__device__ __forceinline__ float half_warp_max(float x) {
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
+    return x;
+}
+__device__ __forceinline__ float half_warp_sum(float x) {
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+    return x;
+}
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kThreads) forward_simt_kernel(const Args a, unsigned *error) {
+    constexpr int P = D + 4;
+    extern __shared__ float4 sm4[];
+    float *q_s = reinterpret_cast<float *>(sm4), *k_s = q_s + kRes * P, *v_s = k_s + kStr * P, *p_s = v_s + kStr * P;
+    if (threadIdx.x == 0) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int ty = threadIdx.x >> 4, tx = threadIdx.x & 15;
+    const int h = (int)(blockIdx.x % (unsigned)a.nh), g = h / a.hpk;
+    const Unit u = find_unit(a, blockIdx.x / (unsigned)a.nh, 5, true, blockIdx.x == 0, error);
+    if (!u.live) return;
+    const int live = u.len - u.p0 < kRes ? u.len - u.p0 : kRes;
+    const int64_t row0 = (int64_t)u.begin + u.p0;
+    T *out = static_cast<T *>(a.out) + (row0 * a.nh + h) * a.hd;
+    float2 acc[4][D / 32];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int c = 0; c < D / 32; ++c) acc[i][c] = make_float2(0.f, 0.f);
+    float top[4], sum[4], factor[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) top[i] = -INFINITY, sum[i] = 0.f, factor[i] = 0.f;
+    if (u.pad) {
+        store_rows<T, D>(out, (int64_t)a.nh * a.hd, ty, tx, live, a.hd, acc, factor);
+        if (threadIdx.x < live) {
+            float *l = a.lse + ((row0 + threadIdx.x) * a.nh + h) * 2;
+            l[0] = 0.f, l[1] = INFINITY;
+        }
+        return;
+    }
+    load_tile<T, kRes, D>(q_s, static_cast<const T *>(a.q) + row0 * a.qs + (int64_t)h * a.hd, a.qs, live, a.hd);
+    const int last = u.p0 + live - 1;
+    int first = 0;
+    if (a.window > 0 && u.p0 - a.window + 1 > 0) first = (u.p0 - a.window + 1) / kRes * kRes;
+    for (int t0 = first; t0 <= last; t0 += kStr) {
+        // Keys past the tile's last query are masked for all of it: they need not be read.
+        const int keys = last + 1 - t0 < kStr ? last + 1 - t0 : kStr;
+        const int64_t t_row = (int64_t)u.begin + t0;
+        __syncthreads();  // the last step's tiles are read
+        load_tile<T, kStr, D>(k_s, static_cast<const T *>(a.k) + t_row * a.ks + (int64_t)g * a.hd, a.ks, keys, a.hd);
+        load_tile<T, kStr, D>(v_s, static_cast<const T *>(a.v) + t_row * a.vs + (int64_t)g * a.hd, a.vs, keys, a.hd);
+        __syncthreads();
+        float s[4][4];
+        score_tile<D>(q_s, k_s, ty, tx, s);
+        const bool whole = t0 + kStr - 1 <= u.p0 && (a.window == 0 || u.p0 + kRes - 1 < t0 + a.window);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int pos = u.p0 + 4 * ty + i;
+            float m = -INFINITY;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int t = t0 + tx + 16 * j;
+                const bool in = whole || (t <= pos && (a.window == 0 || pos - t < a.window));
+                s[i][j] = in ? s[i][j] * a.scale : -INFINITY;
+                m = fmaxf(m, s[i][j]);
+            }
+            m = half_warp_max(m);
+            const float now = fmaxf(top[i], m);
+            // A row whose keys so far are all masked keeps sum 0 and factor 1.
+            const float keep = now == -INFINITY ? 1.f : expf(top[i] - now);
+            float part = 0.f;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int t = t0 + tx + 16 * j;
+                const bool in = whole || (t <= pos && (a.window == 0 || pos - t < a.window));
+                const float e = in ? expf(s[i][j] - now) : 0.f;
+                part += e;
+                p_s[(4 * ty + i) * kP + tx + 16 * j] = e;
+            }
+            sum[i] = sum[i] * keep + half_warp_sum(part);
+            top[i] = now;
+#pragma unroll
+            for (int c = 0; c < D / 32; ++c) acc[i][c] = __fmul2_rn(acc[i][c], make_float2(keep, keep));
+        }
+        __syncwarp();  // a warp's eight rows of p are its own
+        if (whole)
+            add_tile<D, false>(p_s, v_s, ty, tx, acc);
+        else
+            add_tile<D, true>(p_s, v_s, ty, tx, acc);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        factor[i] = 1.0f / sum[i];
+        if (tx == 0 && 4 * ty + i < live) {
+            float *l = a.lse + ((row0 + 4 * ty + i) * a.nh + h) * 2;
+            l[0] = top[i], l[1] = logf(sum[i]);
+        }
+    }
+    store_rows<T, D>(out, (int64_t)a.nh * a.hd, ty, tx, live, a.hd, acc, factor);
+}
+
+// delta = dO . O of every row and head into stats[h][row].y; one warp per row and head.
+template <typename T>
+__global__ void __launch_bounds__(256) delta_simt_kernel(const Args a) {
+    if (threadIdx.x == 0) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int64_t w = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
+    if (w >= (int64_t)a.tokens * a.nh) return;
+    const T *o = static_cast<const T *>(a.o) + w * a.hd, *go = static_cast<const T *>(a.go) + w * a.hd;
+    float s = 0.f;
+    for (int d = threadIdx.x & 31; d < a.hd; d += 32) s = fmaf(to_f(o[d]), to_f(go[d]), s);
+    s = warp_sum(s);
+    if ((threadIdx.x & 31) == 0) a.stats[(w % a.nh) * a.tokens + w / a.nh].y = s;
+}
+
+// The step (streamed tile at c0, query head h): accumulates into acc1 and, with KEYS, acc2.
+template <typename T, int D, bool KEYS>
+__device__ __forceinline__ void backward_unit(const Args &a, unsigned block, unsigned *error, int split, float *sm) {
+    constexpr int P = D + 4;
+    float *r1 = sm, *r2 = r1 + kRes * P, *x1 = r2 + kRes * P, *x2 = x1 + kStr * P;
+    float *ds_s = x2 + kStr * P, *p_s = ds_s + kRes * kP;
+    const int ty = threadIdx.x >> 4, tx = threadIdx.x & 15;
+    // With keys resident, `split` blocks of a cluster share a unit: rank z has heads z, z + split, .. of the group.
+    const unsigned heads = KEYS ? a.nkv : a.nh, rank = KEYS ? block % (unsigned)split : 0u;
+    if (KEYS) block /= (unsigned)split;
+    const int head = (int)(block % heads), g = KEYS ? head : head / a.hpk;
+    const Unit u = find_unit(a, block / heads, 5, !KEYS, KEYS && block == 0 && rank == 0, error);
+    const int live = !u.live ? 0 : u.len - u.p0 < kRes ? u.len - u.p0 : kRes;
+    const int64_t row0 = (int64_t)u.begin + u.p0;
+    float2 acc1[4][D / 32], acc2[4][D / 32];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int c = 0; c < D / 32; ++c) acc1[i][c] = acc2[i][c] = make_float2(0.f, 0.f);
+    if (u.live && !u.pad) {
+        if (KEYS) {
+            load_tile<T, kRes, D>(r1, static_cast<const T *>(a.k) + row0 * a.ks + (int64_t)g * a.hd, a.ks, live, a.hd);
+            load_tile<T, kRes, D>(r2, static_cast<const T *>(a.v) + row0 * a.vs + (int64_t)g * a.hd, a.vs, live, a.hd);
+        } else {
+            load_tile<T, kRes, D>(r1, static_cast<const T *>(a.q) + row0 * a.qs + (int64_t)head * a.hd, a.qs, live, a.hd);
+            load_tile<T, kRes, D>(r2, static_cast<const T *>(a.go) + (row0 * a.nh + head) * a.hd, (int64_t)a.nh * a.hd,
+                                  live, a.hd);
+        }
+        // Streamed rows [lo, hi) of the sequence: the queries that reach these keys, or the keys these queries reach.
+        int lo = 0, hi = u.p0 + live;
+        if (KEYS) {
+            lo = u.p0, hi = u.len;
+            if (a.window > 0 && u.p0 + live - 1 < u.len - a.window) hi = u.p0 + live - 1 + a.window;
+        } else if (a.window > 0 && u.p0 - a.window + 1 > 0) {
+            lo = (u.p0 - a.window + 1) / kRes * kRes;
+        }
+        for (int c0 = lo; c0 < hi; c0 += kStr)
+            for (int r = KEYS ? (int)rank : 0; r < (KEYS ? a.hpk : 1); r += KEYS ? split : 1) {
+                const int h = KEYS ? g * a.hpk + r : head;
+                const int cols = hi - c0 < kStr ? hi - c0 : kStr;
+                const int64_t c_row = (int64_t)u.begin + c0;
+                __syncthreads();  // the last step's tiles are read
+                if (KEYS) {
+                    load_tile<T, kStr, D>(x1, static_cast<const T *>(a.q) + c_row * a.qs + (int64_t)h * a.hd, a.qs, cols,
+                                          a.hd);
+                    load_tile<T, kStr, D>(x2, static_cast<const T *>(a.go) + (c_row * a.nh + h) * a.hd,
+                                          (int64_t)a.nh * a.hd, cols, a.hd);
+                } else {
+                    load_tile<T, kStr, D>(x1, static_cast<const T *>(a.k) + c_row * a.ks + (int64_t)g * a.hd, a.ks, cols,
+                                          a.hd);
+                    load_tile<T, kStr, D>(x2, static_cast<const T *>(a.v) + c_row * a.vs + (int64_t)g * a.hd, a.vs, cols,
+                                          a.hd);
+                }
+                __syncthreads();
+                float s[4][4], dp[4][4];
+                score_tile<D>(r1, x1, ty, tx, s);
+                score_tile<D>(r2, x2, ty, tx, dp);
+                const bool whole = KEYS ? c0 >= u.p0 + kRes - 1 && cols == kStr &&
+                                              (a.window == 0 || c0 + kStr - 1 < u.p0 + a.window)
+                                        : c0 + kStr - 1 <= u.p0 && (a.window == 0 || u.p0 + kRes - 1 < c0 + a.window);
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const int row = u.p0 + 4 * ty + i, col = c0 + tx + 16 * j;
+                        const int pos = KEYS ? col : row, t = KEYS ? row : col;
+                        float p = 0.f, d = 0.f;
+                        if (pos < u.len && t <= pos && (a.window == 0 || pos - t < a.window)) {
+                            const int64_t at = (int64_t)u.begin + pos;
+                            const float *l = a.lse_in + (at * a.nh + h) * 2;
+                            p = expf(s[i][j] * a.scale - __ldg(l) - __ldg(l + 1));
+                            d = p * (dp[i][j] - __ldg(&a.stats[(int64_t)h * a.tokens + at].y));
+                        }
+                        ds_s[(4 * ty + i) * kP + tx + 16 * j] = d;
+                        if (KEYS) p_s[(4 * ty + i) * kP + tx + 16 * j] = p;
+                    }
+                __syncwarp();  // a warp's eight rows of p and ds are its own
+                if (whole) {
+                    add_tile<D, false>(ds_s, x1, ty, tx, acc1);
+                    if (KEYS) add_tile<D, false>(p_s, x2, ty, tx, acc2);
+                } else {
+                    add_tile<D, true>(ds_s, x1, ty, tx, acc1);
+                    if (KEYS) add_tile<D, true>(p_s, x2, ty, tx, acc2);
+                }
+            }
+    }
+    if (KEYS && split > 1) {
+        // Ranks above 0 leave their sums in their own shared memory; rank 0 adds them in the ranks' order.
+        namespace cg = cooperative_groups;
+        cg::cluster_group cluster = cg::this_cluster();
+        float2 *mine = reinterpret_cast<float2 *>(sm);
+        __syncthreads();
+        if (rank != 0) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int c = 0; c < D / 32; ++c) {
+                    mine[(i * (D / 32) + c) * kThreads + threadIdx.x] = acc1[i][c];
+                    mine[((4 + i) * (D / 32) + c) * kThreads + threadIdx.x] = acc2[i][c];
+                }
+        }
+        cluster.sync();
+        if (rank == 0)
+            for (int z = 1; z < split; ++z) {
+                const unsigned base = cluster.block_rank();
+                const float2 *theirs = cluster.map_shared_rank(mine, base + (unsigned)z);
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+#pragma unroll
+                    for (int c = 0; c < D / 32; ++c) {
+                        acc1[i][c] = __fadd2_rn(acc1[i][c], theirs[(i * (D / 32) + c) * kThreads + threadIdx.x]);
+                        acc2[i][c] = __fadd2_rn(acc2[i][c], theirs[((4 + i) * (D / 32) + c) * kThreads + threadIdx.x]);
+                    }
+            }
+        cluster.sync();
+        if (rank != 0) return;
+    }
+    if (!u.live) return;
+    const float one[4] = {1.f, 1.f, 1.f, 1.f}, scaled[4] = {a.scale, a.scale, a.scale, a.scale};
+    const int64_t stride = (int64_t)heads * a.hd, at = (row0 * heads + head) * a.hd;
+    store_rows<T, D>(static_cast<T *>(KEYS ? a.dk : a.dq) + at, stride, ty, tx, live, a.hd, acc1, scaled);
+    if (KEYS) store_rows<T, D>(static_cast<T *>(a.dv) + at, stride, ty, tx, live, a.hd, acc2, one);
+}
+
+// Blocks [0, key_blocks) have keys resident; key_blocks is a multiple of the cluster size, which is `split`.
+template <typename T, int D>
+__global__ void __launch_bounds__(kThreads) backward_simt_kernel(const Args a, unsigned key_blocks, int split,
+                                                                 unsigned *error) {
+    extern __shared__ float4 sm4[];
+    if (threadIdx.x == 0) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (blockIdx.x < key_blocks)
+        backward_unit<T, D, true>(a, blockIdx.x, error, split, reinterpret_cast<float *>(sm4));
+    else
+        backward_unit<T, D, false>(a, blockIdx.x - key_blocks, error, 1, reinterpret_cast<float *>(sm4));
+}
+
+template <typename K, typename... A>
+int launch(K kern, int64_t blocks, int threads, size_t smem, int cluster, std::atomic<uint64_t> &configured,
+           cudaStream_t st, A... args) {
+    if (blocks > INT32_MAX) return DGRAD_ERR_UNSUPPORTED;
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return DGRAD_ERR_CUDA;
+    const uint64_t bit = dev < 64 ? (uint64_t)1 << dev : 0;
+    if (smem > 48 * 1024 && (!bit || !(configured.load() & bit))) {
+        if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
+            return DGRAD_ERR_CUDA;
+        configured.fetch_or(bit);
+    }
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)blocks);
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = (unsigned)cluster;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, kern, args...) == cudaSuccess ? DGRAD_OK : DGRAD_ERR_CUDA;
+}
+
+template <typename T, int D>
+int forward_d(const Args &a, const mha_packed_params *p, unsigned *error, cudaStream_t st) {
+    static std::atomic<uint64_t> configured{0};
+    const size_t smem = sizeof(float) * ((kRes + 2 * kStr) * (D + 4) + kRes * kP);
+    return launch(forward_simt_kernel<T, D>, unit_bound(p, kRes) * a.nh, kThreads, smem, 1, configured, st, a, error);
+}
+
+template <typename T, int D>
+int backward_d(const Args &a, const mha_packed_params *p, unsigned *error, cudaStream_t st) {
+    static std::atomic<uint64_t> delta_configured{0}, configured{0};
+    int rc = launch(delta_simt_kernel<T>, ((int64_t)a.tokens * a.nh + 7) / 8, 256, 0, 1, delta_configured, st, a);
+    if (rc != DGRAD_OK) return rc;
+    int split = 8;  // blocks per group of heads: the largest portable cluster that divides the group
+    while (a.hpk % split != 0) split /= 2;
+    const size_t smem = sizeof(float) * ((2 * kRes + 2 * kStr) * (D + 4) + 2 * kRes * kP);
+    const int64_t units = unit_bound(p, kRes), key_blocks = units * a.nkv * split;
+    const int64_t query_blocks = (units * a.nh + split - 1) / split * split;  // whole clusters; find_unit ends the spare
+    return launch(backward_simt_kernel<T, D>, key_blocks + query_blocks, kThreads, smem, split, configured, st, a,
+                  (unsigned)key_blocks, split, error);
+}
+
+template <typename T>
+int forward_any(const Args &a, const mha_packed_params *p, unsigned *error, cudaStream_t st) {
+    if (a.hd <= 64) return forward_d<T, 64>(a, p, error, st);
+    if (a.hd <= 96) return forward_d<T, 96>(a, p, error, st);
+    if (a.hd <= 128) return forward_d<T, 128>(a, p, error, st);
+    if (a.hd <= 192) return forward_d<T, 192>(a, p, error, st);
+    return forward_d<T, 256>(a, p, error, st);
+}
+template <typename T>
+int backward_any(const Args &a, const mha_packed_params *p, unsigned *error, cudaStream_t st) {
+    if (a.hd <= 64) return backward_d<T, 64>(a, p, error, st);
+    if (a.hd <= 96) return backward_d<T, 96>(a, p, error, st);
+    if (a.hd <= 128) return backward_d<T, 128>(a, p, error, st);
+    if (a.hd <= 192) return backward_d<T, 192>(a, p, error, st);
+    return backward_d<T, 256>(a, p, error, st);
+}
+
+}  // namespace
+}  // namespace mhapk
