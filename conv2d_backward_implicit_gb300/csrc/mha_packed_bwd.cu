@@ -92,7 +92,7 @@ struct BwdArgs {
 };
 
 struct Ctl {
-    uint64_t r_full, r_ready, x1_full[5], x1_empty[5], x2_full[4], x2_empty[4], st_full[kStatSlots], st_empty[kStatSlots];
+    uint64_t r_full[2], r_ready[2], x1_full[5], x1_empty[5], x2_full[4], x2_empty[4], st_full[kStatSlots], st_empty[kStatSlots];
     uint64_t full[3], p_ready[2], d_ready[2], turn[2], acc_full, mma_done[2];
     uint32_t tmem_base;
     int abort_flag, bad;
@@ -256,8 +256,8 @@ __device__ void role_load(const BwdArgs &p, Ctl &c, uint32_t smem, const Unit &u
     using C = Cfg<D>;
     const CUtensorMap *r1 = KEYS ? &p.k_map : &p.q_map, *r2 = KEYS ? &p.v_map : &p.go_map;
     const CUtensorMap *x1 = KEYS ? &p.q_map : &p.k_map, *x2 = KEYS ? &p.go_map : &p.v_map;
-    load_rows<D>(smem + C::kOffR, r1, p.a.hd, head, u.begin + u.p0, kRows, su32(&c.r_full));
-    load_rows<D>(smem + C::kOffR + C::kTile, r2, p.a.hd, head, u.begin + u.p0, kRows, su32(&c.r_full));
+    // What the first products need first: R1, X1, then R2, X2.
+    load_rows<D>(smem + C::kOffR, r1, p.a.hd, head, u.begin + u.p0, kRows, su32(&c.r_full[0]));
     const int n = k.steps();
     Ring<C::kX1> a;
     Ring<C::kX2> b;
@@ -280,10 +280,14 @@ __device__ void role_load(const BwdArgs &p, Ctl &c, uint32_t smem, const Unit &u
             return true;
         };
         // X1 is wanted first; once the rings are full, X2's slot is the one that comes free first.
-        if (j < C::kX1 ? !load1() || !load2() : !load2() || !load1()) break;
+        if (j < C::kX1 && !load1()) break;
+        if (j == 0)
+            load_rows<D>(smem + C::kOffR + C::kTile, r2, p.a.hd, head, u.begin + u.p0, kRows, su32(&c.r_full[1]));
+        if (!load2() || (j >= C::kX1 && !load1())) break;
     }
     // Copies still landing must finish before the block exits.
-    drain(su32(&c.r_full), 0, w);
+    drain(su32(&c.r_full[0]), 0, w);
+    if (n1) drain(su32(&c.r_full[1]), 0, w);
     for (int q = n1 > C::kX1 ? n1 - C::kX1 : 0; q < n1; ++q)
         drain(su32(&c.x1_full[q % C::kX1]), (uint32_t)((q / C::kX1) & 1), w);
     for (int q = n2 > C::kX2 ? n2 - C::kX2 : 0; q < n2; ++q)
@@ -370,7 +374,8 @@ __device__ __forceinline__ void issue(const BwdArgs &p, Ctl &c, uint32_t smem, u
         xs.next();
         use += 2;
     };
-    if (!wait_warp(su32(KEYS ? &c.r_full : &c.r_ready), 0, w)) return;
+    constexpr int RES = IS_S ? 0 : 1;
+    if (!wait_warp(su32(KEYS ? &c.r_full[RES] : &c.r_ready[RES]), 0, w)) return;
     for (int j = 0; j < AHEAD && j < n; ++j) {
         if (!operand()) return;
         next_scores();
@@ -506,7 +511,7 @@ __device__ void role_soft(const BwdArgs &p, Ctl &c, uint32_t smem, uint32_t tmem
         // Q and dO of this thread's row go to tensor memory, where acc2 would be: as the A operand they then cost shared
         // memory no reads (the scores' operands in shared memory alone would keep it busy for as long as the products).
         const int which = warp >> 3, part = (warp >> 2) & 1;  // R1 or R2, half of its columns
-        if (!wait_warp(su32(&c.r_full), 0, w)) return;
+        if (!wait_warp(su32(&c.r_full[which]), 0, w)) return;
         const uint32_t r = (uint32_t)(32 * quad + lane);
         const uint32_t src = smem + C::kOffR + (uint32_t)which * C::kTile + (D == 128 ? (uint32_t)part * kHalf : 0u) + r * 128u;
         const uint32_t dst = tmem + lane_tm + C::kColAcc2 + (uint32_t)(which * (D / 2) + part * (D / 4));
@@ -524,7 +529,7 @@ __device__ void role_soft(const BwdArgs &p, Ctl &c, uint32_t smem, uint32_t tmem
         tc_wait_st();
         tc_before();
         __syncwarp();
-        if (lane == 0) bar_arrive(su32(&c.r_ready));
+        if (lane == 0) bar_arrive(su32(&c.r_ready[which]));
     }
     // The rows that this one meets: queries [row, end) with keys resident, else keys [first, row].
     const int first = a.window > 0 ? row - a.window + 1 : 0;
@@ -715,8 +720,10 @@ __global__ void __launch_bounds__(kThreads, 1) backward_tc_kernel(const __grid_c
     }
     const int warp = uniform((int)(threadIdx.x >> 5)), lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
-        bar_init(su32(&c.r_full), 2);
-        bar_init(su32(&c.r_ready), kSoftWarps);
+        for (int i = 0; i < 2; ++i) {
+            bar_init(su32(&c.r_full[i]), 1);
+            bar_init(su32(&c.r_ready[i]), kSoftWarps / 2);
+        }
         bar_init(su32(&c.acc_full), 2);
         bar_init(su32(&c.mma_done[0]), 1);
         bar_init(su32(&c.mma_done[1]), 1);

@@ -26,8 +26,7 @@
 //     softmax does.  A warp's products run in order, so S may overwrite P behind PV; two
 //     warps, because a warp's waits otherwise stand between its products (2850 cycles per
 //     key block with one warp, of which 850 were waits).
-//   * warps 18 and 19 (one thread each): TMA copies of K (and Q tile 0) and V (and Q
-//     tile 1).
+//   * warp 18 (one thread): TMA copies of the Q tiles, K and V.
 // V rows past the sequence's end are zeroed in shared memory (other sequences' rows,
 // possibly with infinities); what is masked inside the sequence has P = 0, and if a
 // value there is not finite the product with 0 leaves a NaN in O: the tile is then
@@ -52,9 +51,9 @@ namespace {
 
 constexpr int kRows = 128;                     // queries per tile, keys per step
 constexpr uint32_t kHalf = kRows * 128;        // bytes of a [128][64] 16-bit half tile
-constexpr int kSoftWarps = 16, kMmaWarp = 16, kLoadWarp = 18;  // one for each tile; K, then V
+constexpr int kSoftWarps = 16, kMmaWarp = 16, kLoadWarp = 18;  // 16, 17: one for each tile
 constexpr uint32_t kColS = 0, kColO = 256;     // + 128 i, + 128 i
-constexpr int kThreads = 32 * (kLoadWarp + 2);
+constexpr int kThreads = 32 * (kLoadWarp + 1);
 constexpr float kLag = 8.0f;                   // log2 of how far the scaling maximum may lag
 constexpr float kShift16 = 7.0f;               // log2 of fp16's scale of P: P <= 2^15, and 7 more bits below
 
@@ -101,27 +100,38 @@ __device__ __forceinline__ Tile tile_of(const FwdArgs &p, const Unit &u, int pai
     return t;
 }
 
-// One loading thread: K and Q tile 0 (tensor 0), or V and Q tile 1 (tensor 1).
+// The loading thread: what the first products need first (Q_0, K, Q_1, V), then K and V of block after block.
 template <int D>
-__device__ void role_load(const FwdArgs &p, Ctl &c, uint32_t smem, const Unit &u, const Tile &own, int g, int lo,
-                          int hi, int tensor, const Waiter &w) {
+__device__ void role_load(const FwdArgs &p, Ctl &c, uint32_t smem, const Unit &u, const Tile (&t)[2], int g, int lo, int hi,
+                          const Waiter &w) {
     using C = Cfg<D>;
-    const CUtensorMap *map = tensor ? &p.v_map : &p.k_map;
-    uint64_t *full = tensor ? c.v_full : c.k_full, *empty = tensor ? c.v_empty : c.k_empty;
-    const uint32_t ring = smem + (tensor ? C::kOffV : C::kOffK);
-    if (own.live)
-        load_rows<D>(smem + C::kOffQ + (uint32_t)tensor * C::kTile, &p.q_map, p.a.hd, own.head, u.begin + own.p0, kRows,
-                     su32(&c.q_full[tensor]));
-    int it = 0;
-    for (int b = hi - 1; b >= lo; --b, ++it) {
-        const int s = it % C::kStages;
-        if (!wait(su32(&empty[s]), (uint32_t)(((it / C::kStages) & 1) ^ 1), w)) break;
-        load_rows<D>(ring + (uint32_t)s * C::kTile, map, p.a.hd, g, u.begin + kRows * b, kRows, su32(&full[s]));
+    auto query = [&](int i) {
+        if (t[i].live)
+            load_rows<D>(smem + C::kOffQ + (uint32_t)i * C::kTile, &p.q_map, p.a.hd, t[i].head, u.begin + t[i].p0, kRows,
+                         su32(&c.q_full[i]));
+    };
+    query(0);
+    int nk = 0, nv = 0;
+    for (int b = hi - 1; b >= lo; --b) {
+        const int s = nk % C::kStages;
+        const uint32_t parity = (uint32_t)(((nk / C::kStages) & 1) ^ 1);
+        if (!wait(su32(&c.k_empty[s]), parity, w)) break;
+        load_rows<D>(smem + C::kOffK + (uint32_t)s * C::kTile, &p.k_map, p.a.hd, g, u.begin + kRows * b, kRows,
+                     su32(&c.k_full[s]));
+        ++nk;
+        if (b == hi - 1) query(1);
+        if (!wait(su32(&c.v_empty[s]), parity, w)) break;
+        load_rows<D>(smem + C::kOffV + (uint32_t)s * C::kTile, &p.v_map, p.a.hd, g, u.begin + kRows * b, kRows,
+                     su32(&c.v_full[s]));
+        ++nv;
     }
     // Copies still landing must finish before the block exits.
-    if (own.live) drain(su32(&c.q_full[tensor]), 0, w);
-    for (int q = it > C::kStages ? it - C::kStages : 0; q < it; ++q)
-        drain(su32(&full[q % C::kStages]), (uint32_t)((q / C::kStages) & 1), w);
+    for (int i = 0; i < 2; ++i)
+        if (t[i].live) drain(su32(&c.q_full[i]), 0, w);
+    for (int q = nk > C::kStages ? nk - C::kStages : 0; q < nk; ++q)
+        drain(su32(&c.k_full[q % C::kStages]), (uint32_t)((q / C::kStages) & 1), w);
+    for (int q = nv > C::kStages ? nv - C::kStages : 0; q < nv; ++q)
+        drain(su32(&c.v_full[q % C::kStages]), (uint32_t)((q / C::kStages) & 1), w);
 }
 
 // The products of tile i; returns early when aborting.  Iteration b: PV of key block b + 1, then S of block b.  The two
@@ -470,8 +480,7 @@ __global__ void __launch_bounds__(kThreads, 1) forward_tc_kernel(const __grid_co
                 drain(su32(&c.mma_done[i]), 0, w);
                 __syncwarp();
             } else {
-                const int tensor = warp - kLoadWarp;
-                if (lane == 0) role_load<D>(p, c, smem, u, tensor ? t[1] : t[0], g, lo, hi, tensor, w);
+                if (lane == 0) role_load<D>(p, c, smem, u, t, g, lo, hi, w);
                 __syncwarp();
             }
             tc_before();
