@@ -85,7 +85,7 @@ struct Cfg {
 
 struct BwdArgs {
     Args a;
-    CUtensorMap q_map, k_map, v_map, go_map;
+    CUtensorMap q_map, k_map, v_map, go_map, dq_map, dk_map, dv_map;
     const unsigned *norms;  // fp16: bits of max |dO row|^2, max |V row|^2
     unsigned key_units;     // blocks [0, key_units) have keys resident
     uint32_t idesc1, idesc2;
@@ -462,36 +462,6 @@ __device__ __forceinline__ void grads32(const uint32_t (&p)[32], const uint32_t 
     }
 }
 
-// W columns of 32 rows from tensor memory, times `factor`, through this warp's staging rows to dst (a row every
-// `stride` elements; `cols` of the columns exist).  Returns whether this lane's row is finite.
-template <int W, bool F16>
-__device__ __forceinline__ bool store_acc(uint32_t acc_tm, uint32_t stage, float factor, uint16_t *dst, int64_t stride,
-                                          int live, int cols, int lane) {
-    constexpr int kChunks = W / 8;  // 16-byte chunk j of row r lies at j ^ (r & 7), of 64-byte rows at j ^ (r / 2 & 3)
-    auto place = [](int r, int j) { return (uint32_t)((kChunks == 4 ? j ^ ((r >> 1) & 3) : j ^ (r & 7)) << 4); };
-    float2 odd = make_float2(0.f, 0.f);  // 0 as long as every value is finite
-#pragma unroll
-    for (int k = 0; k < W / 32; ++k) {
-        uint32_t o[32];
-        tc_ld_32x32(acc_tm + 32 * k, o);
-        tc_wait_ld(o);
-        scale_pack<F16>(o, factor, odd);
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-            sts128(stage + (uint32_t)lane * (2 * W) + place(lane, 4 * k + j), o[4 * j], o[4 * j + 1], o[4 * j + 2],
-                   o[4 * j + 3]);
-    }
-    const bool good = odd.x + odd.y == 0.f;
-    __syncwarp();
-    const int j = lane % kChunks;
-    for (int r = lane / kChunks; r < 32; r += 32 / kChunks) {
-        if (r >= live || 8 * j >= cols) continue;
-        const uint4 x = lds128(stage + (uint32_t)r * (2 * W) + place(r, j));
-        *reinterpret_cast<uint4 *>(dst + (int64_t)r * stride + 8 * j) = x;
-    }
-    return good;
-}
-
 template <int D, bool F16, bool KEYS>
 __device__ void role_soft(const BwdArgs &p, Ctl &c, uint32_t smem, uint32_t tmem, const Unit &u, const Walk &k, int live,
                           int head, float sigma, int warp, int lane, const Waiter &w) {
@@ -594,15 +564,16 @@ __device__ void role_soft(const BwdArgs &p, Ctl &c, uint32_t smem, uint32_t tmem
     const int grp = warp >> 3, part = (warp >> 2) & 1;
     if (!KEYS && grp == 1) return;
     constexpr int W = D / 2;
-    const int heads = KEYS ? a.nkv : a.nh;
-    const int64_t stride = (int64_t)heads * a.hd;
-    const int64_t at = (((int64_t)u.begin + u.p0 + 32 * quad) * heads + head) * a.hd + W * part;
     const float factor = grp == 0 ? a.scale / sigma : (F16 ? 0x1p-13f : 1.f);
-    uint16_t *dst = static_cast<uint16_t *>(grp == 0 ? (KEYS ? a.dk : a.dq) : a.dv) + at;
-    const uint32_t stage = smem + C::kOffR + (uint32_t)grp * C::kTile + (uint32_t)(warp & 7) * (C::kTile / 8);
-    const bool good = store_acc<W, F16>(tmem + lane_tm + (grp == 0 ? C::kColAcc1 : C::kColAcc2) + W * part, stage, factor,
-                                        dst, stride, live - 32 * quad, a.hd - W * part, lane);
+    const CUtensorMap *map = grp == 1 ? &p.dv_map : KEYS ? &p.dk_map : &p.dq_map;
+    const bool good = store_rows<W, F16>(tmem + lane_tm + (grp == 0 ? C::kColAcc1 : C::kColAcc2) + W * part,
+                                         smem + C::kOffR + (uint32_t)grp * C::kTile + (uint32_t)(warp & 7) * (C::kTile / 8),
+                                         factor, map, static_cast<uint16_t *>(grp == 1 ? a.dv : KEYS ? a.dk : a.dq),
+                                         KEYS ? a.nkv : a.nh, a.hd, head, (int64_t)u.begin + u.p0 + 32 * quad, W * part,
+                                         live - 32 * quad, lane);
     if (__any_sync(0xffffffffu, row < u.len && !good) && lane == 0) c.bad = 1;
+    if (lane == 0) stores_read();
+    __syncwarp();
 }
 
 // The unit's rows one by one over the attended pairs alone, one warp per row.
@@ -705,7 +676,11 @@ __device__ __forceinline__ void unit_body(const BwdArgs &p, Ctl &c, uint32_t sme
     tc_before();
     __syncthreads();
     tc_after();
-    if (c.bad && !c.abort_flag) recompute<D, F16, KEYS>(p.a, u, live, head);
+    if (c.bad && !c.abort_flag) {
+        if (lane == 0) stores_done();
+        __syncthreads();
+        recompute<D, F16, KEYS>(p.a, u, live, head);
+    }
 }
 
 template <int D, bool F16>
@@ -808,7 +783,10 @@ int backward_tc(const Args &a, unsigned *norms, const mha_packed_params *p, int 
     if (!encode_rows(&q.q_map, a.q, a.tokens, a.nh, a.hd, a.qs, kRows) ||
         !encode_rows(&q.k_map, a.k, a.tokens, a.nkv, a.hd, a.ks, kRows) ||
         !encode_rows(&q.v_map, a.v, a.tokens, a.nkv, a.hd, a.vs, kRows) ||
-        !encode_rows(&q.go_map, a.go, a.tokens, a.nh, a.hd, dense, kRows))
+        !encode_rows(&q.go_map, a.go, a.tokens, a.nh, a.hd, dense, kRows) ||
+        !encode_store(&q.dq_map, a.dq, a.tokens, a.nh, a.hd, D / 2) ||
+        !encode_store(&q.dk_map, a.dk, a.tokens, a.nkv, a.hd, D / 2) ||
+        !encode_store(&q.dv_map, a.dv, a.tokens, a.nkv, a.hd, D / 2))
         return DGRAD_ERR_UNSUPPORTED;
     const bool f16 = dtype == DGRAD_F16;
     const int rc = f16 ? launch_stats<__half>(a, norms, st) : launch_stats<__nv_bfloat16>(a, norms, st);

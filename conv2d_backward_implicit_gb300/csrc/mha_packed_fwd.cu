@@ -70,7 +70,7 @@ struct Cfg {
 
 struct FwdArgs {
     Args a;
-    CUtensorMap q_map, k_map, v_map;
+    CUtensorMap q_map, k_map, v_map, o_map;
     uint32_t idesc1, idesc2;
     int pair_heads;  // the two tiles are two heads of a group (else two runs of positions)
 };
@@ -327,27 +327,7 @@ __device__ void role_soft(const FwdArgs &p, Ctl &c, uint32_t smem, uint32_t tmem
     const Tile own = i ? t[1] : t[0];
     if (!own.live) return;
     const float all = i ? total[1] : total[0], was = i ? used[1] : used[0], best = i ? top[1] : top[0];
-    if (!wait_warp(su32(&c.o_full[i]), 0, w)) return;
-    tc_after();
-    constexpr int W = D / 2, kChunks = W / 8;  // 16-byte chunk j of row r lies at j ^ (r & 7), of 64-byte rows at j ^ (r / 2 & 3)
-    auto place = [](int r, int j) { return (uint32_t)((kChunks == 4 ? j ^ ((r >> 1) & 3) : j ^ (r & 7)) << 4); };
-    const float inv = 1.0f / all;
-    const uint32_t o_tm = tmem + lane_tm + kColO + 128u * i + (uint32_t)W * half;
-    const uint32_t stage = smem + C::kOffQ + (uint32_t)i * C::kTile + (uint32_t)(warp & 7) * (C::kTile / 8);
     const bool row_live = 32 * quad + lane < own.live;
-    float2 odd = make_float2(0.f, 0.f);  // 0 as long as every value is finite
-#pragma unroll
-    for (int k = 0; k < W / 32; ++k) {
-        uint32_t o[32];
-        tc_ld_32x32(o_tm + 32 * k, o);
-        tc_wait_ld(o);
-        scale_pack<F16>(o, inv, odd);
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-            sts128(stage + (uint32_t)lane * (2 * W) + place(lane, 4 * k + j), o[4 * j], o[4 * j + 1], o[4 * j + 2],
-                   o[4 * j + 3]);
-    }
-    if (__any_sync(0xffffffffu, row_live && !(odd.x + odd.y == 0.f)) && lane == 0) c.bad[i] = 1;
     const int64_t row0 = (int64_t)u.begin + own.p0 + 32 * quad;
     if (row_live && half == 0) {
         // The sum is relative to the maximum in use; LSE wants it relative to the true one.
@@ -356,14 +336,17 @@ __device__ void role_soft(const FwdArgs &p, Ctl &c, uint32_t smem, uint32_t tmem
         float *st = p.a.lse + ((row0 + lane) * p.a.nh + own.head) * 2;
         st[0] = best * p.a.scale, st[1] = l;
     }
+    const float inv = 1.0f / all;
+    if (!wait_warp(su32(&c.o_full[i]), 0, w)) return;
+    tc_after();
+    constexpr int W = D / 2;
+    const bool good = store_rows<W, F16>(tmem + lane_tm + kColO + 128u * i + (uint32_t)W * half,
+                                         smem + C::kOffQ + (uint32_t)i * C::kTile + (uint32_t)(warp & 7) * (C::kTile / 8),
+                                         inv, &p.o_map, static_cast<uint16_t *>(p.a.out), p.a.nh, p.a.hd, own.head, row0,
+                                         W * half, own.live - 32 * quad, lane);
+    if (__any_sync(0xffffffffu, row_live && !good) && lane == 0) c.bad[i] = 1;
+    if (lane == 0) stores_read();
     __syncwarp();
-    uint16_t *out = static_cast<uint16_t *>(p.a.out) + (row0 * p.a.nh + own.head) * p.a.hd + W * half;
-    const int j = lane % kChunks;
-    for (int r = lane / kChunks; r < 32; r += 32 / kChunks) {
-        if (32 * quad + r >= own.live || W * half + 8 * j >= p.a.hd) continue;
-        const uint4 x = lds128(stage + (uint32_t)r * (2 * W) + place(r, j));
-        *reinterpret_cast<uint4 *>(out + (int64_t)r * p.a.nh * p.a.hd + 8 * j) = x;
-    }
 }
 
 // A tile row by row over the attended keys, one warp per row: for tiles where a masked value is not finite.
@@ -435,8 +418,8 @@ __global__ void __launch_bounds__(kThreads, 1) forward_tc_kernel(const __grid_co
             bar_init(su32(&c.mma_done[lane - 9]), 1);
             c.bad[lane - 9] = 0;
         }
-    } else if (threadIdx.x < 35) {
-        const CUtensorMap *m = lane == 0 ? &p.q_map : lane == 1 ? &p.k_map : &p.v_map;
+    } else if (threadIdx.x < 36) {
+        const CUtensorMap *m = lane == 0 ? &p.q_map : lane == 1 ? &p.k_map : lane == 2 ? &p.v_map : &p.o_map;
         asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(m)) : "memory");
     }
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -486,7 +469,9 @@ __global__ void __launch_bounds__(kThreads, 1) forward_tc_kernel(const __grid_co
             tc_before();
             __syncthreads();
             tc_after();
-            if (!c.abort_flag) {
+            if (!c.abort_flag && (c.bad[0] || c.bad[1])) {
+                if (lane == 0) stores_done();
+                __syncthreads();
                 if (c.bad[0]) recompute<D, F16>(p.a, u, t[0], g);
                 if (c.bad[1]) recompute<D, F16>(p.a, u, t[1], g);
             }
@@ -513,7 +498,8 @@ int forward_tc(const Args &a, const mha_packed_params *p, int dtype, cudaStream_
     q.idesc2 = instr_desc(dtype, kRows, D, true);
     if (!encode_rows(&q.q_map, a.q, a.tokens, a.nh, a.hd, a.qs, kRows) ||
         !encode_rows(&q.k_map, a.k, a.tokens, a.nkv, a.hd, a.ks, kRows) ||
-        !encode_rows(&q.v_map, a.v, a.tokens, a.nkv, a.hd, a.vs, kRows))
+        !encode_rows(&q.v_map, a.v, a.tokens, a.nkv, a.hd, a.vs, kRows) ||
+        !encode_store(&q.o_map, a.out, a.tokens, a.nh, a.hd, D / 2))
         return DGRAD_ERR_UNSUPPORTED;
     const int64_t blocks = q.pair_heads ? unit_bound(p, kRows) * (a.nh / 2) : unit_bound(p, 2 * kRows) * a.nh;
     const bool f16 = dtype == DGRAD_F16;

@@ -175,6 +175,70 @@ __device__ __forceinline__ void load_rows(uint32_t dst, const CUtensorMap *map, 
     }
 }
 
+// The same tensor for stores: boxes of 32 tokens x W elements of one head from rows of 2 W bytes, W = 64 (128-byte
+// swizzle) or 32 (64-byte swizzle).  Elements past hd are not written.
+inline bool encode_store(CUtensorMap *m, void *ptr, int tokens, int heads, int hd, int W) {
+    PFN_cuTensorMapEncodeTiled_v12000 fn = encode_fn();
+    if (!fn) return false;
+    const cuuint64_t dims[3] = {(cuuint64_t)hd, (cuuint64_t)heads, (cuuint64_t)tokens};
+    const cuuint64_t strides[2] = {(cuuint64_t)hd * 2, (cuuint64_t)heads * hd * 2};
+    const cuuint32_t box[3] = {(cuuint32_t)W, 1, 32};
+    const cuuint32_t es[3] = {1, 1, 1};
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT16, 3, ptr, dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+              W == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// W columns of 32 rows of an accumulator: tensor memory -> (times factor, rounded) -> this warp's staging rows (2 W bytes
+// each, 16-byte chunks swizzled as the store map has them) -> rows token .. token + 31 of `head`, columns col .. .  The
+// first `live` rows exist: a whole box goes out as one TMA store, which lane 0 of the caller waits for (stores_read), part of one
+// row by row.  Returns whether this lane's row is finite.
+template <int W, bool F16>
+__device__ __forceinline__ bool store_rows(uint32_t acc_tm, uint32_t stage, float factor, const CUtensorMap *map,
+                                           uint16_t *dst, int heads, int hd, int head, int64_t token, int col, int live,
+                                           int lane) {
+    constexpr int kChunks = W / 8;
+    auto place = [](int r, int j) { return (uint32_t)((kChunks == 4 ? j ^ ((r >> 1) & 3) : j ^ (r & 7)) << 4); };
+    float2 odd = make_float2(0.f, 0.f);  // 0 as long as every value is finite
+#pragma unroll
+    for (int k = 0; k < W / 32; ++k) {
+        uint32_t o[32];
+        tc_ld_32x32(acc_tm + 32 * k, o);
+        tc_wait_ld(o);
+        scale_pack<F16>(o, factor, odd);
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            sts128(stage + (uint32_t)lane * (2 * W) + place(lane, 4 * k + j), o[4 * j], o[4 * j + 1], o[4 * j + 2],
+                   o[4 * j + 3]);
+    }
+    if (live >= 32) {
+        fence_async_proxy();
+        __syncwarp();
+        if (lane == 0 && col < hd) {
+            asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(
+                             reinterpret_cast<uint64_t>(map)),
+                         "r"(col), "r"(head), "r"((int)token), "r"(stage)
+                         : "memory");
+            asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+        }
+    } else {
+        __syncwarp();
+        const int64_t stride = (int64_t)heads * hd;
+        uint16_t *out = dst + (token * heads + head) * hd + col;
+        const int j = lane % kChunks;
+        for (int r = lane / kChunks; r < live; r += 32 / kChunks) {
+            if (col + 8 * j >= hd) continue;
+            const uint4 x = lds128(stage + (uint32_t)r * (2 * W) + place(r, j));
+            *reinterpret_cast<uint4 *>(out + (int64_t)r * stride + 8 * j) = x;
+        }
+    }
+    return odd.x + odd.y == 0.f;
+}
+// This thread's TMA stores have read shared memory (before the block exits), or are complete (before anything rewrites
+// what they write).
+__device__ __forceinline__ void stores_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
+__device__ __forceinline__ void stores_done() { bulk_wait_all(); }
+
 inline uint32_t instr_desc(int dtype, int m, int n, bool b_mn_major) {  // D float32, A and B of the input type
     const uint32_t fmt = dtype == DGRAD_BF16 ? 1u : 0u;
     return (1u << 4) | (fmt << 7) | (fmt << 10) | (b_mn_major ? 1u << 16 : 0u) | ((uint32_t)(n >> 3) << 17) |
