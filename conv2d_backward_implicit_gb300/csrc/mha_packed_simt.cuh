@@ -37,30 +37,33 @@ namespace {
 constexpr int kThreads = 128, kRes = 32, kStr = 64;  // threads, resident rows, streamed rows
 constexpr int kP = kStr + 4;                         // pitch of the 32 x 64 products
 
-// rows [0, ROWS) of a head into shared memory as float32, zero past `live` rows and past hd.
+// The same in pieces of V elements, of the unsigned type R.
+template <typename T, typename R, int ROWS, int D>
+__device__ __forceinline__ void load_pieces(float *dst, const T *src, int64_t stride, int live, int hd) {
+    constexpr int P = D + 4, V = sizeof(R) / sizeof(T);
+#pragma unroll 4
+    for (int e = threadIdx.x; e < ROWS * (D / V); e += kThreads) {
+        const int r = e / (D / V), d = (e - r * (D / V)) * V;
+        R w{};
+        if (r < live && d < hd) w = __ldg(reinterpret_cast<const R *>(src + (int64_t)r * stride + d));
+        const T *h = reinterpret_cast<const T *>(&w);
+#pragma unroll
+        for (int i = 0; i < V; ++i) dst[r * P + d + i] = to_f(h[i]);
+    }
+}
+// rows [0, ROWS) of a head into shared memory as float32, zero past `live` rows and past hd, in the widest pieces that
+// the row's length, stride and address allow.
 template <typename T, int ROWS, int D>
 __device__ __forceinline__ void load_tile(float *dst, const T *src, int64_t stride, int live, int hd) {
-    constexpr int P = D + 4;
-    constexpr int V = 16 / sizeof(T);  // elements of a 16-byte load
-    if (hd % V == 0 && stride % V == 0 && (reinterpret_cast<uintptr_t>(src) & 15u) == 0) {
-#pragma unroll 4
-        for (int e = threadIdx.x; e < ROWS * (D / V); e += kThreads) {
-            const int r = e / (D / V), d = (e - r * (D / V)) * V;
-            uint4 w = make_uint4(0, 0, 0, 0);
-            if (r < live && d < hd) w = __ldg(reinterpret_cast<const uint4 *>(src + (int64_t)r * stride + d));
-            const T *h = reinterpret_cast<const T *>(&w);
-#pragma unroll
-            for (int i = 0; i < V; i += 4)
-                *reinterpret_cast<float4 *>(dst + r * P + d + i) =
-                    make_float4(to_f(h[i]), to_f(h[i + 1]), to_f(h[i + 2]), to_f(h[i + 3]));
-        }
-    } else {
-#pragma unroll 4
-        for (int e = threadIdx.x; e < ROWS * D; e += kThreads) {
-            const int r = e / D, d = e - r * D;
-            dst[r * P + d] = r < live && d < hd ? to_f(src[(int64_t)r * stride + d]) : 0.f;
-        }
-    }
+    const uintptr_t bits = (uintptr_t)hd * sizeof(T) | (uintptr_t)stride * sizeof(T) | reinterpret_cast<uintptr_t>(src);
+    if (bits % 16 == 0)
+        load_pieces<T, uint4, ROWS, D>(dst, src, stride, live, hd);
+    else if (bits % 8 == 0)
+        load_pieces<T, uint2, ROWS, D>(dst, src, stride, live, hd);
+    else if (sizeof(T) == 4 || bits % 4 == 0)
+        load_pieces<T, unsigned, ROWS, D>(dst, src, stride, live, hd);
+    else
+        load_pieces<T, T, ROWS, D>(dst, src, stride, live, hd);
 }
 
 // out[i][j] = sum over d of a[4 ty + i][d] b[tx + 16 j][d].

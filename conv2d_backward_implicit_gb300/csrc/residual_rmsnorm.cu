@@ -4,8 +4,8 @@
 //
 // Both directions read each row once into registers or shared memory and write their
 // results once; the floor is the bytes.  A row belongs to a team of 1 to 16 warps, each
-// thread holding ITER pieces of it (16 bytes each, or single elements where n or a
-// pointer does not allow 16-byte accesses); the two statistics of a row follow one
+// thread holding ITER pieces of it (16 bytes each, or single elements where a pointer
+// does not allow 16-byte accesses); the two statistics of a row follow one
 // another, each a shuffle reduction plus, for teams of several warps, one barrier of
 // that team alone.
 //
@@ -178,7 +178,57 @@ struct Piece {
         }
     }
     __device__ __forceinline__ void store(void *base, int64_t piece) const { static_cast<Raw *>(base)[piece] = raw; }
+    __device__ __forceinline__ T &at(int e) { return reinterpret_cast<T *>(&raw)[e]; }
 };
+
+// Where a thread's 16-byte piece lies in a row whose first element is `shift` elements into the piece before: elements
+// [lo, hi) of the piece are columns j0 + lo .. of the row, the others belong to its neighbours.
+template <typename T>
+struct Span {
+    using P = Piece<T, true>;
+    int j0, lo, hi;
+    __device__ __forceinline__ Span(int c, int shift, int n) {
+        j0 = c * P::V - shift;
+        lo = j0 < 0 ? -j0 : 0;
+        hi = n - j0 < P::V ? n - j0 : P::V;
+        if (hi < lo) hi = lo;
+    }
+    __device__ __forceinline__ bool whole() const { return lo == 0 && hi == P::V; }
+    // All ones in the bytes of the row's own elements.
+    __device__ __forceinline__ uint4 keep() const {
+        uint32_t w[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            w[i] = 0;
+            if constexpr (sizeof(T) == 4) {
+                if (i >= lo && i < hi) w[i] = 0xffffffffu;
+            } else {
+                if (2 * i >= lo && 2 * i < hi) w[i] |= 0xffffu;
+                if (2 * i + 1 >= lo && 2 * i + 1 < hi) w[i] |= 0xffff0000u;
+            }
+        }
+        return make_uint4(w[0], w[1], w[2], w[3]);
+    }
+    // A vector of n values, element by element (its pieces lie elsewhere).
+    __device__ __forceinline__ void load(P &p, const void *src) const {
+#pragma unroll
+        for (int e = 0; e < P::V; ++e)
+            if (e >= lo && e < hi) p.at(e) = __ldg(static_cast<const T *>(src) + j0 + e);
+    }
+    // The row's own elements of a piece.
+    __device__ __forceinline__ void store(P p, void *base, int64_t piece) const {
+        if (whole()) {
+            p.store(base, piece);
+            return;
+        }
+#pragma unroll
+        for (int e = 0; e < P::V; ++e)
+            if (e >= lo && e < hi) static_cast<T *>(base)[piece * P::V + e] = p.at(e);
+    }
+};
+__device__ __forceinline__ uint4 operator&(uint4 a, uint4 b) {
+    return make_uint4(a.x & b.x, a.y & b.y, a.z & b.z, a.w & b.w);
+}
 __device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
 __device__ __forceinline__ float sum2(float2 x) { return x.x + x.y; }
 __device__ __forceinline__ float2 add2(float2 x, float2 y) { return __fadd2_rn(x, y); }
@@ -187,8 +237,10 @@ __device__ __forceinline__ float2 fma2(float2 x, float2 y, float2 z) { return __
 
 __device__ __forceinline__ float rstd_of(float sum, const Args &a) { return 1.0f / sqrtf(sum / (float)a.n + a.eps); }
 
-__device__ __forceinline__ void copy16(void *dst, const void *src) {  // asynchronous, shared <- global
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((uint32_t)__cvta_generic_to_shared(dst)), "l"(src)
+// Asynchronous, shared <- global: `bytes` of 16, the rest zero.
+__device__ __forceinline__ void copy16(void *dst, const void *src, int bytes) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"((uint32_t)__cvta_generic_to_shared(dst)), "l"(src),
+                 "r"(bytes)
                  : "memory");
 }
 __device__ __forceinline__ void copies_end() { asm volatile("cp.async.commit_group;" ::: "memory"); }
@@ -222,20 +274,21 @@ struct ForwardRow {
             }
         rq = rstd_of(team_sum(sum2(s), red, turn, tw, warp), a);
     }
-    __device__ __forceinline__ void store(const P (&wq)[ITER], const Args &a, int64_t row, int pieces, int t,
-                                          int step) const {
+    // put(piece, tensor, i): piece i of this thread goes to the row of a tensor.
+    template <typename Put>
+    __device__ __forceinline__ void store(const P (&wq)[ITER], const Args &a, int64_t row, int pieces, int t, int step,
+                                          Put put) const {
 #pragma unroll
         for (int i = 0; i < ITER; ++i) {
-            const int c = t + i * step;
-            if (c >= pieces) continue;
+            if (t + i * step >= pieces) continue;
             float2 y[P::V2];
 #pragma unroll
             for (int p = 0; p < P::V2; ++p) y[p] = mul2(mul2(h[i][p], both(rq)), wq[i].get(p));
             P o;
             o.set(h[i]);
-            o.store(a.h, row * pieces + c);
+            put(o, a.h, i);
             o.set(y);
-            o.store(a.y, row * pieces + c);
+            put(o, a.y, i);
         }
         if (t == 0 && a.rstd) a.rstd[2 * row] = rp, a.rstd[2 * row + 1] = rq;
     }
@@ -273,7 +326,7 @@ __global__ void __launch_bounds__(512) forward_kernel(const Args a, int tw, int 
               return a.kind == RESIDUAL_GATE_NONE ? w : mul2(w, g[i].get(p));
           },
           a, red, turn, tw, warp);
-    r.store(wq, a, row, pieces, t, step);
+    r.store(wq, a, row, pieces, t, step, [&](const P &o, void *base, int i) { o.store(base, at + t + i * step); });
 }
 
 // The ring's shared memory: 208 KB for 512 threads' 16-byte pieces, as many rows as fit (a thread's row: `tensors` x
@@ -283,10 +336,12 @@ constexpr int ring_rows(int tensors, int iter) {
 }
 
 // Persistent: each team walks its rows, the next ones' pieces in flight.  RING: rows of the ring.
-template <typename T, int ITER, bool ELEMENT, int RING>
-__global__ void __launch_bounds__(512, 1) forward_ring_kernel(const Args a, int tw, int pieces) {
+// SHIFT: n is no multiple of a piece, so rows begin inside pieces; a team's rows are a multiple of a piece's elements
+// apart and all begin at the same place in one, so that its threads' columns, weights and sums stay what they are.
+template <typename T, int ITER, bool ELEMENT, bool SHIFT, int RING>
+__global__ void __launch_bounds__(512, 1) forward_ring_kernel(const Args a, int tw) {
     using P = Piece<T, true>;
-    constexpr int K = ELEMENT ? 3 : 2;
+    constexpr int K = ELEMENT ? 3 : 2, V = P::V;
     extern __shared__ uint4 ring[];  // [RING][K][ITER][512]
     __shared__ float red[32];
     if (threadIdx.x == 0) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -294,15 +349,20 @@ __global__ void __launch_bounds__(512, 1) forward_ring_kernel(const Args a, int 
     const int warp = threadIdx.x >> 5, teams = 16 / tw, team = warp / tw;
     const int t = (warp - team * tw) * 32 + (threadIdx.x & 31), step = 32 * tw;
     const int64_t first = (int64_t)blockIdx.x * teams + team, stride = (int64_t)gridDim.x * teams;
+    const int shift = SHIFT ? (int)(first * a.n % V) : 0, pieces = (a.n + shift + V - 1) / V;
+    const int64_t total = (int64_t)a.m * a.n;
     auto slot_of = [&](int slot, int k, int i) { return ring + ((slot * K + k) * ITER + i) * 512 + threadIdx.x; };
-    auto fetch = [&](int64_t row, int slot) {  // one group per row, empty past the last
+    auto base_of = [&](int64_t row) { return row * a.n / V; };  // the piece in which the row begins
+    auto fetch = [&](int64_t row, int slot) {                    // one group per row, empty past the last
 #pragma unroll
         for (int i = 0; i < ITER; ++i) {
             const int c = t + i * step;
             if (row < a.m && c < pieces) {
-                copy16(slot_of(slot, 0, i), static_cast<const uint4 *>(a.f) + row * pieces + c);
-                copy16(slot_of(slot, 1, i), static_cast<const uint4 *>(a.x) + row * pieces + c);
-                if (ELEMENT) copy16(slot_of(slot, 2, i), static_cast<const uint4 *>(a.gate) + row * pieces + c);
+                const int64_t at = base_of(row) + c, left = total - at * V;
+                const int bytes = !SHIFT || left >= V ? 16 : (int)left * (int)sizeof(T);
+                copy16(slot_of(slot, 0, i), static_cast<const uint4 *>(a.f) + at, bytes);
+                copy16(slot_of(slot, 1, i), static_cast<const uint4 *>(a.x) + at, bytes);
+                if (ELEMENT) copy16(slot_of(slot, 2, i), static_cast<const uint4 *>(a.gate) + at, bytes);
             }
         }
         copies_end();
@@ -317,8 +377,14 @@ __global__ void __launch_bounds__(512, 1) forward_ring_kernel(const Args a, int 
         P wp, g;
         wp.zero(), g.zero(), wq[i].zero();
         if (c < pieces) {
-            wp.load(a.w_post, c), wq[i].load(a.w_pre, c);
-            if (a.kind == RESIDUAL_GATE_CHANNEL) g.load(a.gate, c);
+            if (SHIFT) {
+                const Span<T> span(c, shift, a.n);
+                span.load(wp, a.w_post), span.load(wq[i], a.w_pre);
+                if (a.kind == RESIDUAL_GATE_CHANNEL) span.load(g, a.gate);
+            } else {
+                wp.load(a.w_post, c), wq[i].load(a.w_pre, c);
+                if (a.kind == RESIDUAL_GATE_CHANNEL) g.load(a.gate, c);
+            }
         }
 #pragma unroll
         for (int p = 0; p < P::V2; ++p) {
@@ -338,12 +404,22 @@ __global__ void __launch_bounds__(512, 1) forward_ring_kernel(const Args a, int 
             if (t + i * step < pieces) {
                 f[i].raw = *slot_of(slot, 0, i), x[i].raw = *slot_of(slot, 1, i);
                 if (ELEMENT) g[i].raw = *slot_of(slot, 2, i);
+                if (SHIFT) {
+                    const uint4 keep = Span<T>(t + i * step, shift, a.n).keep();
+                    f[i].raw = f[i].raw & keep, x[i].raw = x[i].raw & keep, g[i].raw = g[i].raw & keep;
+                }
             }
         }
         ForwardRow<T, ITER, true> r;
         r.run(f, x, [&](int i, int p) { return ELEMENT ? mul2(coef[i][p], g[i].get(p)) : coef[i][p]; }, a, red, turn, tw,
               warp);
-        r.store(wq, a, row, pieces, t, step);
+        const int64_t at = base_of(row) + t;
+        r.store(wq, a, row, pieces, t, step, [&](const P &o, void *base, int i) {
+            if (SHIFT)
+                Span<T>(t + i * step, shift, a.n).store(o, base, at + i * step);
+            else
+                o.store(base, at + i * step);
+        });
         slot = slot == RING - 1 ? 0 : slot + 1;
     }
     copies_wait<0>();
@@ -354,11 +430,11 @@ __global__ void __launch_bounds__(512, 1) forward_ring_kernel(const Args a, int 
 // so that both statistics of a row come from four sums of one pass, one reduction and one barrier.  The sums over
 // rows are post = sum of G F rp (times the gate where it is per element) and pre = sum of dY H rq:
 // dW_post = scale gate post and dgate = scale W_post post for a channel's gate, so one sum serves both.
-// VEC: a ring of RING rows as in the forward; else the next row's elements wait in registers.
-template <typename T, int ITER, bool VEC, bool ELEMENT, int RING>
-__global__ void __launch_bounds__(512, 1) backward_kernel(const Args a, int tw, int pieces) {
+// VEC: a ring of RING rows and SHIFT as in the forward; else the next row's elements wait in registers.
+template <typename T, int ITER, bool VEC, bool ELEMENT, bool SHIFT, int RING>
+__global__ void __launch_bounds__(512, 1) backward_kernel(const Args a, int tw) {
     using P = Piece<T, VEC>;
-    constexpr int V2 = P::V2, K = ELEMENT ? 5 : 4;  // 0 f, 1 h, 2 dy, 3 dh, 4 gate
+    constexpr int V = P::V, V2 = P::V2, K = ELEMENT ? 5 : 4;  // 0 f, 1 h, 2 dy, 3 dh, 4 gate
     extern __shared__ uint4 ring[];  // VEC: [RING][K][ITER][512]; then the teams' sums [2][n]
     __shared__ float red[128];
     if (threadIdx.x == 0) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -366,6 +442,9 @@ __global__ void __launch_bounds__(512, 1) backward_kernel(const Args a, int tw, 
     const int warp = threadIdx.x >> 5, teams = 16 / tw, team = warp / tw;
     const int t = (warp - team * tw) * 32 + (threadIdx.x & 31), step = 32 * tw;
     const int64_t first = (int64_t)blockIdx.x * teams + team, stride = (int64_t)gridDim.x * teams;
+    const int shift = SHIFT ? (int)(first * a.n % V) : 0, pieces = (a.n + shift + V - 1) / V;
+    const int64_t total = (int64_t)a.m * a.n;
+    auto base_of = [&](int64_t row) { return row * a.n / V; };  // the piece in which the row begins
     P next[VEC ? 1 : K][VEC ? 1 : ITER];
     auto slot_of = [&](int slot, int k, int i) { return ring + ((slot * K + k) * ITER + i) * 512 + threadIdx.x; };
     auto fetch = [&](int64_t row, int slot) {
@@ -376,11 +455,15 @@ __global__ void __launch_bounds__(512, 1) backward_kernel(const Args a, int tw, 
             for (int i = 0; i < ITER; ++i) {
                 const int c = t + i * step;
                 const bool in = row < a.m && c < pieces && src;
+                const int64_t at = base_of(row) + c;
                 if constexpr (VEC) {
-                    if (in) copy16(slot_of(slot, k, i), static_cast<const uint4 *>(src) + row * pieces + c);
+                    const int64_t left = total - at * V;
+                    if (in)
+                        copy16(slot_of(slot, k, i), static_cast<const uint4 *>(src) + at,
+                               !SHIFT || left >= V ? 16 : (int)left * (int)sizeof(T));
                 } else {
                     next[k][i].zero();
-                    if (in) next[k][i].load(src, row * pieces + c);
+                    if (in) next[k][i].load(src, at);
                 }
             }
         }
@@ -400,8 +483,14 @@ __global__ void __launch_bounds__(512, 1) backward_kernel(const Args a, int tw, 
         const int c = t + i * step;
         wp[i].zero(), wq[i].zero(), gc[i].zero();
         if (c < pieces) {
-            wp[i].load(a.w_post, c), wq[i].load(a.w_pre, c);
-            if (a.kind == RESIDUAL_GATE_CHANNEL) gc[i].load(a.gate, c);
+            if constexpr (SHIFT) {
+                const Span<T> span(c, shift, a.n);
+                span.load(wp[i], a.w_post), span.load(wq[i], a.w_pre);
+                if (a.kind == RESIDUAL_GATE_CHANNEL) span.load(gc[i], a.gate);
+            } else {
+                wp[i].load(a.w_post, c), wq[i].load(a.w_pre, c);
+                if (a.kind == RESIDUAL_GATE_CHANNEL) gc[i].load(a.gate, c);
+            }
         }
 #pragma unroll
         for (int p = 0; p < V2; ++p) post[i][p] = pre[i][p] = both(0.f);
@@ -432,7 +521,15 @@ __global__ void __launch_bounds__(512, 1) backward_kernel(const Args a, int tw, 
                 p.raw = *slot_of(slot, k, i);
             else
                 p = cur[k][i];
+            if constexpr (SHIFT) p.raw = p.raw & Span<T>(t + i * step, shift, a.n).keep();
             return p;
+        };
+        const int64_t at = base_of(row);
+        auto put = [&](const P &o, void *base, int c) {
+            if constexpr (SHIFT)
+                Span<T>(c, shift, a.n).store(o, base, at + c);
+            else
+                o.store(base, at + c);
         };
         float2 s1 = both(0.f), s2 = both(0.f), s3 = both(0.f), s4 = both(0.f);
 #pragma unroll
@@ -484,12 +581,12 @@ __global__ void __launch_bounds__(512, 1) backward_kernel(const Args a, int tw, 
                 }
             }
             o.set(df);
-            o.store(a.df, row * pieces + c);
+            put(o, a.df, c);
             o.set(g);
-            o.store(a.dx, row * pieces + c);
+            put(o, a.dx, c);
             if (ELEMENT) {
                 o.set(dg);
-                o.store(a.dgate, row * pieces + c);
+                put(o, a.dgate, c);
             }
         }
         if (VEC && RING == 1) fetch(row + stride, 0);  // the row is read: its place is the next one's
@@ -508,7 +605,8 @@ __global__ void __launch_bounds__(512, 1) backward_kernel(const Args a, int tw, 
             if (c >= pieces) continue;
 #pragma unroll
             for (int e = 0; e < P::V; ++e) {
-                const int j = c * P::V + e;
+                const int j = c * V + e - shift;
+                if (SHIFT && (j < 0 || j >= a.n)) continue;
                 const float x = e % 2 ? post[i][e / 2].y : post[i][e / 2].x, y = e % 2 ? pre[i][e / 2].y : pre[i][e / 2].x;
                 dst[j] = x + (k ? all[j] : 0.f);
                 dst[a.n + j] = y + (k ? all[a.n + j] : 0.f);
@@ -635,10 +733,10 @@ int check(const residual_rmsnorm_params *p, int dtype, const void *gate, const P
     return (aligned(ptr, e) && ...) && aligned(gate, e) ? DGRAD_OK : DGRAD_ERR_ALIGNMENT;
 }
 
-int blocks_of(const residual_rmsnorm_params *p) { return p->m < (uint32_t)kMaxBlocks ? (int)p->m : kMaxBlocks; }
-
+// One partial row of both sums per block, at most (m rounded up to 8, so that shifted rows keep their places).
 size_t workspace_bytes_of(const residual_rmsnorm_params *p) {
-    return (size_t)blocks_of(p) * 2 * p->n * sizeof(float);
+    const size_t blocks = p->m < (uint32_t)kMaxBlocks ? (p->m + 7) / 8 * 8 : kMaxBlocks;
+    return blocks * 2 * p->n * sizeof(float);
 }
 
 // A launch that may start while the kernel before it ends (each kernel waits before it touches memory).
@@ -671,9 +769,11 @@ Layout layout_of(int64_t pieces, int most) {
     return {0, 0};
 }
 
+// All of these at 16 bytes.  For the [m][n] tensors it is the condition of 16-byte pieces; rows may begin inside one,
+// and vectors of n values may lie anywhere, but then the kernels with `shifted` rows take them.
 template <typename... P>
-bool vector_applies(int n, size_t esize, const P *...ptr) {
-    return (size_t)n * esize % 16 == 0 && (aligned(ptr, 16) && ...);
+bool at_piece(const P *...ptr) {
+    return (aligned(ptr, 16) && ...);
 }
 
 // Dynamic shared memory above 48 KB is allowed once per kernel and device.
@@ -690,14 +790,14 @@ int allow_smem(K kern, size_t smem, std::atomic<uint64_t> &configured) {
     return DGRAD_OK;
 }
 
-template <typename T, int ITER, bool ELEMENT>
-int forward_ring(const Args &a, int tw, int pieces, cudaStream_t st) {
+template <typename T, int ITER, bool ELEMENT, bool SHIFT>
+int forward_ring(const Args &a, int tw, cudaStream_t st) {
     constexpr int R = ring_rows(ELEMENT ? 3 : 2, ITER);
     const size_t smem = (size_t)R * (ELEMENT ? 3 : 2) * ITER * 512 * 16;
     static std::atomic<uint64_t> configured{0};
-    auto kern = forward_ring_kernel<T, ITER, ELEMENT, R>;
+    auto kern = forward_ring_kernel<T, ITER, ELEMENT, SHIFT, R>;
     const int rc = allow_smem(kern, smem, configured);
-    return rc != DGRAD_OK ? rc : launch(kern, kMaxBlocks, 512, smem, st, a, tw, pieces);
+    return rc != DGRAD_OK ? rc : launch(kern, kMaxBlocks, 512, smem, st, a, tw);
 }
 
 template <typename T, int ITER, bool VEC>
@@ -706,60 +806,88 @@ int forward_direct(const Args &a, int tw, int pieces, cudaStream_t st) {
     return launch(forward_kernel<T, ITER, VEC>, ((int64_t)a.m + teams - 1) / teams, 32 * warps, 0, st, a, tw, pieces);
 }
 
+template <typename T, int ITER, bool SHIFT>
+int forward_kind(const Args &a, int tw, cudaStream_t st) {
+    if (a.kind == RESIDUAL_GATE_ELEMENT) return forward_ring<T, ITER, true, SHIFT>(a, tw, st);
+    return forward_ring<T, ITER, false, SHIFT>(a, tw, st);
+}
+
 template <typename T, int ITER>
-int forward_vec(const Args &a, int tw, int pieces, cudaStream_t st) {
-    if (a.m <= kRingRows * kMaxBlocks * (16 / tw)) return forward_direct<T, ITER, true>(a, tw, pieces, st);
-    if (a.kind == RESIDUAL_GATE_ELEMENT) return forward_ring<T, ITER, true>(a, tw, pieces, st);
-    return forward_ring<T, ITER, false>(a, tw, pieces, st);
+int forward_vec(const Args &a, int tw, bool few, bool shifted, int pieces, cudaStream_t st) {
+    if (few) return forward_direct<T, ITER, true>(a, tw, pieces, st);
+    return shifted ? forward_kind<T, ITER, true>(a, tw, st) : forward_kind<T, ITER, false>(a, tw, st);
 }
 
 template <typename T>
 int forward_t(const Args &a, cudaStream_t st) {
-    const bool vec = vector_applies(a.n, sizeof(T), a.f, a.x, a.gate, a.w_post, a.w_pre, a.h, a.y);
-    const int pieces = vec ? a.n * (int)sizeof(T) / 16 : a.n;
-    const Layout l = layout_of(pieces, vec ? 4 : 8);
-    if (vec && l.iter == 1) return forward_vec<T, 1>(a, l.warps, pieces, st);
-    if (vec && l.iter == 2) return forward_vec<T, 2>(a, l.warps, pieces, st);
-    if (vec && l.iter == 4) return forward_vec<T, 4>(a, l.warps, pieces, st);
-    if (l.iter == 1 || l.iter == 2) return forward_direct<T, 2, false>(a, l.warps, pieces, st);
-    if (l.iter == 4 || l.iter == 8) return forward_direct<T, 8, false>(a, l.warps, pieces, st);
+    constexpr int V = 16 / (int)sizeof(T);
+    const bool element = a.kind == RESIDUAL_GATE_ELEMENT;
+    const bool vec = at_piece(a.f, a.x, element ? a.gate : nullptr, a.h, a.y);
+    const bool shifted = a.n % V != 0 || !at_piece(a.w_post, a.w_pre, element ? nullptr : a.gate);
+    if (vec) {
+        const Layout l = layout_of((a.n + (shifted ? V - 1 : 0) + V - 1) / V, 4);
+        const bool few = a.m <= kRingRows * kMaxBlocks * (16 / (l.iter ? l.warps : 16));
+        if (!few || !shifted) {  // one row per team needs no ring, but has no use for shifted pieces
+            const int pieces = a.n / V;
+            if (l.iter == 1) return forward_vec<T, 1>(a, l.warps, few, shifted, pieces, st);
+            if (l.iter == 2) return forward_vec<T, 2>(a, l.warps, few, shifted, pieces, st);
+            if (l.iter == 4) return forward_vec<T, 4>(a, l.warps, few, shifted, pieces, st);
+        }
+    }
+    const Layout l = layout_of(a.n, 8);
+    if (l.iter == 1 || l.iter == 2) return forward_direct<T, 2, false>(a, l.warps, a.n, st);
+    if (l.iter == 4 || l.iter == 8) return forward_direct<T, 8, false>(a, l.warps, a.n, st);
     forward_row_kernel<T><<<a.m, kThreads, 0, st>>>(a);
     return cudaGetLastError() == cudaSuccess ? DGRAD_OK : DGRAD_ERR_CUDA;
 }
 
-template <typename T, int ITER, bool VEC, bool ELEMENT>
-int backward_iter(const Args &a, int tw, int pieces, cudaStream_t st) {
+template <typename T, int ITER, bool VEC, bool ELEMENT, bool SHIFT>
+int backward_iter(const Args &a, int tw, cudaStream_t st) {
     constexpr int K = ELEMENT ? 5 : 4, R = VEC ? ring_rows(K, ITER) : 1;
     const size_t row = VEC ? (size_t)K * ITER * 512 * 16 : 0, sums = tw < 16 ? (size_t)2 * a.n * sizeof(float) : 0;
     const size_t smem = std::max(R * row, sums);
     static std::atomic<uint64_t> configured{0};
-    auto kern = backward_kernel<T, ITER, VEC, ELEMENT, R>;
+    auto kern = backward_kernel<T, ITER, VEC, ELEMENT, SHIFT, R>;
     const int rc = allow_smem(kern, smem, configured);
-    return rc != DGRAD_OK ? rc : launch(kern, a.blocks, 512, smem, st, a, tw, pieces);
+    return rc != DGRAD_OK ? rc : launch(kern, a.blocks, 512, smem, st, a, tw);
 }
-template <typename T, int ITER, bool VEC>
-int backward_kind(const Args &a, int tw, int pieces, cudaStream_t st) {
-    if (a.kind == RESIDUAL_GATE_ELEMENT) return backward_iter<T, ITER, VEC, true>(a, tw, pieces, st);
-    return backward_iter<T, ITER, VEC, false>(a, tw, pieces, st);
+template <typename T, int ITER, bool VEC, bool SHIFT>
+int backward_kind(const Args &a, int tw, cudaStream_t st) {
+    if (a.kind == RESIDUAL_GATE_ELEMENT) return backward_iter<T, ITER, VEC, true, SHIFT>(a, tw, st);
+    return backward_iter<T, ITER, VEC, false, SHIFT>(a, tw, st);
+}
+template <typename T, int ITER>
+int backward_vec(const Args &a, int tw, bool shifted, cudaStream_t st) {
+    return shifted ? backward_kind<T, ITER, true, true>(a, tw, st) : backward_kind<T, ITER, true, false>(a, tw, st);
 }
 
 template <typename T>
 int backward_rows(Args &a, cudaStream_t st) {
-    const void *dgate = a.kind == RESIDUAL_GATE_ELEMENT ? a.dgate : nullptr;
-    const bool vec =
-        vector_applies(a.n, sizeof(T), a.f, a.h, a.gate, a.w_post, a.w_pre, a.dy, a.dh, a.df, a.dx, dgate);
-    const int pieces = vec ? a.n * (int)sizeof(T) / 16 : a.n;
-    const Layout l = layout_of(pieces, vec ? (sizeof(T) == 4 ? 4 : 2) : 8);
-    if (l.iter) {
-        const int64_t teams = 16 / l.warps, need = (a.m + teams - 1) / teams;
-        a.blocks = need < a.blocks ? (int)need : a.blocks;
+    constexpr int V = 16 / (int)sizeof(T);
+    const bool element = a.kind == RESIDUAL_GATE_ELEMENT;
+    const bool vec = at_piece(a.f, a.h, a.dy, a.dh, a.df, a.dx, element ? a.gate : nullptr, element ? a.dgate : nullptr);
+    const bool shifted = a.n % V != 0 || !at_piece(a.w_post, a.w_pre, element ? nullptr : a.gate);
+    // Blocks for m rows in teams, few enough that each has a row -- with shifted rows, in steps that keep the rows of a
+    // team a multiple of V apart (152 is one).
+    auto blocks_for = [&](int warps) {
+        const int64_t teams = 16 / warps, need = (a.m + teams - 1) / teams;
+        const int64_t unit = vec && shifted && teams < V ? V / teams : 1, n = (need + unit - 1) / unit * unit;
+        return (int)(n < kMaxBlocks ? n : kMaxBlocks);
+    };
+    if (vec) {
+        const Layout l = layout_of((a.n + (shifted ? V - 1 : 0) + V - 1) / V, sizeof(T) == 4 ? 4 : 2);
+        if (l.iter) a.blocks = blocks_for(l.warps);
+        if (l.iter == 1) return backward_vec<T, 1>(a, l.warps, shifted, st);
+        if (l.iter == 2) return backward_vec<T, 2>(a, l.warps, shifted, st);
+        if constexpr (sizeof(T) == 4)
+            if (l.iter == 4) return backward_vec<T, 4>(a, l.warps, shifted, st);
+    } else {
+        const Layout l = layout_of(a.n, 8);
+        if (l.iter) a.blocks = blocks_for(l.warps);
+        if (l.iter == 1 || l.iter == 2) return backward_kind<T, 2, false, false>(a, l.warps, st);
+        if (l.iter == 4 || l.iter == 8) return backward_kind<T, 8, false, false>(a, l.warps, st);
     }
-    if (vec && l.iter == 1) return backward_kind<T, 1, true>(a, l.warps, pieces, st);
-    if (vec && l.iter == 2) return backward_kind<T, 2, true>(a, l.warps, pieces, st);
-    if constexpr (sizeof(T) == 4)
-        if (vec && l.iter == 4) return backward_kind<T, 4, true>(a, l.warps, pieces, st);
-    if (!vec && (l.iter == 1 || l.iter == 2)) return backward_kind<T, 2, false>(a, l.warps, pieces, st);
-    if (!vec && (l.iter == 4 || l.iter == 8)) return backward_kind<T, 8, false>(a, l.warps, pieces, st);
+    a.blocks = a.m < kMaxBlocks ? a.m : kMaxBlocks;
     backward_row_kernel<T><<<a.blocks, kThreads, 0, st>>>(a);
     return cudaGetLastError() == cudaSuccess ? DGRAD_OK : DGRAD_ERR_CUDA;
 }
@@ -818,7 +946,6 @@ int residual_rmsnorm_backward(const void *f, const void *h, const void *gate, co
     a.rstd = const_cast<float *>(rstd), a.dy = dy, a.dh = dh, a.df = df, a.dx = dx, a.dgate = dgate;
     a.dw_post = dw_post, a.dw_pre = dw_pre, a.partial = static_cast<float *>(workspace);
     a.m = (int)p->m, a.n = (int)p->n, a.kind = (int)p->gate_kind, a.eps = p->eps, a.scale = p->scale;
-    a.blocks = blocks_of(p);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     if (dtype == DGRAD_F32) return backward_t<float>(a, st);
     if (dtype == DGRAD_BF16) return backward_t<__nv_bfloat16>(a, st);

@@ -66,11 +66,12 @@ def within(got, ref, bound, what):
     return float(err.max() / max(np.abs(ref).max(), 1e-30))
 
 
-def check(dg, m, n, gate, dtype, scale=0.7, offset=0, in_place=False, with_dh=True, seed=0):
+def check(dg, m, n, gate, dtype, scale=0.7, offset=0, in_place=False, with_dh=True, seed=0, vectors=None):
     d = inputs(m, n, gate, dtype, seed)
     t, code = TORCH[dtype], dg.DTYPE_CODE[dtype]
     p = dg.ResidualRmsnormParams(m, n, KIND[gate], EPS, scale)
-    c = {k: placed(v, offset) for k, v in d.items()}
+    c = {k: placed(v, vectors if vectors is not None and v is not None and v.dim() == 1 else offset)
+         for k, v in d.items()}
     yb, y = guarded((m, n), t, offset)
     hb, h = guarded((m, n), t, offset)
     rb, rstd = guarded((m, 2), torch.float32)
@@ -114,7 +115,8 @@ def check(dg, m, n, gate, dtype, scale=0.7, offset=0, in_place=False, with_dh=Tr
 
 
 # One row; widths below, at and above vectors, warps and blocks; more rows than blocks; a wide row.
-SIZES = [(1, 1), (1, 1024), (3, 7), (700, 64), (5, 96), (33, 1001), (650, 256), (17, 2048), (9, 4096), (4, 5000),
+# Widths that are no multiple of a 16-byte piece have rows that begin inside one, with one row per team and with many.
+SIZES = [(1200, 577), (650, 2050), (333, 4090), (2500, 9), (153, 130), (9, 6883), (1, 1), (1, 1024), (3, 7), (700, 64), (5, 96), (33, 1001), (650, 256), (17, 2048), (9, 4096), (4, 5000),
          (3, 8192), (2, 20000)]
 
 
@@ -130,6 +132,13 @@ def test_both_directions(dg, m, n, gate, dtype, parity_log):
 def test_off_alignment(dg, gate, dtype):
     check(dg, 20, 1024, gate, dtype, offset=1)
     check(dg, 20, 512, gate, dtype, offset=4 if dtype == "bf16" else 2)
+
+
+@pytest.mark.parametrize("gate", ["channel", "element"])
+@pytest.mark.parametrize("m,n", [(700, 577), (650, 1024), (2, 1001)])
+def test_vectors_off_alignment(dg, m, n, gate):
+    """The weights (and a channel's gate) lie anywhere; the [m, n] tensors are aligned."""
+    check(dg, m, n, gate, "bf16", vectors=3)
 
 
 @pytest.mark.parametrize("n", [512, 333])
