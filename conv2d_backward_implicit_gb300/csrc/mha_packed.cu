@@ -60,7 +60,7 @@ int validate(const mha_packed_params *p, int dtype) {
 template <typename... P>
 bool tc_applies(const mha_packed_params *p, int dtype, const P *...ptr) {
     return dtype != DGRAD_F32 && p->head_dim % 8 == 0 && p->head_dim <= 128 && p->q_stride % 8 == 0 &&
-           p->k_stride % 8 == 0 && p->v_stride % 8 == 0 && (aligned(ptr, 16) && ...);
+           p->k_stride % 8 == 0 && p->v_stride % 8 == 0 && (aligned(ptr, 16) && ... && true);
 }
 
 int choose(bool tc) {
@@ -97,11 +97,16 @@ Args make_args(const void *q, const void *k, const void *v, const int32_t *off, 
     return a;
 }
 
-// The statistics of every head and row, behind a header of two maxima.
+// A header of two maxima, the statistics of every head and row, and the tensor-core kernel's partial dK and dV.
 constexpr size_t kHeader = 256;
 
-size_t workspace_bytes_of(const mha_packed_params *p) {
-    return kHeader + (size_t)p->tokens * p->num_heads * sizeof(float2);
+size_t stats_bytes_of(const mha_packed_params *p) {
+    return ((size_t)p->tokens * p->num_heads * sizeof(float2) + 255) / 256 * 256;
+}
+size_t workspace_bytes_of(const mha_packed_params *p, int dtype) {
+    const int split = tc_applies(p, dtype) ? key_split(p) : 1;
+    const size_t part = (size_t)p->tokens * p->num_kv_heads * p->head_dim * 2 * sizeof(float);
+    return kHeader + stats_bytes_of(p) + (split > 1 ? split * part : 0);
 }
 
 }  // namespace
@@ -126,7 +131,7 @@ int mha_packed_forward(const void *q, const void *k, const void *v, const int32_
 }
 
 size_t mha_packed_workspace_size(const mha_packed_params *p, int dtype) {
-    return mhapk::validate(p, dtype) == DGRAD_OK ? mhapk::workspace_bytes_of(p) : 0;
+    return mhapk::validate(p, dtype) == DGRAD_OK ? mhapk::workspace_bytes_of(p, dtype) : 0;
 }
 
 int mha_packed_backward(const void *q, const void *k, const void *v, const void *o, const void *d_out,
@@ -139,12 +144,13 @@ int mha_packed_backward(const void *q, const void *k, const void *v, const void 
     if (kern < 0) return -kern;
     if (!seq_offsets || !lse || !workspace) return DGRAD_ERR_INVALID_ARG;
     if (!aligned(seq_offsets, 4) || !aligned(lse, 4) || !aligned(workspace, 16)) return DGRAD_ERR_ALIGNMENT;
-    if (workspace_bytes < workspace_bytes_of(p)) return DGRAD_ERR_WORKSPACE;
+    if (workspace_bytes < workspace_bytes_of(p, dtype)) return DGRAD_ERR_WORKSPACE;
     Args a = make_args(q, k, v, seq_offsets, p);
     a.o = o, a.go = d_out;
     a.lse_in = lse;
     a.dq = dq, a.dk = dk, a.dv = dv;
     a.stats = reinterpret_cast<float2 *>(static_cast<char *>(workspace) + kHeader);
+    a.part = reinterpret_cast<float *>(static_cast<char *>(workspace) + kHeader + stats_bytes_of(p));
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     if (kern == DGRAD_KERNEL_TC) return backward_tc(a, static_cast<unsigned *>(workspace), p, dtype, st);
     return run_simt(backward_simt_f32, backward_simt_bf16, backward_simt_f16, a, p, dtype, st);

@@ -2,11 +2,12 @@
 // sequences (include/mha_packed.h): bf16 / fp16, head_dim a multiple of 8 up to 128
 // (padded to D = 64 or 128 by the TMA copies' zero fill), sm_103a.
 //
-// Two launches.  The first makes, per head and position, the folded statistic
+// Two launches, and a third where blocks share keys.  The first makes, per head and position, the folded statistic
 // (m + l) log2(e) and delta = dO . O.  The second has one block per work unit of
 // 128 resident rows, of two kinds with one body:
 //   keys resident (R1 = K, R2 = V; streamed X1 = Q, X2 = dO, over the query blocks that
-//   reach them and the heads of the group):  dK = acc1, dV = acc2;
+//   reach them and the heads of the group):  dK = acc1, dV = acc2 -- with few such units
+//   the heads are dealt to several blocks, whose float32 sums the third launch adds;
 //   queries resident (R1 = Q, R2 = dO; streamed X1 = K, X2 = V):  dQ = acc1.
 // For every step of 128 streamed rows (columns below):
 //   S = R1 X1^T, G = R2 X2^T      tcgen05 M128 N128 K16, D / 16 steps each
@@ -88,6 +89,7 @@ struct BwdArgs {
     CUtensorMap q_map, k_map, v_map, go_map, dq_map, dk_map, dv_map;
     const unsigned *norms;  // fp16: bits of max |dO row|^2, max |V row|^2
     unsigned key_units;     // blocks [0, key_units) have keys resident
+    int split;              // blocks that share a tile of keys
     uint32_t idesc1, idesc2;
 };
 
@@ -100,15 +102,15 @@ struct Ctl {
 };
 static_assert(sizeof(Ctl) <= 1024, "control block too large");
 
-// The streamed rows [lo, hi) of a unit in steps of 128, each for `heads` query heads: step j is rows lo + 128 (j / heads)
-// of head j % heads.
+// The streamed rows [lo, hi) of a unit in steps of 128, each for `heads` query heads from h0 on: step j is rows
+// lo + 128 (j / heads) of head h0 + j % heads.
 struct Walk {
-    int lo, hi, heads;
+    int lo, hi, heads, h0;
     __device__ __forceinline__ int steps() const { return (hi - lo + kRows - 1) / kRows * heads; }
 };
 // Walks the steps without a division each.
 struct Cursor {
-    int row, r;  // first row of the step, head of the group
+    int row, r;  // first row of the step, head (less h0)
     __device__ __forceinline__ void next(const Walk &k) {
         if (++r == k.heads) r = 0, row += kRows;
     }
@@ -130,12 +132,11 @@ __device__ __forceinline__ Walk walk_of(const Args &a, const Unit &u, int live) 
         w.lo = u.p0;
         w.hi = u.len;
         if (a.window > 0 && u.p0 + live - 1 < u.len - a.window) w.hi = u.p0 + live - 1 + a.window;
-        w.heads = a.hpk;
     } else {
         w.lo = a.window > 0 && u.p0 - a.window + 1 > 0 ? (u.p0 - a.window + 1) / 64 * 64 : 0;
         w.hi = u.p0 + live;
-        w.heads = 1;
     }
+    w.heads = 1, w.h0 = 0;
     return w;
 }
 
@@ -264,7 +265,7 @@ __device__ void role_load(const BwdArgs &p, Ctl &c, uint32_t smem, const Unit &u
     Cursor at{k.lo, 0};
     int n1 = 0, n2 = 0;
     for (int j = 0; j < n; ++j, at.next(k)) {
-        const int h = KEYS ? g * p.a.hpk + at.r : g, row = u.begin + at.row;
+        const int h = KEYS ? k.h0 + at.r : g, row = u.begin + at.row;
         auto load1 = [&] {
             if (!wait(su32(&c.x1_empty[a.slot]), a.phase ^ 1u, w)) return false;
             load_rows<D>(smem + C::kOffX1 + (uint32_t)a.slot * C::kTile, x1, p.a.hd, h, row, kRows,
@@ -296,14 +297,14 @@ __device__ void role_load(const BwdArgs &p, Ctl &c, uint32_t smem, const Unit &u
 
 // Statistics of each step's 128 queries: -stat of all, then -delta of all.
 template <int D, bool F16>
-__device__ void role_stats(const BwdArgs &p, Ctl &c, uint32_t smem, const Unit &u, const Walk &k, int g, float kappa,
-                           int lane, const Waiter &w) {
+__device__ void role_stats(const BwdArgs &p, Ctl &c, uint32_t smem, const Unit &u, const Walk &k, float kappa, int lane,
+                           const Waiter &w) {
     const int n = k.steps();
     const float shift = F16 ? kPShift : 0.f;
     Ring<kStatSlots> ring;
     Cursor at{k.lo, 0};
     for (int j = 0; j < n; ++j, at.next(k), ring.next()) {
-        const float2 *st = p.a.stats + (int64_t)(g * p.a.hpk + at.r) * p.a.tokens + u.begin;
+        const float2 *st = p.a.stats + (int64_t)(k.h0 + at.r) * p.a.tokens + u.begin;
         float2 x[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -462,6 +463,11 @@ __device__ __forceinline__ void grads32(const uint32_t (&p)[32], const uint32_t 
     }
 }
 
+// Row `token` of KV head g in split z's partial dK (which 0) or dV (1).
+__device__ __forceinline__ float *part_row(const Args &a, int z, int which, int64_t token, int g) {
+    return a.part + ((((int64_t)z * 2 + which) * a.tokens + token) * a.nkv + g) * a.hd;
+}
+
 template <int D, bool F16, bool KEYS>
 __device__ void role_soft(const BwdArgs &p, Ctl &c, uint32_t smem, uint32_t tmem, const Unit &u, const Walk &k, int live,
                           int head, float sigma, int warp, int lane, const Waiter &w) {
@@ -565,6 +571,27 @@ __device__ void role_soft(const BwdArgs &p, Ctl &c, uint32_t smem, uint32_t tmem
     if (!KEYS && grp == 1) return;
     constexpr int W = D / 2;
     const float factor = grp == 0 ? a.scale / sigma : (F16 ? 0x1p-13f : 1.f);
+    if (KEYS && p.split > 1) {  // float32 partial sums: each thread its row
+        float2 odd = make_float2(0.f, 0.f);
+        float *dst = part_row(a, k.h0 / k.heads % p.split, grp, (int64_t)u.begin + row, head) + W * part;
+#pragma unroll
+        for (int b = 0; b < W; b += 32) {
+            uint32_t o[32];
+            tc_ld_32x32(tmem + lane_tm + (grp == 0 ? C::kColAcc1 : C::kColAcc2) + W * part + b, o);
+            tc_wait_ld(o);
+#pragma unroll
+            for (int e = 0; e < 32; e += 4) {
+                const float2 f2 = make_float2(factor, factor), z2 = make_float2(0.f, 0.f);
+                const float2 x = __fmul2_rn(make_float2(__uint_as_float(o[e]), __uint_as_float(o[e + 1])), f2);
+                const float2 y = __fmul2_rn(make_float2(__uint_as_float(o[e + 2]), __uint_as_float(o[e + 3])), f2);
+                odd = __ffma2_rn(x, z2, __ffma2_rn(y, z2, odd));
+                if (row < u.len && W * part + b + e < a.hd)
+                    *reinterpret_cast<float4 *>(dst + b + e) = make_float4(x.x, x.y, y.x, y.y);
+            }
+        }
+        if (__any_sync(0xffffffffu, row < u.len && !(odd.x + odd.y == 0.f)) && lane == 0) c.bad = 1;
+        return;
+    }
     const CUtensorMap *map = grp == 1 ? &p.dv_map : KEYS ? &p.dk_map : &p.dq_map;
     const bool good = store_rows<W, F16>(tmem + lane_tm + (grp == 0 ? C::kColAcc1 : C::kColAcc2) + W * part,
                                          smem + C::kOffR + (uint32_t)grp * C::kTile + (uint32_t)(warp & 7) * (C::kTile / 8),
@@ -578,7 +605,7 @@ __device__ void role_soft(const BwdArgs &p, Ctl &c, uint32_t smem, uint32_t tmem
 
 // The unit's rows one by one over the attended pairs alone, one warp per row.
 template <int D, bool F16, bool KEYS>
-__device__ __noinline__ void recompute(const Args &a, const Unit &u, int live, int head) {
+__device__ __noinline__ void recompute(const Args &a, const Unit &u, int live, int head, int h0, int heads_of, int split) {
     using T = typename std::conditional<F16, __half, __nv_bfloat16>::type;
     constexpr int N = D / 32;
     const int lane = threadIdx.x & 31, warps = blockDim.x >> 5, heads = KEYS ? a.nkv : a.nh;
@@ -597,8 +624,8 @@ __device__ __noinline__ void recompute(const Args &a, const Unit &u, int live, i
             lo = a.window > 0 && row - a.window + 1 > 0 ? row - a.window + 1 : 0;
         }
         for (int x = lo; x < hi; ++x)
-            for (int z = 0; z < (KEYS ? a.hpk : 1); ++z) {
-                const int h = KEYS ? head * a.hpk + z : head, g = h / a.hpk;
+            for (int z = 0; z < (KEYS ? heads_of : 1); ++z) {
+                const int h = KEYS ? h0 + z : head, g = h / a.hpk;
                 const int64_t pos = (int64_t)u.begin + (KEYS ? x : row), t = (int64_t)u.begin + (KEYS ? row : x);
                 const T *qr = q + pos * a.qs + (int64_t)h * a.hd, *kr = k + t * a.ks + (int64_t)g * a.hd;
                 const T *vr = v + t * a.vs + (int64_t)g * a.hd, *gr = go + (pos * a.nh + h) * a.hd;
@@ -626,6 +653,12 @@ __device__ __noinline__ void recompute(const Args &a, const Unit &u, int live, i
         for (int i = 0; i < N; ++i) {
             const int d = lane + 32 * i;
             if (d >= a.hd) continue;
+            if (KEYS && split > 1) {
+                const int z = h0 / heads_of % split;
+                part_row(a, z, 0, (int64_t)u.begin + row, head)[d] = acc1[i] * a.scale;
+                part_row(a, z, 1, (int64_t)u.begin + row, head)[d] = acc2[i];
+                continue;
+            }
             static_cast<T *>(KEYS ? a.dk : a.dq)[at + d] = from_f<T>(acc1[i] * a.scale);
             if (KEYS) static_cast<T *>(a.dv)[at + d] = from_f<T>(acc2[i]);
         }
@@ -637,6 +670,8 @@ __device__ __forceinline__ void unit_body(const BwdArgs &p, Ctl &c, uint32_t sme
                                           bool check, int warp, int lane) {
     using C = Cfg<D>;
     const unsigned heads = KEYS ? p.a.nkv : p.a.nh;
+    const int z = KEYS ? (int)(index % (unsigned)p.split) : 0;
+    if (KEYS) index /= (unsigned)p.split;
     const int head = (int)(index % heads), g = KEYS ? head : head / p.a.hpk;
     const Unit u = find_unit(p.a, index / heads, 7, !KEYS, check, &g_bwd_error_word, c.lookup);
     if (!u.live) return;
@@ -645,6 +680,11 @@ __device__ __forceinline__ void unit_body(const BwdArgs &p, Ctl &c, uint32_t sme
         for (int r = warp; r < live; r += kThreads / 32) {
             const int64_t at = (((int64_t)u.begin + u.p0 + r) * heads + head) * p.a.hd;
             for (int d = lane; d < p.a.hd; d += 32) {
+                if (KEYS && p.split > 1) {
+                    const int64_t token = (int64_t)u.begin + u.p0 + r;
+                    part_row(p.a, z, 0, token, head)[d] = part_row(p.a, z, 1, token, head)[d] = 0.f;
+                    continue;
+                }
                 static_cast<uint16_t *>(KEYS ? p.a.dk : p.a.dq)[at + d] = 0;
                 if (KEYS) static_cast<uint16_t *>(p.a.dv)[at + d] = 0;
             }
@@ -652,14 +692,15 @@ __device__ __forceinline__ void unit_body(const BwdArgs &p, Ctl &c, uint32_t sme
         return;
     }
     const Waiter w{&c.abort_flag, &g_bwd_error_word};
-    const Walk k = walk_of<KEYS>(p.a, u, live);
+    Walk k = walk_of<KEYS>(p.a, u, live);
+    if (KEYS) k.heads = p.a.hpk / p.split, k.h0 = head * p.a.hpk + z * k.heads;
     const float sigma = ds_scale<F16>(p);
     if (warp < kSoftWarps) {
         role_soft<D, F16, KEYS>(p, c, smem, tmem, u, k, live, head, sigma, warp, lane, w);
     } else if (warp == kMmaWarp || warp == kMmaWarp + 1) {
         const int second = warp - kMmaWarp;
         const uint32_t sm = uniform(smem), tm = uniform(tmem);
-        const Walk ku{uniform(k.lo), uniform(k.hi), uniform(k.heads)};
+        const Walk ku{uniform(k.lo), uniform(k.hi), uniform(k.heads), uniform(k.h0)};
         if (second)
             issue<D, KEYS, false>(p, c, sm, tm, uniform(u.len), ku, lane, w);
         else
@@ -671,7 +712,7 @@ __device__ __forceinline__ void unit_body(const BwdArgs &p, Ctl &c, uint32_t sme
         if (lane == 0) role_load<D, KEYS>(p, c, smem, u, k, head, g, w);
         __syncwarp();
     } else if (KEYS) {
-        role_stats<D, F16>(p, c, smem, u, k, g, F16 ? sigma * 0x1p-13f : 1.f, lane, w);
+        role_stats<D, F16>(p, c, smem, u, k, F16 ? sigma * 0x1p-13f : 1.f, lane, w);
     }
     tc_before();
     __syncthreads();
@@ -679,7 +720,7 @@ __device__ __forceinline__ void unit_body(const BwdArgs &p, Ctl &c, uint32_t sme
     if (c.bad && !c.abort_flag) {
         if (lane == 0) stores_done();
         __syncthreads();
-        recompute<D, F16, KEYS>(p.a, u, live, head);
+        recompute<D, F16, KEYS>(p.a, u, live, head, k.h0, k.heads, p.split);
     }
 }
 
@@ -741,6 +782,41 @@ __global__ void __launch_bounds__(kThreads, 1) backward_tc_kernel(const __grid_c
     if (warp == kMmaWarp) tc_dealloc(tmem, 512);
 }
 
+// ------------------------------------------------------------ third launch
+// dK and dV from the splits' partial sums, in the splits' order; a thread takes 8 elements of one of the two.
+template <bool F16>
+__global__ void __launch_bounds__(256) join_kernel(const Args a, int split) {
+    if (threadIdx.x == 0) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int64_t n = (int64_t)a.tokens * a.nkv * a.hd, at = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 8;
+    const int which = (int)blockIdx.y;
+    if (at >= n) return;
+    float4 x = make_float4(0.f, 0.f, 0.f, 0.f), y = x;
+    for (int z = 0; z < split; ++z) {
+        const float4 *src = reinterpret_cast<const float4 *>(a.part + ((int64_t)z * 2 + which) * n + at);
+        const float4 u = __ldcg(src), v = __ldcg(src + 1);
+        x.x += u.x, x.y += u.y, x.z += u.z, x.w += u.w;
+        y.x += v.x, y.y += v.y, y.z += v.z, y.w += v.w;
+    }
+    *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(which ? a.dv : a.dk) + at) =
+        make_uint4(pack2<F16>(x.x, x.y), pack2<F16>(x.z, x.w), pack2<F16>(y.x, y.y), pack2<F16>(y.z, y.w));
+}
+
+int launch_join(const Args &a, int split, bool f16, cudaStream_t st) {
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)(((int64_t)a.tokens * a.nkv * a.hd / 8 + 255) / 256), 2);
+    cfg.blockDim = dim3(256);
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    const cudaError_t e = f16 ? cudaLaunchKernelEx(&cfg, join_kernel<true>, a, split)
+                              : cudaLaunchKernelEx(&cfg, join_kernel<false>, a, split);
+    return e == cudaSuccess ? DGRAD_OK : DGRAD_ERR_CUDA;
+}
+
 template <int D, bool F16>
 int launch(const BwdArgs &q, int64_t blocks, cudaStream_t st) {
     static std::atomic<uint64_t> configured{0};
@@ -789,14 +865,18 @@ int backward_tc(const Args &a, unsigned *norms, const mha_packed_params *p, int 
         !encode_store(&q.dv_map, a.dv, a.tokens, a.nkv, a.hd, D / 2))
         return DGRAD_ERR_UNSUPPORTED;
     const bool f16 = dtype == DGRAD_F16;
-    const int rc = f16 ? launch_stats<__half>(a, norms, st) : launch_stats<__nv_bfloat16>(a, norms, st);
+    int rc = f16 ? launch_stats<__half>(a, norms, st) : launch_stats<__nv_bfloat16>(a, norms, st);
     if (rc != DGRAD_OK) return rc;
     const int64_t units = unit_bound(p, kRows);
-    const int64_t blocks = units * (a.nkv + a.nh);
+    q.split = key_split(p);
+    const int64_t blocks = units * ((int64_t)a.nkv * q.split + a.nh);
     if (blocks > INT32_MAX) return DGRAD_ERR_UNSUPPORTED;
-    q.key_units = (unsigned)(units * a.nkv);
-    if (D == 64) return f16 ? launch<64, true>(q, blocks, st) : launch<64, false>(q, blocks, st);
-    return f16 ? launch<128, true>(q, blocks, st) : launch<128, false>(q, blocks, st);
+    q.key_units = (unsigned)(units * a.nkv * q.split);
+    if (D == 64)
+        rc = f16 ? launch<64, true>(q, blocks, st) : launch<64, false>(q, blocks, st);
+    else
+        rc = f16 ? launch<128, true>(q, blocks, st) : launch<128, false>(q, blocks, st);
+    return rc == DGRAD_OK && q.split > 1 ? launch_join(a, q.split, f16, st) : rc;
 }
 
 }  // namespace mhapk

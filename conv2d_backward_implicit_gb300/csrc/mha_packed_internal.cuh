@@ -27,6 +27,7 @@ struct Args {
     const float *lse_in;
     float *lse;
     float2 *stats;  // workspace: [heads][tokens] (statistic, delta)
+    float *part;    // workspace: [split][dK, dV][tokens][KV heads][head_dim], with split > 1
     int tokens, seqs, nh, nkv, hpk, hd, window;
     int64_t qs, ks, vs;  // elements between two tokens' rows
     float scale;         // 1 / sqrt(head_dim)
@@ -44,6 +45,29 @@ struct Unit {
 // floor(tokens / rows) + the number of segments.
 inline int64_t unit_bound(const mha_packed_params *p, int rows) {
     return (int64_t)p->tokens / rows + p->num_seqs + 2;
+}
+
+// Blocks that share the keys of one tile in the tensor-core backward, each with as many of the group's query heads: the
+// divisor of the group with the least estimated time, for sequences of the mean length.  A block takes one step of 128
+// x 128 pairs after another, so without sharing a block with all queries and heads of the group may last longer than
+// everything else (1 KV head, 8 heads of 128, 2048 tokens: 171 us, shared by 8 blocks 51); but float32 sums then pass
+// through the workspace and a third launch adds them (8 KV heads, 32 heads of 128, 2048 tokens: 107 us, shared by 2
+// blocks 131).  A step takes 1.3 us (0.85 at head_dim up to 64); sharing about 18 us and the sums' bytes at 5 TB/s.
+inline int key_split(const mha_packed_params *p) {
+    const int hpk = (int)(p->num_heads / p->num_kv_heads);
+    if (hpk == 1 || p->num_seqs == 0) return 1;
+    const double len = (double)p->tokens / p->num_seqs, blocks = len < 128 ? 1 : len / 128, step = p->head_dim <= 64 ? 0.85 : 1.3;
+    const double all = p->num_seqs * blocks * (blocks + 1) / 2 * p->num_heads * 2 / 152;  // steps of an SM's share
+    const double bytes = (double)p->tokens * p->num_kv_heads * p->head_dim * 2 * 4 * 2;   // of one block's sums, both ways
+    int best = 1;
+    double least = 0;
+    for (int s = 1; s <= hpk; ++s) {
+        if (hpk % s != 0) continue;
+        const double longest = blocks * hpk / s;
+        const double us = (longest > all ? longest : all) * step + (s > 1 ? 18 + s * bytes / 5e6 : 0);
+        if (s == 1 || us < least) best = s, least = us;
+    }
+    return best;
 }
 
 __device__ __forceinline__ int clamp_row(int x, int tokens) { return x < 0 ? 0 : (x > tokens ? tokens : x); }

@@ -173,6 +173,37 @@ def test_cuda_core_kernels(dg, case, dtype, parity_log):
         dg.mha_packed_set_kernel(dg.DGRAD_KERNEL_AUTO)
 
 
+# Few KV heads and many tokens: the heads of a group are dealt to several blocks, and a third launch adds their sums.
+SHARED = {
+    "shared keys": ([2000], 8, 1, 64),
+    "shared keys padded": ([1500, 40], 12, 1, 128, 0, 5, 130),
+    "shared keys window": ([1700], 8, 1, 80, 900),
+}
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("case", list(SHARED))
+def test_blocks_that_share_keys(dg, case, dtype, parity_log):
+    lens, H, G, d, *rest = SHARED[case]
+    p = Problem(lens, H, G, d, dtype=dtype, seed=5, **dict(zip(("window", "head", "tail"), rest)))
+    plain = 256 + (p.T * H * 8 + 255) // 256 * 256
+    assert dg.mha_packed_workspace_size(p.params(dg), dg.DTYPE_CODE[dtype]) > plain  # room for the partial sums
+    check_backward(dg, p, dg.DGRAD_KERNEL_TC, parity_log, f"tc {dtype} {case}")
+
+
+def test_shared_keys_recompute_what_is_not_finite(dg):
+    """A query row that is not finite early in the sequence: later keys' gradients stay finite and right."""
+    p = Problem([1600], 8, 1, 64, dtype="bf16", seed=6)
+    p.q[1, :, 2] = float("nan")
+    with np.errstate(all="ignore"):
+        qkv = p.f64("q", "k", "v")
+        ref_o, ref_l = om.forward(*qkv, p.offsets, 0)
+        o_in, l_in = torch.from_numpy(ref_o).to(torch.bfloat16), torch.from_numpy(ref_l).float()
+        refs = om.backward(*qkv, o_in.double().numpy(), p.f64("go")[0], l_in.double().numpy(), p.offsets, 0)
+    for name, got, ref in zip(("dQ", "dK", "dV"), run_backward(dg, p, o_in, l_in), refs):
+        within(got, ref, 8 * 2.0 ** -7 * np.abs(ref[np.isfinite(ref)]).max(), name)
+
+
 # More key blocks than ring stages, tiles and blocks that end inside a sequence, windows that skip blocks.
 LONG = {
     "long": ([1000], 4, 2, 128),
