@@ -174,8 +174,7 @@ __device__ __forceinline__ float transpose_sum(float (&v)[G], int piece) {
 // One warp per head and run of 32 positions: G lanes take a row's 16-byte pieces, 32 / G rows a turn, G turns.
 template <typename T, int G>
 __global__ void __launch_bounds__(256) stats_kernel(const Args a, unsigned *norms) {
-    if (threadIdx.x == 0) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    grid_begin();
     constexpr bool F16 = std::is_same<T, __half>::value;
     constexpr int PER = 32 / G, BATCH = G < 8 ? G : 8;  // rows a turn; turns whose loads are in flight together
     const int lane = threadIdx.x & 31, piece = lane % G, sub = lane / G;
@@ -183,7 +182,7 @@ __global__ void __launch_bounds__(256) stats_kernel(const Args a, unsigned *norm
     const unsigned own = runs * (unsigned)a.nh;
     const bool has = piece * 8 < a.hd;
     int first = 0, last = 0;  // the rows of sequences
-    if (F16) first = clamp_row(__ldg(a.off), a.tokens), last = clamp_row(__ldg(a.off + a.seqs), a.tokens);
+    if (F16) first = clamp_row(a.off[0], a.tokens), last = clamp_row(a.off[a.seqs], a.tokens);
     float norm = 0.f;
     if (w < own) {
         const int h = (int)(w % (unsigned)a.nh), t0 = (int)(w / (unsigned)a.nh) * 32;
@@ -198,8 +197,8 @@ __global__ void __launch_bounds__(256) stats_kernel(const Args a, unsigned *norm
             for (int i = 0; i < BATCH; ++i) {
                 x[i] = y[i] = make_uint4(0, 0, 0, 0);
                 if (has && t0 + sub + (b + i) * PER < a.tokens) {
-                    x[i] = __ldg(reinterpret_cast<const uint4 *>(o + (b + i) * PER * step));
-                    y[i] = __ldg(reinterpret_cast<const uint4 *>(go + (b + i) * PER * step));
+                    x[i] = *reinterpret_cast<const uint4 *>(o + (b + i) * PER * step);
+                    y[i] = *reinterpret_cast<const uint4 *>(go + (b + i) * PER * step);
                 }
             }
 #pragma unroll
@@ -232,7 +231,7 @@ __global__ void __launch_bounds__(256) stats_kernel(const Args a, unsigned *norm
         for (int i = 0; i < G; ++i) {
             n[i] = 0.f;
             if (has && t0 + sub + i * PER < a.tokens) {
-                const uint4 y = __ldg(reinterpret_cast<const uint4 *>(v + i * PER * a.vs));
+                const uint4 y = *reinterpret_cast<const uint4 *>(v + i * PER * a.vs);
                 const T *ys = reinterpret_cast<const T *>(&y);
 #pragma unroll
                 for (int e = 0; e < 8; ++e) n[i] = fmaf(to_f(ys[e]), to_f(ys[e]), n[i]);
@@ -309,7 +308,7 @@ __device__ void role_stats(const BwdArgs &p, Ctl &c, uint32_t smem, const Unit &
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const int col = at.row + 4 * lane + i;
-            x[i] = col < u.len ? __ldg(st + col) : make_float2(0.f, 0.f);
+            x[i] = col < u.len ? st[col] : make_float2(0.f, 0.f);
         }
         if (!wait_warp(su32(&c.st_empty[ring.slot]), ring.phase ^ 1u, w)) return;
         const uint32_t dst = smem + Cfg<D>::kOffStat + (uint32_t)ring.slot * kStatBytes + (uint32_t)lane * 16u;
@@ -480,7 +479,7 @@ __device__ void role_soft(const BwdArgs &p, Ctl &c, uint32_t smem, uint32_t tmem
     const float cs = a.scale * kLog2e, kappa = F16 ? sigma * 0x1p-13f : 1.f;
     float nl = 0.f, nd = 0.f;
     if (!KEYS && row < u.len) {
-        const float2 st = __ldg(a.stats + (int64_t)head * a.tokens + u.begin + row);
+        const float2 st = a.stats[(int64_t)head * a.tokens + u.begin + row];
         nl = (F16 ? kPShift : 0.f) - st.x, nd = -st.y * kappa;
     }
     if (!KEYS) {
@@ -772,8 +771,7 @@ __global__ void __launch_bounds__(kThreads, 1) backward_tc_kernel(const __grid_c
     __syncthreads();
     tc_after();
     const uint32_t tmem = c.tmem_base;
-    if (threadIdx.x == 0) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    grid_begin();
     if (blockIdx.x < p.key_units)
         unit_body<D, F16, true>(p, c, smem, tmem, blockIdx.x, blockIdx.x == 0, warp, lane);
     else
@@ -786,15 +784,14 @@ __global__ void __launch_bounds__(kThreads, 1) backward_tc_kernel(const __grid_c
 // dK and dV from the splits' partial sums, in the splits' order; a thread takes 8 elements of one of the two.
 template <bool F16>
 __global__ void __launch_bounds__(256) join_kernel(const Args a, int split) {
-    if (threadIdx.x == 0) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    grid_begin();
     const int64_t n = (int64_t)a.tokens * a.nkv * a.hd, at = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 8;
     const int which = (int)blockIdx.y;
     if (at >= n) return;
     float4 x = make_float4(0.f, 0.f, 0.f, 0.f), y = x;
     for (int z = 0; z < split; ++z) {
         const float4 *src = reinterpret_cast<const float4 *>(a.part + ((int64_t)z * 2 + which) * n + at);
-        const float4 u = __ldcg(src), v = __ldcg(src + 1);
+        const float4 u = src[0], v = src[1];
         x.x += u.x, x.y += u.y, x.z += u.z, x.w += u.w;
         y.x += v.x, y.y += v.y, y.z += v.z, y.w += v.w;
     }

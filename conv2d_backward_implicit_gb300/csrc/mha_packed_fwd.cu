@@ -428,8 +428,7 @@ __global__ void __launch_bounds__(kThreads, 1) forward_tc_kernel(const __grid_co
     __syncthreads();
     tc_after();
     const uint32_t tmem = c.tmem_base;
-    if (threadIdx.x == 0) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    grid_begin();
 
     const unsigned pairs = p.pair_heads ? p.a.nh / 2 : p.a.nh;
     const int pair = (int)(blockIdx.x % pairs);

@@ -11,6 +11,7 @@
 #include <cstdint>
 #include <type_traits>
 
+#include "grid_begin.cuh"
 #include "mha_packed.h"
 
 namespace mhapk {
@@ -76,11 +77,11 @@ __device__ __forceinline__ int clamp_row(int x, int tokens) { return x < 0 ? 0 :
 __device__ __forceinline__ void segment(const Args &a, int i, int &begin, int &len) {
     int lo, hi;
     if (i < a.seqs) {
-        lo = __ldg(a.off + i), hi = __ldg(a.off + i + 1);
+        lo = a.off[i], hi = a.off[i + 1];
     } else if (i == a.seqs) {
-        lo = 0, hi = __ldg(a.off);
+        lo = 0, hi = a.off[0];
     } else {
-        lo = __ldg(a.off + a.seqs), hi = a.tokens;
+        lo = a.off[a.seqs], hi = a.tokens;
     }
     begin = clamp_row(lo, a.tokens);
     hi = clamp_row(hi, a.tokens);
@@ -100,7 +101,7 @@ struct Lookup {  // its shared memory
     Unit found;
 };
 __device__ __forceinline__ void check_offsets(const Args &a, int i, unsigned *error) {
-    const int lo = __ldg(a.off + i), hi = __ldg(a.off + i + 1);
+    const int lo = a.off[i], hi = a.off[i + 1];
     if (lo < 0 || hi < lo || hi > a.tokens) atomicOr(error, kErrOffsets);
 }
 __device__ __forceinline__ unsigned scan32(unsigned x, int lane) {  // inclusive

@@ -45,7 +45,7 @@ __device__ __forceinline__ void load_pieces(float *dst, const T *src, int64_t st
     for (int e = threadIdx.x; e < ROWS * (D / V); e += kThreads) {
         const int r = e / (D / V), d = (e - r * (D / V)) * V;
         R w{};
-        if (r < live && d < hd) w = __ldg(reinterpret_cast<const R *>(src + (int64_t)r * stride + d));
+        if (r < live && d < hd) w = *reinterpret_cast<const R *>(src + (int64_t)r * stride + d);
         const T *h = reinterpret_cast<const T *>(&w);
 #pragma unroll
         for (int i = 0; i < V; ++i) dst[r * P + d + i] = to_f(h[i]);
@@ -151,8 +151,7 @@ __global__ void __launch_bounds__(kThreads) forward_simt_kernel(const Args a, un
     constexpr int P = D + 4;
     extern __shared__ float4 sm4[];
     float *q_s = reinterpret_cast<float *>(sm4), *k_s = q_s + kRes * P, *v_s = k_s + kStr * P, *p_s = v_s + kStr * P;
-    if (threadIdx.x == 0) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    grid_begin();
     const int ty = threadIdx.x >> 4, tx = threadIdx.x & 15;
     const int h = (int)(blockIdx.x % (unsigned)a.nh), g = h / a.hpk;
     const Unit u = find_unit(a, blockIdx.x / (unsigned)a.nh, 5, true, blockIdx.x == 0, error);
@@ -240,8 +239,7 @@ __global__ void __launch_bounds__(kThreads) forward_simt_kernel(const Args a, un
 // delta = dO . O of every row and head into stats[h][row].y; one warp per row and head.
 template <typename T>
 __global__ void __launch_bounds__(256) delta_simt_kernel(const Args a) {
-    if (threadIdx.x == 0) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    grid_begin();
     const int64_t w = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
     if (w >= (int64_t)a.tokens * a.nh) return;
     const T *o = static_cast<const T *>(a.o) + w * a.hd, *go = static_cast<const T *>(a.go) + w * a.hd;
@@ -321,8 +319,8 @@ __device__ __forceinline__ void backward_unit(const Args &a, unsigned block, uns
                         if (pos < u.len && t <= pos && (a.window == 0 || pos - t < a.window)) {
                             const int64_t at = (int64_t)u.begin + pos;
                             const float *l = a.lse_in + (at * a.nh + h) * 2;
-                            p = expf(s[i][j] * a.scale - __ldg(l) - __ldg(l + 1));
-                            d = p * (dp[i][j] - __ldg(&a.stats[(int64_t)h * a.tokens + at].y));
+                            p = expf(s[i][j] * a.scale - l[0] - l[1]);
+                            d = p * (dp[i][j] - a.stats[(int64_t)h * a.tokens + at].y);
                         }
                         ds_s[(4 * ty + i) * kP + tx + 16 * j] = d;
                         if (KEYS) p_s[(4 * ty + i) * kP + tx + 16 * j] = p;
@@ -380,8 +378,7 @@ template <typename T, int D>
 __global__ void __launch_bounds__(kThreads) backward_simt_kernel(const Args a, unsigned key_blocks, int split,
                                                                  unsigned *error) {
     extern __shared__ float4 sm4[];
-    if (threadIdx.x == 0) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    grid_begin();
     if (blockIdx.x < key_blocks)
         backward_unit<T, D, true>(a, blockIdx.x, error, split, reinterpret_cast<float *>(sm4));
     else

@@ -29,6 +29,7 @@
 #include <cstdint>
 #include <type_traits>
 
+#include "grid_begin.cuh"
 #include "nvtx_range.h"
 #include "residual_rmsnorm.h"
 
@@ -145,7 +146,7 @@ struct Piece {
     using Raw = typename std::conditional<VEC, uint4, T>::type;
     Raw raw;
     __device__ __forceinline__ void load(const void *base, int64_t piece) {
-        raw = __ldg(static_cast<const Raw *>(base) + piece);
+        raw = static_cast<const Raw *>(base)[piece];
     }
     __device__ __forceinline__ void zero() { raw = Raw{}; }
     __device__ __forceinline__ float2 get(int p) const {
@@ -213,7 +214,7 @@ struct Span {
     __device__ __forceinline__ void load(P &p, const void *src) const {
 #pragma unroll
         for (int e = 0; e < P::V; ++e)
-            if (e >= lo && e < hi) p.at(e) = __ldg(static_cast<const T *>(src) + j0 + e);
+            if (e >= lo && e < hi) p.at(e) = static_cast<const T *>(src)[j0 + e];
     }
     // The row's own elements of a piece.
     __device__ __forceinline__ void store(P p, void *base, int64_t piece) const {
@@ -299,8 +300,7 @@ template <typename T, int ITER, bool VEC>
 __global__ void __launch_bounds__(512) forward_kernel(const Args a, int tw, int pieces) {
     using P = Piece<T, VEC>;
     __shared__ float red[32];
-    if (threadIdx.x == 0) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    grid_begin();
     const int warp = threadIdx.x >> 5, teams = (int)(blockDim.x >> 5) / tw, team = warp / tw;
     const int64_t row = (int64_t)blockIdx.x * teams + team;
     if (row >= a.m) return;  // the whole team
@@ -344,8 +344,7 @@ __global__ void __launch_bounds__(512, 1) forward_ring_kernel(const Args a, int 
     constexpr int K = ELEMENT ? 3 : 2, V = P::V;
     extern __shared__ uint4 ring[];  // [RING][K][ITER][512]
     __shared__ float red[32];
-    if (threadIdx.x == 0) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    grid_begin();
     const int warp = threadIdx.x >> 5, teams = 16 / tw, team = warp / tw;
     const int t = (warp - team * tw) * 32 + (threadIdx.x & 31), step = 32 * tw;
     const int64_t first = (int64_t)blockIdx.x * teams + team, stride = (int64_t)gridDim.x * teams;
@@ -437,8 +436,7 @@ __global__ void __launch_bounds__(512, 1) backward_kernel(const Args a, int tw) 
     constexpr int V = P::V, V2 = P::V2, K = ELEMENT ? 5 : 4;  // 0 f, 1 h, 2 dy, 3 dh, 4 gate
     extern __shared__ uint4 ring[];  // VEC: [RING][K][ITER][512]; then the teams' sums [2][n]
     __shared__ float red[128];
-    if (threadIdx.x == 0) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    grid_begin();
     const int warp = threadIdx.x >> 5, teams = 16 / tw, team = warp / tw;
     const int t = (warp - team * tw) * 32 + (threadIdx.x & 31), step = 32 * tw;
     const int64_t first = (int64_t)blockIdx.x * teams + team, stride = (int64_t)gridDim.x * teams;
@@ -471,7 +469,7 @@ __global__ void __launch_bounds__(512, 1) backward_kernel(const Args a, int tw) 
     };
     float2 rstd_next = both(0.f);
     auto fetch_rstd = [&](int64_t row) {
-        if (row < a.m) rstd_next = make_float2(__ldg(a.rstd + 2 * row), __ldg(a.rstd + 2 * row + 1));
+        if (row < a.m) rstd_next = make_float2(a.rstd[2 * row], a.rstd[2 * row + 1]);
     };
 #pragma unroll
     for (int s = 0; s < (RING > 1 ? RING - 1 : 1); ++s) fetch(first + s * stride, s);
@@ -683,14 +681,13 @@ __global__ void __launch_bounds__(kThreads) backward_row_kernel(const Args a) {
 template <typename T>
 __global__ void __launch_bounds__(kThreads) partial_sum_kernel(const Args a) {
     __shared__ float s[kThreads / 32][32];
-    if (threadIdx.x == 0) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    grid_begin();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int64_t j = (int64_t)blockIdx.x * 32 + lane;
     float t = 0.f;
     if (j < 2 * (int64_t)a.n) {
 #pragma unroll 8
-        for (int b = warp; b < a.blocks; b += kThreads / 32) t += __ldcg(a.partial + (int64_t)b * 2 * a.n + j);
+        for (int b = warp; b < a.blocks; b += kThreads / 32) t += a.partial[(int64_t)b * 2 * a.n + j];
     }
     s[warp][lane] = t;
     __syncthreads();

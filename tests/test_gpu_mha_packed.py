@@ -152,6 +152,7 @@ CASES = {
     "head 8": ([70], 2, 1, 8),
     "head 40": ([333], 2, 2, 40, 33),
     "nothing but padding": ([0, 0], 2, 1, 64, 0, 5, 140),
+    "no sequence": ([], 2, 2, 64, 0, 3, 70),
 }
 
 
@@ -344,6 +345,75 @@ def test_gradients_against_differences(dg):
         want = (loss[0] - loss[1]) / (2 * h)
         terms = (grad.double().cpu() * direction.double())
         assert abs(float(terms.sum()) - want) <= 1e-2 * float(terms.square().sum().sqrt()) + 1e-3
+
+
+@pytest.mark.parametrize("dtype,d", [("bf16", 64), ("f16", 128), ("f32", 64)])
+def test_captured_in_a_graph(dg, dtype, d):
+    """Both directions replayed from a CUDA graph on new inputs give what calls give."""
+    p = Problem([200, 75], 4, 1, d, tail=5, dtype=dtype, seed=1)
+    other = Problem([200, 75], 4, 1, d, tail=5, dtype=dtype, seed=2)
+    t, code, params = TORCH[dtype], dg.DTYPE_CODE[dtype], p.params(dg)
+    q, k, v, go = p.q.cuda(), p.k.cuda(), p.v.cuda(), p.go.cuda()
+    off = torch.tensor(p.offsets, dtype=torch.int32, device="cuda")
+    o, lse = torch.empty_like(q), torch.empty(p.T, 4, 2, device="cuda")
+    dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
+    size = dg.mha_packed_workspace_size(params, code)
+    ws = torch.empty(size, dtype=torch.uint8, device="cuda")
+
+    def both():
+        s = torch.cuda.current_stream()
+        dg.mha_packed_forward(q, k, v, off, o, lse, params, code, s)
+        dg.mha_packed_backward(q, k, v, o, go, lse, off, dq, dk, dv, ws, size, params, code, s)
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        both()
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        both()
+    for buf, new in ((q, other.q), (k, other.k), (v, other.v), (go, other.go)):
+        buf.copy_(new.cuda())
+    for out in (o, lse, dq, dk, dv):
+        out.zero_()
+    for _ in range(3):  # replays one after another, each waiting for the last
+        graph.replay()
+    torch.cuda.synchronize()
+    got = [x.clone() for x in (o, lse, dq, dk, dv)]
+    both()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, (o, lse, dq, dk, dv)))
+    assert dg.mha_packed_check_errors() == 0
+
+
+def test_calls_in_a_row_read_what_the_last_one_wrote(dg):
+    """Forward and backward over and over on the same buffers with new inputs, nothing waiting between: the launches
+    overlap at their edges, and each must see its predecessor's results."""
+    a, b = (Problem([300, 128, 41], 4, 2, 64, dtype="bf16", seed=s) for s in (1, 2))
+    want = []
+    for p in (a, b):
+        o, lse = run_forward(dg, p)
+        want.append([o.cpu(), lse.cpu()] + [x.cpu() for x in run_backward(dg, p, o.cpu(), lse.cpu())])
+    params, code = a.params(dg), dg.DGRAD_BF16
+    q, k, v, go = (torch.empty_like(x, device="cuda") for x in (a.q, a.k, a.v, a.go))
+    off = torch.tensor(a.offsets, dtype=torch.int32, device="cuda")
+    o, lse = torch.empty_like(q), torch.empty(a.T, 4, 2, device="cuda")
+    grads = [torch.empty_like(x) for x in (q, k, v)]
+    size = dg.mha_packed_workspace_size(params, code)
+    ws = torch.empty(size, dtype=torch.uint8, device="cuda")
+    inputs = [[x.cuda() for x in (p.q, p.k, p.v, p.go)] for p in (a, b)]
+    got, s = [], torch.cuda.current_stream()
+    for i in range(20):
+        for buf, new in zip((q, k, v, go), inputs[i % 2]):
+            buf.copy_(new)
+        for _ in range(2):
+            dg.mha_packed_forward(q, k, v, off, o, lse, params, code, s)
+            dg.mha_packed_backward(q, k, v, o, go, lse, off, *grads, ws, size, params, code, s)
+        got.append([x.clone() for x in (o, lse, *grads)])
+    torch.cuda.synchronize()
+    for i, out in enumerate(got):
+        assert all(torch.equal(x.cpu(), y) for x, y in zip(out, want[i % 2])), i
 
 
 @pytest.mark.parametrize("offsets", [[0, 50, 40, 90], [-3, 50, 60, 90], [0, 50, 60, 1000]])
