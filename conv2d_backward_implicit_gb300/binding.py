@@ -416,25 +416,24 @@ def _dense(dtype, device: int, *buffers):
     """Addresses of dense buffers given as (x, name, elements, type), with ``dtype`` (a dgrad_dtype code) where the
     type is None.  These are the checks of _addr, one comparison per property for a tensor that passes them; whatever
     does not pass goes to _addr, which names what is wrong."""
-    types, out = _torch_types(), []
+    types, out = _types or _torch_types(), []
+    own = types.get(dtype)
     for x, name, numel, t in buffers:
-        if x is not None and type(x) is not int:
-            try:
-                if (x.get_device() == device and x.numel() == numel and x.is_contiguous()
-                        and x.dtype is types[dtype if t is None else t]):
-                    out.append(x.data_ptr())
-                    continue
-            except (AttributeError, KeyError):
-                pass
-            x = _addr(x, name, _in_dtype(dtype) if t is None else t, numel)
-        out.append(x)
+        try:
+            if (x.numel() == numel and x.dtype is (own if t is None else types[t]) and x.get_device() == device
+                    and x.is_contiguous()):
+                out.append(x.data_ptr())
+                continue
+        except AttributeError:  # None, an address, or no torch tensor
+            pass
+        out.append(_addr(x, name, _in_dtype(dtype) if t is None else t, numel))
     return out
 
 
-def _device_of(*tensors) -> int:
-    """The current device, or a number no tensor has when none of the arguments is on a GPU (then _addr says so)."""
-    if any(getattr(x, "is_cuda", False) for x in tensors):
-        return _torch_types()["current_device"]()
+def _device_of(x) -> int:
+    """The current device, or a number no tensor has when ``x`` is not on a GPU (then _addr says so)."""
+    if getattr(x, "is_cuda", False):
+        return (_types or _torch_types())["current_device"]()
     return -2
 
 
