@@ -20,7 +20,8 @@
 // acc2's place, the scores' A operand), and a ring of two (D = 128) or three
 // regions of 128 columns that takes S and G of step after step in turn, with P and dS
 // over the first 16 of each 32.  Steps of 128 columns because a product of N = 64 takes
-// nearly as long as one of N = 128 (65 against 75 cycles); what overlaps is then not two
+// nearly as long as one of N = 128 (50 cycles against 65 with both operands in shared
+// memory); what overlaps is then not two
 // steps but the two halves of one: while P of a step goes through acc2 and the region's
 // next scores, its dS is formed, and the other way round.
 //   * warps 0-15: P, then dS, 32 columns of one resident row per thread; at the end dK /

@@ -15,7 +15,7 @@
 // cp.async -- a thread copies and reads its own pieces only, so the ring needs no
 // barrier.  After the backward, teams add up their sums in a fixed order, each block
 // writes one partial row, and a second kernel adds those in a fixed order.
-// With few rows the forward takes one row per team and ends.
+// With few rows the forward takes one row per team and ends (kDirectHalfRows).
 //
 // Measured (bf16, 8192 x 4096, gate per channel): forward 47.5 us, 5.6 TB/s, 84% of the
 // measured copy rate; backward 87 us, 4.65 TB/s, 69%, bound by a row's latency at the 16
@@ -42,7 +42,10 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kMaxBlocks = 152;  // of the backward: one for each SM
-constexpr int kRingRows = 2;     // rows per team from which the forward's ring pays
+// The forward takes one row per team up to this many half rows for each team of the persistent form (16-byte rows 4096
+// wide: 1216 rows, 4 a team, 8.0 against 8.6 us, 2432 rows 15.3 against 14.9; shifted rows 4090 wide, whose other form
+// goes element by element: 152 rows, half a row a team, 4.1 against 4.5, 304 rows 7.3 against 6.2).
+constexpr int kDirectHalfRows = 12, kDirectHalfRowsShifted = 1;
 constexpr uint32_t kMaxN = 1u << 20;
 
 struct Args {
@@ -395,6 +398,11 @@ __global__ void __launch_bounds__(512, 1) forward_ring_kernel(const Args a, int 
             if (a.kind == RESIDUAL_GATE_CHANNEL) coef[i][p] = mul2(coef[i][p], g.get(p));
         }
     }
+    uint4 keep[SHIFT ? ITER : 1];  // the same for every row of the team
+    if constexpr (SHIFT) {
+#pragma unroll
+        for (int i = 0; i < ITER; ++i) keep[i] = Span<T>(t + i * step, shift, a.n).keep();
+    }
     int turn = 0, slot = 0;
     for (int64_t row = first; row < a.m; row += stride) {
         copies_wait<RING - 2>();  // RING - 1 rows are asked for: the oldest has landed
@@ -407,10 +415,8 @@ __global__ void __launch_bounds__(512, 1) forward_ring_kernel(const Args a, int 
             if (t + i * step < pieces) {
                 f[i].raw = *slot_of(slot, 0, i), x[i].raw = *slot_of(slot, 1, i);
                 if (ELEMENT) g[i].raw = *slot_of(slot, 2, i);
-                if (SHIFT) {
-                    const uint4 keep = Span<T>(t + i * step, shift, a.n).keep();
-                    f[i].raw = f[i].raw & keep, x[i].raw = x[i].raw & keep, g[i].raw = g[i].raw & keep;
-                }
+                if constexpr (SHIFT)
+                    f[i].raw = f[i].raw & keep[i], x[i].raw = x[i].raw & keep[i], g[i].raw = g[i].raw & keep[i];
             }
         }
         ForwardRow<T, ITER, true> r;
@@ -500,6 +506,11 @@ __global__ void __launch_bounds__(512, 1) backward_kernel(const Args a, int tw) 
     // scale W_post, and with it the gate: A.
     auto weight = [&](int i, int p) { return mul2(wp[i].get(p), both(a.scale)); };
     const bool channel = a.kind == RESIDUAL_GATE_CHANNEL;
+    uint4 keep[SHIFT ? ITER : 1];  // the same for every row of the team
+    if constexpr (SHIFT) {
+#pragma unroll
+        for (int i = 0; i < ITER; ++i) keep[i] = Span<T>(t + i * step, shift, a.n).keep();
+    }
     int turn = 0, slot = 0;
     for (int64_t row = first; row < a.m; row += stride) {
         P cur[VEC ? 1 : K][VEC ? 1 : ITER];
@@ -523,7 +534,7 @@ __global__ void __launch_bounds__(512, 1) backward_kernel(const Args a, int tw) 
                 p.raw = *slot_of(slot, k, i);
             else
                 p = cur[k][i];
-            if constexpr (SHIFT) p.raw = p.raw & Span<T>(t + i * step, shift, a.n).keep();
+            if constexpr (SHIFT) p.raw = p.raw & keep[i];
             return p;
         };
         const int64_t at = base_of(row);
@@ -827,7 +838,8 @@ int forward_t(const Args &a, cudaStream_t st) {
     const bool shifted = a.n % V != 0 || !at_piece(a.w_post, a.w_pre, element ? nullptr : a.gate);
     if (vec) {
         const Layout l = layout_of((a.n + (shifted ? V - 1 : 0) + V - 1) / V, 4);
-        const bool few = a.m <= kRingRows * kMaxBlocks * (16 / (l.iter ? l.warps : 16));
+        const int64_t limit = (int64_t)kMaxBlocks * (16 / (l.iter ? l.warps : 16));
+        const bool few = 2 * (int64_t)a.m <= limit * (shifted ? kDirectHalfRowsShifted : kDirectHalfRows);
         if (!few || !shifted) {  // one row per team needs no ring, but has no use for shifted pieces
             const int pieces = a.n / V;
             if (l.iter == 1) return forward_vec<T, 1>(a, l.warps, few, shifted, pieces, st);
