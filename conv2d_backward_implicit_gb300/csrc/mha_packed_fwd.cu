@@ -2,7 +2,7 @@
 // sequences (include/mha_packed.h): bf16 / fp16, head_dim a multiple of 8 up to 128
 // (padded to D = 64 or 128 by the TMA copies' zero fill), sm_103a.
 //
-// One block per work unit: two tiles of 128 queries that read the same K and V
+// A work unit is two tiles of 128 queries that read the same K and V
 // tiles -- two heads of one group at the same positions when the group is even, else
 // two runs of 128 positions of one head -- so that each byte of K and V that enters
 // shared memory serves 256 rows of scores.  For every block of 128 keys, from the
@@ -27,16 +27,19 @@
 //     warps, because a warp's waits otherwise stand between its products (2850 cycles per
 //     key block with one warp, of which 850 were waits).
 //   * warp 18 (one thread): TMA copies of the Q tiles, K and V.
+//   * warp 19: the walk.  The grid has a block per unit, longest first; a running block takes over the units of blocks
+//     that have not started, so tensor memory, barriers and the search for the first unit are paid once per SM, and the
+//     next unit's loads and first products run under the last one's end (118 us -> 104 us on the documents below).
 // V rows past the sequence's end are zeroed in shared memory (other sequences' rows,
 // possibly with infinities); what is masked inside the sequence has P = 0, and if a
-// value there is not finite the product with 0 leaves a NaN in O: the tile is then
-// recomputed row by row over the attended keys alone.
+// value there is not finite the product with 0 leaves a NaN in O: those rows are then
+// recomputed one by one over the attended keys alone.
 // Measured (bf16, head_dim 128): one sequence of 16384, 8 heads over 2: 330 us, 1666
 // TFLOP/s, 86% of a burst of large products; ten documents of 0 to 2048 tokens, 32 heads
-// over 8: 116 us, 896 TFLOP/s.  A key block (both tiles) takes 2,650 cycles, products
+// over 8: 104 us, 1000 TFLOP/s.  A key block (both tiles) takes 2,650 cycles, products
 // 2,048 of them: the time from a tile's scores to its P (1,150) is what the other tile's
-// products (1,024) do not cover.  A block's start and end take about 11,000 cycles more,
-// which is what bounds many short sequences.
+// products (1,024) do not cover.  A block's start takes 5,000 to 8,000 cycles more, and each
+// unit's end 7,000: the warps of a row meet, O leaves.
 // Every wait is bounded; on timeout the kernel raises its error word, lets the copies
 // and products in flight finish, frees tensor memory and returns.
 #include "mha_packed_tc.cuh"
@@ -59,7 +62,8 @@ constexpr int kRows = 128;                     // queries per tile, keys per ste
 constexpr uint32_t kHalf = kRows * 128;        // bytes of a [128][64] 16-bit half tile
 constexpr int kSoftWarps = 16, kMmaWarp = 16, kLoadWarp = 18;  // 16, 17: one for each tile
 constexpr uint32_t kColS = 0, kColO = 256;     // + 128 i, + 128 i
-constexpr int kThreads = 32 * (kLoadWarp + 1);
+constexpr int kWalkWarp = 19, kThreads = 32 * (kWalkWarp + 1);
+constexpr int kWalkers = kWalkWarp;            // warps that take units from the walk
 constexpr float kLag = 8.0f;                   // log2 of how far the scaling maximum may lag
 constexpr float kShift16 = 7.0f;               // log2 of fp16's scale of P: P <= 2^15, and 7 more bits below
 
@@ -76,16 +80,24 @@ struct Cfg {
 
 struct FwdArgs {
     Args a;
-    CUtensorMap q_map, k_map, v_map, o_map;
+    CUtensorMap q_map, k_map, v_map;
     uint32_t idesc1, idesc2;
     int pair_heads;  // the two tiles are two heads of a group (else two runs of positions)
+    int wide;        // rows of O are a multiple of 32 bytes apart
 };
 
+struct Work {
+    Unit u;
+    int pair, stop;
+};
 struct Ctl {
-    uint64_t q_full[2], k_full[4], k_empty[4], v_full[4], v_empty[4];
-    uint64_t s_full[2], p_ready[2], o_full[2], turn[2], mma_done[2];
+    uint4 answer;  // of the request for another block
+    uint64_t q_full[2], q_empty[2], k_full[4], k_empty[4], v_full[4], v_empty[4];
+    uint64_t s_full[2], p_ready[2], o_full[2], o_empty[2], turn[2], mma_done[2];
+    uint64_t work_full[2], work_empty[2], want, answered;
+    Work work[2];
     uint32_t tmem_base;
-    int abort_flag, bad[2];
+    int abort_flag;
 };
 static_assert(sizeof(Ctl) <= 1024, "control block too large");
 
@@ -106,93 +118,194 @@ __device__ __forceinline__ Tile tile_of(const FwdArgs &p, const Unit &u, int pai
     return t;
 }
 
-// The loading thread: what the first products need first (Q_0, K, Q_1, V), then K and V of block after block.
-template <int D>
-__device__ void role_load(const FwdArgs &p, Ctl &c, uint32_t smem, const Unit &u, const Tile (&t)[2], int g, int lo, int hi,
-                          const Waiter &w) {
-    using C = Cfg<D>;
-    auto query = [&](int i) {
-        if (t[i].live)
-            load_rows<D>(smem + C::kOffQ + (uint32_t)i * C::kTile, &p.q_map, p.a.hd, t[i].head, u.begin + t[i].p0, kRows,
-                         su32(&c.q_full[i]));
-    };
-    query(0);
-    int nk = 0, nv = 0;
-    for (int b = hi - 1; b >= lo; --b) {
-        const int s = nk % C::kStages;
-        const uint32_t parity = (uint32_t)(((nk / C::kStages) & 1) ^ 1);
-        if (!wait(su32(&c.k_empty[s]), parity, w)) break;
-        load_rows<D>(smem + C::kOffK + (uint32_t)s * C::kTile, &p.k_map, p.a.hd, g, u.begin + kRows * b, kRows,
-                     su32(&c.k_full[s]));
-        ++nk;
-        if (b == hi - 1) query(1);
-        if (!wait(su32(&c.v_empty[s]), parity, w)) break;
-        load_rows<D>(smem + C::kOffV + (uint32_t)s * C::kTile, &p.v_map, p.a.hd, g, u.begin + kRows * b, kRows,
-                     su32(&c.v_full[s]));
-        ++nv;
-    }
-    // Copies still landing must finish before the block exits.
-    for (int i = 0; i < 2; ++i)
-        if (t[i].live) drain(su32(&c.q_full[i]), 0, w);
-    for (int q = nk > C::kStages ? nk - C::kStages : 0; q < nk; ++q)
-        drain(su32(&c.k_full[q % C::kStages]), (uint32_t)((q / C::kStages) & 1), w);
-    for (int q = nv > C::kStages ? nv - C::kStages : 0; q < nv; ++q)
-        drain(su32(&c.v_full[q % C::kStages]), (uint32_t)((q / C::kStages) & 1), w);
-}
-
-// The products of tile i; returns early when aborting.  Iteration b: PV of key block b + 1, then S of block b.  The two
-// tiles' warps take turns iteration by iteration: one's products then run while the other's scores are in the softmax,
-// where without turns both would share the tensor core evenly and wait for their scores together.
-template <int D>
-__device__ __forceinline__ void issue_products(const FwdArgs &p, Ctl &c, uint32_t smem, uint32_t tmem, int seq_end,
-                                               int first, int end, int lo, int hi, int i, int lane, const Waiter &w) {
-    using C = Cfg<D>;
-    int done = 0;  // products PV issued
-    int ks = 0, vs = 0;
-    uint32_t kph = 0, vph = 0;
-    const uint32_t o_col = tmem + kColO + 128u * i, s_col = tmem + kColS + 128u * i;
-    const uint64_t qd = desc_k(smem + C::kOffQ + (uint32_t)i * C::kTile);
-    if (first < end && !wait_warp(su32(&c.q_full[i]), 0, w)) return;
-    uint32_t it = 0;
-    for (int b = hi - 1; b >= lo - 1; --b, ++it) {
-        const bool more = b >= lo, prev = b + 1 < hi;
-        const bool pv = b + 1 >= first && b + 1 < end, sc = b >= first && b < end;
-        // The operands first: a wait costs about 100 cycles even for what is there, and these pass while the softmax works.
-        if (more && !wait_warp(su32(&c.k_full[ks]), kph, w)) return;
-        const uint32_t v = smem + C::kOffV + (uint32_t)vs * C::kTile;
-        if (prev) {
-            if (!wait_warp(su32(&c.v_full[vs]), vph, w)) return;
-            const int keys = seq_end - kRows * (b + 1);
-            if (i == 0 && keys < kRows) zero_rows(v, keys, kRows, C::kHalves, lane);  // before the first turn that reads it
-        }
-        if ((i == 1 || it > 0) && !wait_warp(su32(&c.turn[i]), (it + (uint32_t)i - 1u) & 1u, w)) return;
-        if (pv && !wait_warp(su32(&c.p_ready[i]), (uint32_t)(done & 1), w)) return;
-        tc_after();
-        if (elect_one()) {
-            if (pv) {
-                const uint64_t vd = desc_mn(v, kHalf, 1024u);
-#pragma unroll
-                for (int k = 0; k < 8; ++k)  // A: 8 columns (16 keys) per step, 32 keys every 32; B: two groups of 8 keys
-                    tc_mma_f16_ts(o_col, s_col + 32u * (k / 2) + 8u * (k % 2), vd + 128u * k, p.idesc2, done > 0 || k > 0);
-                if (b + 1 == first) tc_commit_to(su32(&c.o_full[i]));
-            }
-            if (prev) tc_commit_to(su32(&c.v_empty[vs]));
-            if (sc) {
-                const uint64_t kd = desc_k(smem + C::kOffK + (uint32_t)ks * C::kTile);
-#pragma unroll
-                for (int k = 0; k < D / 16; ++k) {  // +32 bytes of each row, then the next half
-                    const uint64_t step = 2u * (k % 4) + (uint64_t)(k / 4) * (kHalf >> 4);
-                    tc_mma_f16(s_col, qd + step, kd + step, p.idesc1, k > 0);
-                }
-                tc_commit_to(su32(&c.s_full[i]));
-            }
-            if (more) tc_commit_to(su32(&c.k_empty[ks]));
-            bar_arrive(su32(&c.turn[i ^ 1]));
+// The walking warp: this block's unit, then those of blocks that have not started, handed to the other warps through two
+// slots.  The next is asked for when the loading warp comes to its last key block: early enough to be there when it is
+// wanted, late enough that the last units go to the blocks that are free first.
+__device__ __forceinline__ void role_walk(const FwdArgs &p, Ctl &c, int lane, const Waiter &w) {
+    const unsigned pairs = p.pair_heads ? p.a.nh / 2 : p.a.nh;
+    unsigned index = blockIdx.x;
+    uint32_t asked = 0;
+    UnitCursor cur;
+    auto next = [&]() {
+        __syncwarp();
+        if (lane == 0) {
+            bar_expect_tx(su32(&c.answered), 16);
+            take_block(su32(&c.answer), su32(&c.answered));
         }
         __syncwarp();
-        if (pv) ++done;
-        if (prev && ++vs == C::kStages) vs = 0, vph ^= 1u;
-        if (more && ++ks == C::kStages) ks = 0, kph ^= 1u;
+        drain(su32(&c.answered), asked++ & 1u, w);
+        __syncwarp();
+        return taken_block(su32(&c.answer), index);
+    };
+    bool found = true;
+    for (uint32_t k = 0;; ++k) {
+        Unit u{};
+        for (; found; found = next()) {  // units behind the last one are passed over
+            if (index == 0)
+                for (int i = lane; i < p.a.seqs; i += 32) check_offsets(p.a, i, &g_fwd_error_word);
+            u = next_unit(p.a, index / pairs, p.pair_heads ? 7 : 8, true, cur);
+            if (u.live) break;
+        }
+        const uint32_t slot = k & 1u;
+        if (!wait_warp(su32(&c.work_empty[slot]), ((k >> 1) & 1u) ^ 1u, w)) return;
+        if (lane == 0) {
+            c.work[slot] = Work{u, (int)(index % pairs), !found};
+            bar_arrive(su32(&c.work_full[slot]));
+        }
+        __syncwarp();
+        if (!found || !wait_warp(su32(&c.want), k & 1u, w)) return;
+        found = next();
+    }
+}
+
+// A unit as the other warps see it: its tiles and the key blocks [lo, hi) of both.
+struct Job {
+    Unit u;
+    Tile t[2];
+    int g, lo, hi;
+};
+__device__ __forceinline__ void read_job(const FwdArgs &p, const Ctl &c, uint32_t k, Job &job) {
+    const Work x = c.work[k & 1u];
+    job.u = x.u;
+    job.t[0] = tile_of(p, x.u, x.pair, 0), job.t[1] = tile_of(p, x.u, x.pair, 1);
+    job.g = job.t[0].head / p.a.hpk;
+    // Tile 0 is never empty; with an empty tile 1 its range is empty too.
+    job.lo = job.t[1].live && job.t[1].lo < job.t[0].lo ? job.t[1].lo : job.t[0].lo;
+    job.hi = job.t[1].hi > job.t[0].hi ? job.t[1].hi : job.t[0].hi;
+}
+// The k-th unit of this block is there: false when there is none (or when aborting).
+__device__ __forceinline__ bool job_there(Ctl &c, uint32_t k, const Waiter &w) {
+    return wait_warp(su32(&c.work_full[k & 1u]), (k >> 1) & 1u, w) && !c.work[k & 1u].stop;
+}
+__device__ __forceinline__ void job_taken(Ctl &c, uint32_t k, int lane) {
+    __syncwarp();
+    if (lane == 0) bar_arrive(su32(&c.work_empty[k & 1u]));
+}
+__device__ __forceinline__ bool next_job(const FwdArgs &p, Ctl &c, uint32_t k, int lane, Job &job, const Waiter &w) {
+    if (!job_there(c, k, w)) return false;
+    read_job(p, c, k, job);
+    job_taken(c, k, lane);
+    return true;
+}
+
+// The loading warp (lane 0): what a unit's first products need first (K, Q_0, Q_1, V; the
+// unit before may still read Q), then K and V of block after block.
+template <int D>
+__device__ void role_load(const FwdArgs &p, Ctl &c, uint32_t smem, int lane, const Waiter &w) {
+    using C = Cfg<D>;
+    int nk = 0, nv = 0, nq[2] = {0, 0};
+    bool ok = true;
+    Job job;
+    for (uint32_t k = 0; ok && next_job(p, c, k, lane, job, w); ++k) {
+        if (lane == 0 && job.u.pad) bar_arrive(su32(&c.want));
+        if (lane == 0 && !job.u.pad) {
+            auto query = [&](int i) {
+                const Tile &t = job.t[i];
+                if (!t.live) return true;
+                if (!wait(su32(&c.q_empty[i]), (uint32_t)((nq[i] & 1) ^ 1), w)) return false;
+                load_rows<D>(smem + C::kOffQ + (uint32_t)i * C::kTile, &p.q_map, p.a.hd, t.head, job.u.begin + t.p0, kRows,
+                             su32(&c.q_full[i]));
+                ++nq[i];
+                return true;
+            };
+            for (int b = job.hi - 1; ok && b >= job.lo; --b) {
+                if (b == job.lo) bar_arrive(su32(&c.want));
+                const int sk = nk % C::kStages, row = job.u.begin + kRows * b;
+                ok = wait(su32(&c.k_empty[sk]), (uint32_t)(((nk / C::kStages) & 1) ^ 1), w);
+                if (!ok) break;
+                load_rows<D>(smem + C::kOffK + (uint32_t)sk * C::kTile, &p.k_map, p.a.hd, job.g, row, kRows,
+                             su32(&c.k_full[sk]));
+                ++nk;
+                ok = b != job.hi - 1 || (query(0) && query(1));
+                if (!ok) break;
+                const int sv = nv % C::kStages;
+                ok = wait(su32(&c.v_empty[sv]), (uint32_t)(((nv / C::kStages) & 1) ^ 1), w);
+                if (!ok) break;
+                load_rows<D>(smem + C::kOffV + (uint32_t)sv * C::kTile, &p.v_map, p.a.hd, job.g, row, kRows,
+                             su32(&c.v_full[sv]));
+                ++nv;
+            }
+        }
+        ok = __all_sync(0xffffffffu, ok) != 0;
+    }
+    if (lane == 0) {  // copies still landing must finish before the block exits
+        for (int i = 0; i < 2; ++i)
+            if (nq[i]) drain(su32(&c.q_full[i]), (uint32_t)((nq[i] - 1) & 1), w);
+        for (int q = nk > C::kStages ? nk - C::kStages : 0; q < nk; ++q)
+            drain(su32(&c.k_full[q % C::kStages]), (uint32_t)((q / C::kStages) & 1), w);
+        for (int q = nv > C::kStages ? nv - C::kStages : 0; q < nv; ++q)
+            drain(su32(&c.v_full[q % C::kStages]), (uint32_t)((q / C::kStages) & 1), w);
+    }
+    __syncwarp();
+}
+
+// The products of tile i, unit after unit; returns when there are no more or when aborting.  Iteration b: PV of key block
+// b + 1, then S of block b.  The two tiles' warps take turns iteration by iteration: one's products then run while the
+// other's scores are in the softmax, where without turns both would share the tensor core evenly and wait for their
+// scores together.
+template <int D>
+__device__ __forceinline__ void issue_products(const FwdArgs &p, Ctl &c, uint32_t smem, uint32_t tmem, int i, int lane,
+                                               const Waiter &w) {
+    using C = Cfg<D>;
+    int ks = 0, vs = 0;
+    uint32_t kph = 0, vph = 0;
+    uint32_t done = 0, live_units = 0, it = 0;  // products PV issued, units with this tile, turns: over all units
+    const uint32_t o_col = tmem + kColO + 128u * i, s_col = tmem + kColS + 128u * i;
+    const uint64_t qd = desc_k(smem + C::kOffQ + (uint32_t)i * C::kTile);
+    Job job;
+    for (uint32_t k = 0; next_job(p, c, k, lane, job, w); ++k) {
+        if (job.u.pad) continue;  // nothing attends
+        const Tile own = i ? job.t[1] : job.t[0];
+        const int first = uniform(own.lo), end = uniform(own.hi), lo = uniform(job.lo), hi = uniform(job.hi);
+        const int seq_end = uniform(job.u.len);
+        const bool has = first < end;
+        if (has && !wait_warp(su32(&c.q_full[i]), live_units & 1u, w)) return;
+        bool fresh = true;  // no PV of this unit yet
+        for (int b = hi - 1; b >= lo - 1; --b, ++it) {
+            const bool more = b >= lo, prev = b + 1 < hi;
+            const bool pv = b + 1 >= first && b + 1 < end, sc = b >= first && b < end;
+            // The operands first: a wait costs about 100 cycles even for what is there, and these pass while the softmax
+            // works.
+            if (more && !wait_warp(su32(&c.k_full[ks]), kph, w)) return;
+            const uint32_t v = smem + C::kOffV + (uint32_t)vs * C::kTile;
+            if (prev) {
+                if (!wait_warp(su32(&c.v_full[vs]), vph, w)) return;
+                const int keys = seq_end - kRows * (b + 1);
+                if (i == 0 && keys < kRows) zero_rows(v, keys, kRows, C::kHalves, lane);  // before the first turn that reads it
+            }
+            // O of the unit before is out of tensor memory.
+            if (pv && fresh && !wait_warp(su32(&c.o_empty[i]), (live_units & 1u) ^ 1u, w)) return;
+            if ((i == 1 || it > 0) && !wait_warp(su32(&c.turn[i]), (it + (uint32_t)i - 1u) & 1u, w)) return;
+            if (pv && !wait_warp(su32(&c.p_ready[i]), done & 1u, w)) return;
+            tc_after();
+            if (elect_one()) {
+                if (pv) {
+                    const uint64_t vd = desc_mn(v, kHalf, 1024u);
+#pragma unroll
+                    for (int x = 0; x < 8; ++x)  // A: 8 columns (16 keys) per step, 32 keys every 32; B: two groups of 8 keys
+                        tc_mma_f16_ts(o_col, s_col + 32u * (x / 2) + 8u * (x % 2), vd + 128u * x, p.idesc2, !fresh || x > 0);
+                    if (b + 1 == first) tc_commit_to(su32(&c.o_full[i]));
+                }
+                if (prev) tc_commit_to(su32(&c.v_empty[vs]));
+                if (sc) {
+                    const uint64_t kd = desc_k(smem + C::kOffK + (uint32_t)ks * C::kTile);
+#pragma unroll
+                    for (int x = 0; x < D / 16; ++x) {  // +32 bytes of each row, then the next half
+                        const uint64_t step = 2u * (x % 4) + (uint64_t)(x / 4) * (kHalf >> 4);
+                        tc_mma_f16(s_col, qd + step, kd + step, p.idesc1, x > 0);
+                    }
+                    tc_commit_to(su32(&c.s_full[i]));
+                    if (b == first) tc_commit_to(su32(&c.q_empty[i]));
+                }
+                if (more) tc_commit_to(su32(&c.k_empty[ks]));
+                bar_arrive(su32(&c.turn[i ^ 1]));
+            }
+            __syncwarp();
+            if (pv) ++done, fresh = false;
+            if (prev && ++vs == C::kStages) vs = 0, vph ^= 1u;
+            if (more && ++ks == C::kStages) ks = 0, kph ^= 1u;
+        }
+        if (has) ++live_units;
     }
 }
 
@@ -236,132 +349,14 @@ __device__ __forceinline__ bool any_of_quad(bool x, int id) {
     return r != 0;
 }
 
-// The softmax of both tiles, one after the other for each key block.  `xch`: shared floats [2][4][32] of this warp's
-// rows (two turns, four quarters of a row).
+// Rows [r0, r0 + 32) of a tile, columns [c0, c1), row by row over the attended keys, by one warp: where a masked value is
+// not finite.
 template <int D, bool F16>
-__device__ void role_soft(const FwdArgs &p, Ctl &c, uint32_t smem, uint32_t tmem, const Unit &u, const Tile (&t)[2],
-                          int lo, int hi, int warp, int lane, float *xch, const Waiter &w) {
-    using C = Cfg<D>;
-    const int quad = warp & 3, part = warp >> 2;
-    const uint32_t lane_tm = (uint32_t)(32 * quad) << 16;
-    const float cs = p.a.scale * 1.4426950408889634f;
-    float used[2] = {-INFINITY, -INFINITY}, top[2] = {-INFINITY, -INFINITY};  // the maximum that scales, this quarter's own
-    float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-    int it[2] = {0, 0}, turn = 0;
-    float others[3];
-    auto meet = [&](float mine) {  // the other quarters' values of this row
-        float *x = xch + 128 * turn;
-        turn ^= 1;
-        x[32 * part + lane] = mine;
-        asm volatile("bar.sync %0, 128;" ::"r"(1 + quad) : "memory");
-#pragma unroll
-        for (int z = 0; z < 3; ++z) others[z] = x[32 * ((part + 1 + z) & 3) + lane];
-    };
-    for (int b = hi - 1; b >= lo; --b) {
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            if (b < t[i].lo || b >= t[i].hi) continue;
-            if (!wait_warp(su32(&c.s_full[i]), (uint32_t)(it[i] & 1), w)) return;
-            tc_after();
-            const uint32_t s_tm = tmem + lane_tm + kColS + 128u * i + 32u * part;  // P: 16 columns over this warp's scores
-            const int base = kRows * b + 32 * part;
-            uint32_t v[32];
-            tc_ld_32x32(s_tm, v);
-            tc_wait_ld(v);
-            if (!(base + 31 <= t[i].p0 && (p.a.window == 0 || t[i].p0 + kRows - 1 < base + p.a.window))) {
-                const int pos = t[i].p0 + 32 * quad + lane;
-                mask32(v, p.a.window > 0 ? pos - p.a.window + 1 - base : 0, pos - base);
-            }
-            const float m = max32(v, -INFINITY);
-            top[i] = fmaxf(top[i], m);
-            uint32_t pk[16];
-            float2 part_sum = make_float2(0.f, 0.f);
-            auto probs = [&] {
-                part_sum = make_float2(0.f, 0.f);
-                exp32<F16>(v, cs, (used[i] == -INFINITY ? 0.f : used[i] * cs) - (F16 ? kShift16 : 0.f), part_sum, pk);
-            };
-            // P with the maximum in use, before it is known whether that still does: the four warps' answers then meet
-            // at a barrier that the exponentials have covered.
-            bool far = it[i] == 0;
-            if (!far) {
-                probs();
-                far = any_of_quad((m - used[i]) * cs > kLag, 1 + quad);
-            }
-            if (far) {
-                float now = fmaxf(m, used[i]);
-                meet(now);
-                now = fmaxf(fmaxf(now, others[0]), fmaxf(others[1], others[2]));
-                if (it[i] > 0) {  // before the first product O holds nothing
-                    const float keep = now == -INFINITY ? 1.f : fast_exp2((used[i] - now) * cs);
-                    const uint32_t o_tm = tmem + lane_tm + kColO + 128u * i + (uint32_t)(D / 4) * part;
-                    sum[i].x *= keep, sum[i].y *= keep;
-#pragma unroll 1
-                    for (int k = 0; k < D / 4; k += 16) {  // S of this block is behind PV of the last: O is complete
-                        uint32_t o[16];
-                        tc_ld_32x16(o_tm + k, o);
-#pragma unroll
-                        for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * keep);
-                        tc_st_32x16(o_tm + k, o);
-                    }
-                }
-                used[i] = now;
-                probs();
-            }
-            sum[i] = __fadd2_rn(sum[i], part_sum);
-            tc_st_32x16(s_tm, pk);
-            tc_wait_st();
-            tc_before();
-            __syncwarp();
-            if (lane == 0) bar_arrive(su32(&c.p_ready[i]));
-            ++it[i];
-        }
-    }
-    float total[2];
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        meet(top[i]);
-        top[i] = fmaxf(fmaxf(top[i], others[0]), fmaxf(others[1], others[2]));
-        total[i] = sum[i].x + sum[i].y;
-        meet(total[i]);
-        // In the quarters' order, whichever this warp has: the four warps get the same sum.
-        const float a[4] = {total[i], others[0], others[1], others[2]};
-        total[i] = (a[(4 - part) & 3] + a[(5 - part) & 3]) + (a[(6 - part) & 3] + a[(7 - part) & 3]);
-    }
-    // Now warps 0-7 finish tile 0 and 8-15 tile 1, D / 2 columns each: O rows through this warp's part of the Q tile,
-    // read by then.
-    const int i = warp >> 3, half = (warp >> 2) & 1;
-    const Tile own = i ? t[1] : t[0];
-    if (!own.live) return;
-    const float all = i ? total[1] : total[0], was = i ? used[1] : used[0], best = i ? top[1] : top[0];
-    const bool row_live = 32 * quad + lane < own.live;
-    const int64_t row0 = (int64_t)u.begin + own.p0 + 32 * quad;
-    if (row_live && half == 0) {
-        // The sum is relative to the maximum in use; LSE wants it relative to the true one.
-        const float ln2 = 0.6931471805599453f;
-        const float l = logf(all) - ((best - was) * cs + (F16 ? kShift16 : 0.f)) * ln2;
-        float *st = p.a.lse + ((row0 + lane) * p.a.nh + own.head) * 2;
-        st[0] = best * p.a.scale, st[1] = l;
-    }
-    const float inv = 1.0f / all;
-    if (!wait_warp(su32(&c.o_full[i]), 0, w)) return;
-    tc_after();
-    constexpr int W = D / 2;
-    const bool good = store_rows<W, F16>(tmem + lane_tm + kColO + 128u * i + (uint32_t)W * half,
-                                         smem + C::kOffQ + (uint32_t)i * C::kTile + (uint32_t)(warp & 7) * (C::kTile / 8),
-                                         inv, &p.o_map, static_cast<uint16_t *>(p.a.out), p.a.nh, p.a.hd, own.head, row0,
-                                         W * half, own.live - 32 * quad, lane);
-    if (__any_sync(0xffffffffu, row_live && !good) && lane == 0) c.bad[i] = 1;
-    if (lane == 0) stores_read();
-    __syncwarp();
-}
-
-// A tile row by row over the attended keys, one warp per row: for tiles where a masked value is not finite.
-template <int D, bool F16>
-__device__ __noinline__ void recompute(const Args &a, const Unit &u, const Tile &t, int g) {
+__device__ __noinline__ void recompute(const Args &a, const Unit &u, const Tile &t, int g, int r0, int c0, int c1) {
     using T = typename std::conditional<F16, __half, __nv_bfloat16>::type;
     constexpr int N = D / 32;
-    const int lane = threadIdx.x & 31, warps = blockDim.x >> 5;
-    for (int r = threadIdx.x >> 5; r < t.live; r += warps) {
+    const int lane = threadIdx.x & 31;
+    for (int r = r0; r < t.live && r < r0 + 32; ++r) {
         const int pos = t.p0 + r;
         const int64_t row = (int64_t)u.begin + pos;
         const T *q = static_cast<const T *>(a.q) + row * a.qs + (int64_t)t.head * a.hd;
@@ -390,11 +385,182 @@ __device__ __noinline__ void recompute(const Args &a, const Unit &u, const Tile 
         }
         T *o = static_cast<T *>(a.out) + (row * a.nh + t.head) * a.hd;
 #pragma unroll
-        for (int i = 0; i < N; ++i)
-            if (lane + 32 * i < a.hd) o[lane + 32 * i] = from_f<T>(acc[i] / l);
-        if (lane == 0) {
+        for (int i = 0; i < N; ++i) {
+            const int d = lane + 32 * i;
+            if (d >= c0 && d < c1 && d < a.hd) o[d] = from_f<T>(acc[i] / l);
+        }
+        if (c0 == 0 && lane == 0) {
             float *st = a.lse + (row * a.nh + t.head) * 2;
             st[0] = m, st[1] = logf(l);
+        }
+    }
+}
+
+// 32 columns of a row, packed two per word, to `dst`: 32 bytes a store where rows allow it, so that every sector of a
+// thread's line is written whole.  `cols` of the columns exist (a multiple of 8).
+__device__ __forceinline__ void store32(uint16_t *dst, const uint32_t (&o)[32], int cols, bool wide) {
+    if (wide && cols >= 32) {
+#pragma unroll
+        for (int k = 0; k < 16; k += 8)
+            asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst + 2 * k), "r"(o[k]),
+                         "r"(o[k + 1]), "r"(o[k + 2]), "r"(o[k + 3]), "r"(o[k + 4]), "r"(o[k + 5]), "r"(o[k + 6]),
+                         "r"(o[k + 7])
+                         : "memory");
+        return;
+    }
+#pragma unroll
+    for (int k = 0; k < 16; k += 4)
+        if (2 * k < cols) *reinterpret_cast<uint4 *>(dst + 2 * k) = make_uint4(o[k], o[k + 1], o[k + 2], o[k + 3]);
+}
+
+// The softmax of both tiles, one after the other for each key block, unit after unit.  `xch`: shared floats [2][4][32] of
+// this warp's rows (two turns, four quarters of a row).
+template <int D, bool F16>
+__device__ void role_soft(const FwdArgs &p, Ctl &c, uint32_t tmem, int warp, int lane, float *xch, const Waiter &w) {
+    constexpr int W = D / 2;
+    const int quad = warp & 3, part = warp >> 2;
+    const uint32_t lane_tm = (uint32_t)(32 * quad) << 16;
+    const float cs = p.a.scale * 1.4426950408889634f;
+    uint32_t seen[2] = {0, 0}, ended = 0;  // scores and outputs taken, over all units
+    int turn = 0;
+    float others[3];
+    auto meet = [&](float mine) {  // the other quarters' values of this row
+        float *x = xch + 128 * turn;
+        turn ^= 1;
+        x[32 * part + lane] = mine;
+        asm volatile("bar.sync %0, 128;" ::"r"(1 + quad) : "memory");
+#pragma unroll
+        for (int z = 0; z < 3; ++z) others[z] = x[32 * ((part + 1 + z) & 3) + lane];
+    };
+    Job job;
+    for (uint32_t k = 0; job_there(c, k, w); ++k) {
+        read_job(p, c, k, job);
+        const Unit &u = job.u;
+        const Tile (&t)[2] = job.t;
+        if (u.pad) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+                for (int r = warp; r < t[i].live; r += kSoftWarps) {
+                    const int64_t at = ((int64_t)u.begin + t[i].p0 + r) * p.a.nh + t[i].head;
+                    for (int d = lane; d < p.a.hd; d += 32) static_cast<uint16_t *>(p.a.out)[at * p.a.hd + d] = 0;
+                    if (lane == 0) p.a.lse[2 * at] = 0.f, p.a.lse[2 * at + 1] = INFINITY;
+                }
+            job_taken(c, k, lane);
+            continue;
+        }
+        float used[2] = {-INFINITY, -INFINITY}, top[2] = {-INFINITY, -INFINITY};  // the maximum that scales, this quarter's own
+        float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+        bool begun[2] = {false, false};
+        for (int b = job.hi - 1; b >= job.lo; --b) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                if (b < t[i].lo || b >= t[i].hi) continue;
+                if (!wait_warp(su32(&c.s_full[i]), seen[i] & 1u, w)) return;
+                tc_after();
+                const uint32_t s_tm = tmem + lane_tm + kColS + 128u * i + 32u * part;  // P: 16 columns over this warp's scores
+                const int base = kRows * b + 32 * part;
+                uint32_t v[32];
+                tc_ld_32x32(s_tm, v);
+                tc_wait_ld(v);
+                if (!(base + 31 <= t[i].p0 && (p.a.window == 0 || t[i].p0 + kRows - 1 < base + p.a.window))) {
+                    const int pos = t[i].p0 + 32 * quad + lane;
+                    mask32(v, p.a.window > 0 ? pos - p.a.window + 1 - base : 0, pos - base);
+                }
+                const float m = max32(v, -INFINITY);
+                top[i] = fmaxf(top[i], m);
+                uint32_t pk[16];
+                float2 part_sum = make_float2(0.f, 0.f);
+                auto probs = [&] {
+                    part_sum = make_float2(0.f, 0.f);
+                    exp32<F16>(v, cs, (used[i] == -INFINITY ? 0.f : used[i] * cs) - (F16 ? kShift16 : 0.f), part_sum, pk);
+                };
+                // P with the maximum in use, before it is known whether that still does: the four warps' answers then meet
+                // at a barrier that the exponentials have covered.
+                bool far = !begun[i];
+                if (!far) {
+                    probs();
+                    far = any_of_quad((m - used[i]) * cs > kLag, 1 + quad);
+                }
+                if (far) {
+                    float now = fmaxf(m, used[i]);
+                    meet(now);
+                    now = fmaxf(fmaxf(now, others[0]), fmaxf(others[1], others[2]));
+                    if (begun[i]) {  // before the first product O holds nothing
+                        const float keep = now == -INFINITY ? 1.f : fast_exp2((used[i] - now) * cs);
+                        const uint32_t o_tm = tmem + lane_tm + kColO + 128u * i + (uint32_t)(D / 4) * part;
+                        sum[i].x *= keep, sum[i].y *= keep;
+#pragma unroll 1
+                        for (int k = 0; k < D / 4; k += 16) {  // S of this block is behind PV of the last: O is complete
+                            uint32_t o[16];
+                            tc_ld_32x16(o_tm + k, o);
+#pragma unroll
+                            for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * keep);
+                            tc_st_32x16(o_tm + k, o);
+                        }
+                    }
+                    used[i] = now;
+                    probs();
+                }
+                sum[i] = __fadd2_rn(sum[i], part_sum);
+                tc_st_32x16(s_tm, pk);
+                tc_wait_st();
+                tc_before();
+                __syncwarp();
+                if (lane == 0) bar_arrive(su32(&c.p_ready[i]));
+                ++seen[i];
+                begun[i] = true;
+            }
+        }
+        float total[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            meet(top[i]);
+            top[i] = fmaxf(fmaxf(top[i], others[0]), fmaxf(others[1], others[2]));
+            total[i] = sum[i].x + sum[i].y;
+            meet(total[i]);
+            // In the quarters' order, whichever this warp has: the four warps get the same sum.
+            const float a[4] = {total[i], others[0], others[1], others[2]};
+            total[i] = (a[(4 - part) & 3] + a[(5 - part) & 3]) + (a[(6 - part) & 3] + a[(7 - part) & 3]);
+        }
+        read_job(p, c, k, job);  // once more: the loop above has no registers for all of it
+        job_taken(c, k, lane);
+        // Now warps 0-7 finish tile 0 and 8-15 tile 1, D / 2 columns each, a row per thread.
+        const int i = warp >> 3, half = (warp >> 2) & 1;
+        const Tile own = i ? t[1] : t[0];
+        if (!own.live) continue;
+        const float all = i ? total[1] : total[0], was = i ? used[1] : used[0], best = i ? top[1] : top[0];
+        const bool row_live = 32 * quad + lane < own.live;
+        const int64_t row = (int64_t)u.begin + own.p0 + 32 * quad + lane;
+        if (row_live && half == 0) {
+            // The sum is relative to the maximum in use; LSE wants it relative to the true one.
+            const float ln2 = 0.6931471805599453f;
+            const float l = logf(all) - ((best - was) * cs + (F16 ? kShift16 : 0.f)) * ln2;
+            float *st = p.a.lse + (row * p.a.nh + own.head) * 2;
+            st[0] = best * p.a.scale, st[1] = l;
+        }
+        const float inv = 1.0f / all;
+        if (!wait_warp(su32(&c.o_full[i]), ended & 1u, w)) return;
+        ++ended;
+        tc_after();
+        float2 odd = make_float2(0.f, 0.f);  // 0 as long as every value is finite
+        uint16_t *out = static_cast<uint16_t *>(p.a.out) + (row * p.a.nh + own.head) * p.a.hd + W * half;
+        uint32_t o[W / 32][32];
+#pragma unroll
+        for (int x = 0; x < W / 32; ++x) {
+            tc_ld_32x32(tmem + lane_tm + kColO + 128u * i + (uint32_t)(W * half + 32 * x), o[x]);
+            tc_wait_ld(o[x]);
+            scale_pack<F16>(o[x], inv, odd);
+        }
+        tc_before();  // O is read: the next unit's products may overwrite it
+        __syncwarp();
+        if (lane == 0) bar_arrive(su32(&c.o_empty[i]));
+        if (row_live)
+#pragma unroll
+            for (int x = 0; x < W / 32; ++x)
+                store32(out + 32 * x, o[x], p.a.hd - W * half - 32 * x, p.wide != 0);
+        if (__any_sync(0xffffffffu, row_live && !(odd.x + odd.y == 0.f))) {
+            __syncwarp();
+            recompute<D, F16>(p.a, u, own, job.g, 32 * quad, W * half, W * half + W);
         }
     }
 }
@@ -407,6 +573,8 @@ __global__ void __launch_bounds__(kThreads, 1) forward_tc_kernel(const __grid_co
     Ctl &c = *reinterpret_cast<Ctl *>(smem_raw + (smem - su32(smem_raw)));
     const int warp = uniform((int)(threadIdx.x >> 5)), lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
+        bar_init(su32(&c.answered), 1);
+        bar_init(su32(&c.want), 1);
         c.abort_flag = 0;
     } else if (warp == 0) {
         if (lane <= 4) {
@@ -416,16 +584,20 @@ __global__ void __launch_bounds__(kThreads, 1) forward_tc_kernel(const __grid_co
             bar_init(su32(&c.v_full[lane - 5]), 1);
             bar_init(su32(&c.v_empty[lane - 5]), 2);
         } else if (lane <= 10) {
-            bar_init(su32(&c.q_full[lane - 9]), 1);
-            bar_init(su32(&c.s_full[lane - 9]), 1);
-            bar_init(su32(&c.p_ready[lane - 9]), kSoftWarps);
-            bar_init(su32(&c.o_full[lane - 9]), 1);
-            bar_init(su32(&c.turn[lane - 9]), 1);
-            bar_init(su32(&c.mma_done[lane - 9]), 1);
-            c.bad[lane - 9] = 0;
+            const int i = lane - 9;
+            bar_init(su32(&c.q_full[i]), 1);
+            bar_init(su32(&c.q_empty[i]), 1);
+            bar_init(su32(&c.s_full[i]), 1);
+            bar_init(su32(&c.p_ready[i]), kSoftWarps);
+            bar_init(su32(&c.o_full[i]), 1);
+            bar_init(su32(&c.o_empty[i]), kSoftWarps / 2);
+            bar_init(su32(&c.turn[i]), 1);
+            bar_init(su32(&c.mma_done[i]), 1);
+            bar_init(su32(&c.work_full[i]), 1);
+            bar_init(su32(&c.work_empty[i]), kWalkers);
         }
-    } else if (threadIdx.x < 36) {
-        const CUtensorMap *m = lane == 0 ? &p.q_map : lane == 1 ? &p.k_map : lane == 2 ? &p.v_map : &p.o_map;
+    } else if (threadIdx.x < 35) {
+        const CUtensorMap *m = lane == 0 ? &p.q_map : lane == 1 ? &p.k_map : &p.v_map;
         asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(m)) : "memory");
     }
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -436,53 +608,25 @@ __global__ void __launch_bounds__(kThreads, 1) forward_tc_kernel(const __grid_co
     const uint32_t tmem = c.tmem_base;
     grid_begin();
 
-    const unsigned pairs = p.pair_heads ? p.a.nh / 2 : p.a.nh;
-    const int pair = (int)(blockIdx.x % pairs);
-    const Unit u = find_unit(p.a, blockIdx.x / pairs, p.pair_heads ? 7 : 8, true, blockIdx.x == 0,
-                             &g_fwd_error_word);
-    const Waiter w{&c.abort_flag, &g_fwd_error_word};
-    if (u.live) {
-        const Tile t[2] = {tile_of(p, u, pair, 0), tile_of(p, u, pair, 1)};
-        const int g = t[0].head / p.a.hpk;
-        if (u.pad) {
-#pragma unroll
-            for (int i = 0; i < 2; ++i)
-                for (int r = warp; r < t[i].live; r += kThreads / 32) {
-                    const int64_t at = ((int64_t)u.begin + t[i].p0 + r) * p.a.nh + t[i].head;
-                    for (int d = lane; d < p.a.hd; d += 32) static_cast<uint16_t *>(p.a.out)[at * p.a.hd + d] = 0;
-                    if (lane == 0) p.a.lse[2 * at] = 0.f, p.a.lse[2 * at + 1] = INFINITY;
-                }
-        } else {
-            // Tile 0 is never empty; with an empty tile 1 its range is empty too.
-            const int lo = t[1].live && t[1].lo < t[0].lo ? t[1].lo : t[0].lo;
-            const int hi = t[1].hi > t[0].hi ? t[1].hi : t[0].hi;
-            if (warp < kSoftWarps) {
-                float *xch = reinterpret_cast<float *>(reinterpret_cast<uint8_t *>(&c) + 1024) + 256 * (warp & 3);
-                role_soft<D, F16>(p, c, smem, tmem, u, t, lo, hi, warp, lane, xch, w);
-            } else if (warp < kLoadWarp) {
-                const int i = warp - kMmaWarp;
-                const Tile own = i ? t[1] : t[0];
-                issue_products<D>(p, c, uniform(smem), uniform(tmem), uniform(u.len), uniform(own.lo), uniform(own.hi),
-                                  uniform(lo), uniform(hi), i, lane, w);
-                if (elect_one()) tc_commit_to(su32(&c.mma_done[i]));  // nothing may still run when tensor memory is released
-                drain(su32(&c.mma_done[i]), 0, w);
-                __syncwarp();
-            } else {
-                if (lane == 0) role_load<D>(p, c, smem, u, t, g, lo, hi, w);
-                __syncwarp();
-            }
-            tc_before();
-            __syncthreads();
-            tc_after();
-            if (!c.abort_flag && (c.bad[0] || c.bad[1])) {
-                if (lane == 0) stores_done();
-                __syncthreads();
-                if (c.bad[0]) recompute<D, F16>(p.a, u, t[0], g);
-                if (c.bad[1]) recompute<D, F16>(p.a, u, t[1], g);
-            }
-        }
+    // A warp that recomputes its rows keeps the others waiting, for a time that grows with the sequence.
+    const Waiter w{&c.abort_flag, &g_fwd_error_word, kWaitLimitNs + (uint64_t)p.a.tokens * 20000u};
+    if (warp < kSoftWarps) {
+        float *xch = reinterpret_cast<float *>(reinterpret_cast<uint8_t *>(&c) + 1024) + 256 * (warp & 3);
+        role_soft<D, F16>(p, c, tmem, warp, lane, xch, w);
+    } else if (warp < kLoadWarp) {
+        const int i = warp - kMmaWarp;
+        issue_products<D>(p, c, uniform(smem), uniform(tmem), i, lane, w);
+        if (elect_one()) tc_commit_to(su32(&c.mma_done[i]));  // nothing may still run when tensor memory is released
+        drain(su32(&c.mma_done[i]), 0, w);
+        __syncwarp();
+    } else if (warp == kLoadWarp) {
+        role_load<D>(p, c, smem, lane, w);
+    } else {
+        role_walk(p, c, lane, w);
     }
+    tc_before();
     __syncthreads();
+    tc_after();
     if (warp == kMmaWarp) tc_dealloc(tmem, 512);
 }
 
@@ -498,13 +642,13 @@ int forward_tc(const Args &a, const mha_packed_params *p, int dtype, cudaStream_
     FwdArgs q{};
     q.a = a;
     q.pair_heads = a.hpk % 2 == 0;
+    q.wide = a.hd % 16 == 0 && reinterpret_cast<uintptr_t>(a.out) % 32 == 0;
     const int D = a.hd <= 64 ? 64 : 128;
     q.idesc1 = instr_desc(dtype, kRows, kRows, false);
     q.idesc2 = instr_desc(dtype, kRows, D, true);
     if (!encode_rows(&q.q_map, a.q, a.tokens, a.nh, a.hd, a.qs, kRows) ||
         !encode_rows(&q.k_map, a.k, a.tokens, a.nkv, a.hd, a.ks, kRows) ||
-        !encode_rows(&q.v_map, a.v, a.tokens, a.nkv, a.hd, a.vs, kRows) ||
-        !encode_store(&q.o_map, a.out, a.tokens, a.nh, a.hd, D / 2))
+        !encode_rows(&q.v_map, a.v, a.tokens, a.nkv, a.hd, a.vs, kRows))
         return DGRAD_ERR_UNSUPPORTED;
     const int64_t blocks = q.pair_heads ? unit_bound(p, kRows) * (a.nh / 2) : unit_bound(p, 2 * kRows) * a.nh;
     const bool f16 = dtype == DGRAD_F16;

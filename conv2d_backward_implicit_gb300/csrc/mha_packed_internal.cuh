@@ -112,6 +112,34 @@ __device__ __forceinline__ unsigned scan32(unsigned x, int lane) {  // inclusive
     }
     return x;
 }
+// The same by one warp, for a block that takes units one after another: `cur` stays where the last one was.
+struct UnitCursor {
+    int chunk = 0;         // 32 segments
+    unsigned before = 0;   // tiles in the chunks before
+};
+__device__ __forceinline__ Unit next_unit(const Args &a, unsigned u, int shift, bool down, UnitCursor &cur) {
+    const int lane = threadIdx.x & 31, n = a.seqs + 2, round = (1 << shift) - 1;
+    if (u < cur.before) cur = UnitCursor{};
+    Unit x{};
+    for (; cur.chunk * 32 < n; ++cur.chunk) {
+        int begin = 0, len = 0;
+        if (cur.chunk * 32 + lane < n) segment(a, cur.chunk * 32 + lane, begin, len);
+        const unsigned tiles = ((unsigned)len + round) >> shift, incl = cur.before + scan32(tiles, lane);
+        const unsigned hit = __ballot_sync(0xffffffffu, u >= incl - tiles && u < incl);
+        if (hit) {
+            const int at = __ffs(hit) - 1;
+            x.live = true;
+            x.begin = __shfl_sync(0xffffffffu, begin, at);
+            x.len = __shfl_sync(0xffffffffu, len, at);
+            const unsigned k = u - __shfl_sync(0xffffffffu, incl - tiles, at), m = __shfl_sync(0xffffffffu, tiles, at);
+            x.p0 = (int)((down ? m - 1 - k : k) << shift);
+            x.pad = cur.chunk * 32 + at >= a.seqs;
+            return x;
+        }
+        cur.before = __shfl_sync(0xffffffffu, incl, 31);
+    }
+    return x;
+}
 __device__ __forceinline__ Unit find_unit(const Args &a, unsigned u, int shift, bool down, bool check, unsigned *error,
                                           Lookup &s) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, n = a.seqs + 2, round = (1 << shift) - 1;

@@ -21,14 +21,15 @@ constexpr uint64_t kWaitLimitNs = 2000000000ull;  // 2 s: far beyond any step of
 struct Waiter {
     volatile int *abort_flag;
     unsigned *error;
+    uint64_t limit_ns = kWaitLimitNs;
 };
 __device__ __noinline__ bool wait_long(uint32_t bar, uint32_t parity, Waiter w, bool honour_abort) {
     const uint64_t t0 = now_ns();
-    const uint64_t max_spins = kWaitLimitNs / 16 + (1u << 20);
+    const uint64_t max_spins = w.limit_ns / 16 + (1u << 20);
     for (uint64_t spin = 1;; ++spin) {
         if (bar_try(bar, parity)) return true;
         if (honour_abort && *w.abort_flag) return false;
-        if (((spin & 31u) == 0 && now_ns() - t0 > kWaitLimitNs) || spin > max_spins) {
+        if (((spin & 31u) == 0 && now_ns() - t0 > w.limit_ns) || spin > max_spins) {
             *w.abort_flag = 1;
             atomicOr(w.error, kErrTimeout);
             return false;
@@ -120,6 +121,28 @@ __device__ __forceinline__ void zero_rows(uint32_t tile, int from, int rows, int
             sts128(tile + (uint32_t)(h * rows + r) * 128u + (uint32_t)(lane & 7) * 16u, 0, 0, 0, 0);
     fence_async_proxy();
     __syncwarp();
+}
+
+// Asks for a block of this grid that has not started, to do its work in this one: 16 bytes at `answer`, counted by `bar`.
+__device__ __forceinline__ void take_block(uint32_t answer, uint32_t bar) {
+    asm volatile("clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(
+                     answer),
+                 "r"(bar)
+                 : "memory");
+}
+// The answer: whether there was one, and its index.
+__device__ __forceinline__ bool taken_block(uint32_t answer, unsigned &index) {
+    uint32_t ok, x;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b128 r;\n\tld.shared.b128 r, [%2];\n\t"
+        "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, r;\n\tselp.u32 %1, 1, 0, p;\n\tmov.u32 %0, 0;\n\t"
+        "@p clusterlaunchcontrol.query_cancel.get_first_ctaid.v4.b32.b128 {%0, _, _, _}, r;\n\t}"
+        : "=r"(x), "=r"(ok)
+        : "r"(answer)
+        : "memory");
+    fence_async_proxy();  // read before the next request writes it
+    index = x;
+    return ok != 0;
 }
 
 inline PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {

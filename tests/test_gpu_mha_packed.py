@@ -295,6 +295,47 @@ def test_many_short_sequences(dg, parity_log):
     check_backward(dg, p, dg.DGRAD_KERNEL_TC, parity_log, "1200 sequences")
 
 
+@pytest.mark.parametrize("H,G,window", [(8, 2, 0), (3, 3, 70)])
+def test_more_tiles_than_blocks_run_at_once(dg, H, G, window, parity_log):
+    """Each block takes one tile after another, of all lengths, with padding among them; fp16's tiles are whole again after
+    one with values that are not finite."""
+    lens = [(53 * i) % 260 for i in range(200)]
+    p = Problem(lens, H, G, 128, dtype="f16", seed=12, window=window, head=300, tail=200, fused=True)
+    assert sum(-(-n // 256) for n in lens) * H > 3 * 152
+    check_forward(dg, p, dg.DGRAD_KERNEL_TC, parity_log, f"tiles in a row {H}/{G}")
+    for name in ("k", "v"):
+        x = getattr(p, name)
+        x[p.offsets[7::9][:8], 0, 3] = float("inf")   # the first position of some sequences: every query attends it
+        x[[p.offsets[i + 1] - 1 for i in range(4, 200, 11) if lens[i] > 1], -1, 5] = float("nan")  # their last alone does
+    o, _ = run_forward(dg, p)
+    qkv = p.f64("q", "k", "v")
+    with np.errstate(all="ignore"):
+        ref, _ = om.forward(*qkv, p.offsets, window)
+    clean = [np.nan_to_num(x, nan=0, posinf=0, neginf=0) for x in qkv]
+    bound, _ = om.forward_bounds(*clean, p.offsets, window, U["f16"], OUT["f16"], TINY["f16"])
+    got, rows = o.double().cpu().numpy(), np.isfinite(ref).all(axis=2)  # what attends no such value
+    assert (np.abs(got - ref)[rows] <= 2 * bound[rows] + 1e-6).all()
+    assert (np.isnan(got) | np.isinf(got))[~np.isfinite(ref)].all()
+
+
+def test_two_streams_at_once(dg):
+    """Two forwards in flight together, each taking tiles of its own grid alone."""
+    p = [Problem([(31 * i) % 400 for i in range(90)], 8, 2, 64, dtype="bf16", seed=21 + j) for j in range(2)]
+    alone = [run_forward(dg, x) for x in p]
+    code = dg.DTYPE_CODE["bf16"]
+    streams = [torch.cuda.Stream() for _ in p]
+    sets = [(to_gpu(x), torch.tensor(x.offsets, dtype=torch.int32, device="cuda"), torch.empty_like(o), torch.empty_like(l))
+            for x, (o, l) in zip(p, alone)]
+    torch.cuda.synchronize()
+    for _ in range(3):
+        for x, s, (qkv, off, o, l) in zip(p, streams, sets):
+            dg.mha_packed_forward(*qkv, off, o, l, x.params(dg), code, s)
+    torch.cuda.synchronize()
+    assert dg.mha_packed_check_errors() == 0
+    for (a, b), (_, _, o, l) in zip(alone, sets):
+        assert torch.equal(a, o) and torch.equal(b, l)
+
+
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 def test_results_repeat_and_follow_the_stream(dg, dtype):
     p = problem("ragged", dtype)
