@@ -26,20 +26,26 @@
 //     softmax does.  A warp's products run in order, so S may overwrite P behind PV; two
 //     warps, because a warp's waits otherwise stand between its products (2850 cycles per
 //     key block with one warp, of which 850 were waits).
-//   * warp 18 (one thread): TMA copies of the Q tiles, K and V.
-//   * warp 19: the walk.  The grid has a block per unit, longest first; a running block takes over the units of blocks
-//     that have not started, so tensor memory, barriers and the search for the first unit are paid once per SM, and the
-//     next unit's loads and first products run under the last one's end (118 us -> 104 us on the documents below).
+//   * warp 18: the TMA copies, and the units.  The grid has a block per unit, longest first;
+//     a running block takes over the units of blocks that have not started.  Tensor memory,
+//     barriers and the first search are then paid once per SM, and the next unit's loads
+//     and first scores run under the last one's end.
+//   * warps 19-22: O and LSE of a unit's tiles, from the sums that the softmax warps leave in
+//     shared memory, while those begin the next unit.  The documents below: 118 us with a
+//     block per unit; 104 with units taken over; 98 with warps of their own for O.
 // V rows past the sequence's end are zeroed in shared memory (other sequences' rows,
 // possibly with infinities); what is masked inside the sequence has P = 0, and if a
 // value there is not finite the product with 0 leaves a NaN in O: those rows are then
 // recomputed one by one over the attended keys alone.
-// Measured (bf16, head_dim 128): one sequence of 16384, 8 heads over 2: 330 us, 1666
-// TFLOP/s, 86% of a burst of large products; ten documents of 0 to 2048 tokens, 32 heads
-// over 8: 104 us, 1000 TFLOP/s.  A key block (both tiles) takes 2,650 cycles, products
+// Measured (bf16, head_dim 128): one sequence of 16384, 8 heads over 2: 327 us, 1680
+// TFLOP/s, 87% of a burst of large products; ten documents of 0 to 2048 tokens, 32 heads
+// over 8: 98 us, 1060 TFLOP/s.  A key block (both tiles) takes 2,620 cycles, products
 // 2,048 of them: the time from a tile's scores to its P (1,150) is what the other tile's
-// products (1,024) do not cover.  A block's start takes 5,000 to 8,000 cycles more, and each
-// unit's end 7,000: the warps of a row meet, O leaves.
+// products (1,024) do not cover.  A block's start takes 5,000 to 8,000 cycles more, and a
+// unit about 5,000: its first scores, and O of the tile before, which takes 2,600 a tile
+// and which its first products wait for.  O goes straight from registers, 32 bytes a store:
+// boxes staged in shared memory for TMA stores measured 102 us, all of O packed in
+// registers before its first store spilled.
 // Every wait is bounded; on timeout the kernel raises its error word, lets the copies
 // and products in flight finish, frees tensor memory and returns.
 #include "mha_packed_tc.cuh"
@@ -62,19 +68,26 @@ constexpr int kRows = 128;                     // queries per tile, keys per ste
 constexpr uint32_t kHalf = kRows * 128;        // bytes of a [128][64] 16-bit half tile
 constexpr int kSoftWarps = 16, kMmaWarp = 16, kLoadWarp = 18;  // 16, 17: one for each tile
 constexpr uint32_t kColS = 0, kColO = 256;     // + 128 i, + 128 i
-constexpr int kWalkWarp = 19, kThreads = 32 * (kWalkWarp + 1);
-constexpr int kWalkers = kWalkWarp;            // warps that take units from the walk
+constexpr int kOutWarp = 19, kOutWarps = 4;
+constexpr int kThreads = 32 * (kOutWarp + kOutWarps);
+constexpr int kTakers = kOutWarp + kOutWarps - 1;  // all but the loading warp, which hands out the units
 constexpr float kLag = 8.0f;                   // log2 of how far the scaling maximum may lag
 constexpr float kShift16 = 7.0f;               // log2 of fp16's scale of P: P <= 2^15, and 7 more bits below
+
+// A tile's rows when its last key block is through the softmax, for the warps that bring O out.
+struct Sums {
+    float top[4][kRows], sum[4][kRows];  // of each quarter of the keys: the maximum, the sum
+    float used[kRows];                   // the maximum that scales P, O and the sum
+};
 
 template <int D>
 struct Cfg {
     static constexpr int kHalves = D / 64;
     static constexpr uint32_t kTile = kHalf * kHalves;
     static constexpr int kStages = D == 64 ? 4 : 2;
-    static constexpr uint32_t kOffQ = 5120, kOffK = kOffQ + 2 * kTile, kOffV = kOffK + kStages * kTile;
+    static constexpr uint32_t kOffX = 1024, kOffSums = kOffX + 4096, kOffQ = kOffSums + 9 * 1024, kOffK = kOffQ + 2 * kTile, kOffV = kOffK + kStages * kTile;
     static constexpr uint32_t kSmem = 1024 + kOffV + kStages * kTile;  // + 1 KB alignment slack
-    static_assert(kOffQ % 1024 == 0, "operand tiles must be 1 KB aligned");
+    static_assert(2 * sizeof(Sums) <= kOffQ - kOffSums && kOffQ % 1024 == 0, "operand tiles must be 1 KB aligned");
     static_assert(kSmem + 1024 <= 232448, "shared memory over the per-block limit");
 };
 
@@ -93,8 +106,8 @@ struct Work {
 struct Ctl {
     uint4 answer;  // of the request for another block
     uint64_t q_full[2], q_empty[2], k_full[4], k_empty[4], v_full[4], v_empty[4];
-    uint64_t s_full[2], p_ready[2], o_full[2], o_empty[2], turn[2], mma_done[2];
-    uint64_t work_full[2], work_empty[2], want, answered;
+    uint64_t s_full[2], p_ready[2], o_full[2], o_empty[2], sums_full[2], sums_empty[2], turn[2], mma_done[2];
+    uint64_t work_full[2], work_empty[2], answered;
     Work work[2];
     uint32_t tmem_base;
     int abort_flag;
@@ -118,60 +131,22 @@ __device__ __forceinline__ Tile tile_of(const FwdArgs &p, const Unit &u, int pai
     return t;
 }
 
-// The walking warp: this block's unit, then those of blocks that have not started, handed to the other warps through two
-// slots.  The next is asked for when the loading warp comes to its last key block: early enough to be there when it is
-// wanted, late enough that the last units go to the blocks that are free first.
-__device__ __forceinline__ void role_walk(const FwdArgs &p, Ctl &c, int lane, const Waiter &w) {
-    const unsigned pairs = p.pair_heads ? p.a.nh / 2 : p.a.nh;
-    unsigned index = blockIdx.x;
-    uint32_t asked = 0;
-    UnitCursor cur;
-    auto next = [&]() {
-        __syncwarp();
-        if (lane == 0) {
-            bar_expect_tx(su32(&c.answered), 16);
-            take_block(su32(&c.answer), su32(&c.answered));
-        }
-        __syncwarp();
-        drain(su32(&c.answered), asked++ & 1u, w);
-        __syncwarp();
-        return taken_block(su32(&c.answer), index);
-    };
-    bool found = true;
-    for (uint32_t k = 0;; ++k) {
-        Unit u{};
-        for (; found; found = next()) {  // units behind the last one are passed over
-            if (index == 0)
-                for (int i = lane; i < p.a.seqs; i += 32) check_offsets(p.a, i, &g_fwd_error_word);
-            u = next_unit(p.a, index / pairs, p.pair_heads ? 7 : 8, true, cur);
-            if (u.live) break;
-        }
-        const uint32_t slot = k & 1u;
-        if (!wait_warp(su32(&c.work_empty[slot]), ((k >> 1) & 1u) ^ 1u, w)) return;
-        if (lane == 0) {
-            c.work[slot] = Work{u, (int)(index % pairs), !found};
-            bar_arrive(su32(&c.work_full[slot]));
-        }
-        __syncwarp();
-        if (!found || !wait_warp(su32(&c.want), k & 1u, w)) return;
-        found = next();
-    }
-}
-
 // A unit as the other warps see it: its tiles and the key blocks [lo, hi) of both.
 struct Job {
     Unit u;
     Tile t[2];
     int g, lo, hi;
 };
-__device__ __forceinline__ void read_job(const FwdArgs &p, const Ctl &c, uint32_t k, Job &job) {
-    const Work x = c.work[k & 1u];
+__device__ __forceinline__ void set_job(const FwdArgs &p, const Work &x, Job &job) {
     job.u = x.u;
     job.t[0] = tile_of(p, x.u, x.pair, 0), job.t[1] = tile_of(p, x.u, x.pair, 1);
     job.g = job.t[0].head / p.a.hpk;
     // Tile 0 is never empty; with an empty tile 1 its range is empty too.
     job.lo = job.t[1].live && job.t[1].lo < job.t[0].lo ? job.t[1].lo : job.t[0].lo;
     job.hi = job.t[1].hi > job.t[0].hi ? job.t[1].hi : job.t[0].hi;
+}
+__device__ __forceinline__ void read_job(const FwdArgs &p, const Ctl &c, uint32_t k, Job &job) {
+    set_job(p, c.work[k & 1u], job);
 }
 // The k-th unit of this block is there: false when there is none (or when aborting).
 __device__ __forceinline__ bool job_there(Ctl &c, uint32_t k, const Waiter &w) {
@@ -188,47 +163,104 @@ __device__ __forceinline__ bool next_job(const FwdArgs &p, Ctl &c, uint32_t k, i
     return true;
 }
 
-// The loading warp (lane 0): what a unit's first products need first (K, Q_0, Q_1, V; the
-// unit before may still read Q), then K and V of block after block.
+// The loading warp.  It finds this block's unit, then those of blocks that have not started, and hands them to the other
+// warps through two slots.  Lane 0 loads what a unit's first products need first (K, Q_0, Q_1, V; the unit before may still
+// read Q), then K and V of block after block.  The next unit is asked for shortly before the last key block: early enough to
+// be there when it is wanted, late enough that the last units go to the blocks that are free first.
 template <int D>
 __device__ void role_load(const FwdArgs &p, Ctl &c, uint32_t smem, int lane, const Waiter &w) {
     using C = Cfg<D>;
+    const unsigned pairs = p.pair_heads ? p.a.nh / 2 : p.a.nh;
+    unsigned index = blockIdx.x;
+    uint32_t asked = 0, told = 0;
+    UnitCursor cur;
     int nk = 0, nv = 0, nq[2] = {0, 0};
+    auto ask = [&] {
+        if (lane == 0) {
+            bar_expect_tx(su32(&c.answered), 16);
+            take_block(su32(&c.answer), su32(&c.answered));
+        }
+        ++asked;
+    };
+    auto answer = [&] {
+        __syncwarp();
+        drain(su32(&c.answered), told++ & 1u, w);
+        __syncwarp();
+        const bool yes = taken_block(su32(&c.answer), index);
+        __syncwarp();
+        return yes;
+    };
+    // The unit of `index`, or of the first block taken over that has one: units behind the last one are passed over.
+    auto find = [&](bool found) {
+        Unit u{};
+        while (found) {
+            if (index == 0)
+                for (int i = lane; i < p.a.seqs; i += 32) check_offsets(p.a, i, &g_fwd_error_word);
+            u = next_unit(p.a, index / pairs, p.pair_heads ? 7 : 8, true, cur);
+            if (u.live) break;
+            ask();
+            found = answer();
+        }
+        return u;
+    };
     bool ok = true;
-    Job job;
-    for (uint32_t k = 0; ok && next_job(p, c, k, lane, job, w); ++k) {
-        if (lane == 0 && job.u.pad) bar_arrive(su32(&c.want));
-        if (lane == 0 && !job.u.pad) {
-            auto query = [&](int i) {
-                const Tile &t = job.t[i];
-                if (!t.live) return true;
-                if (!wait(su32(&c.q_empty[i]), (uint32_t)((nq[i] & 1) ^ 1), w)) return false;
-                load_rows<D>(smem + C::kOffQ + (uint32_t)i * C::kTile, &p.q_map, p.a.hd, t.head, job.u.begin + t.p0, kRows,
+    Unit u = find(true);
+    for (uint32_t k = 0; ok; ++k) {
+        const Work x{u, (int)(index % pairs), !u.live};
+        if (!wait_warp(su32(&c.work_empty[k & 1u]), ((k >> 1) & 1u) ^ 1u, w)) break;
+        if (lane == 0) {
+            c.work[k & 1u] = x;
+            bar_arrive(su32(&c.work_full[k & 1u]));
+        }
+        __syncwarp();
+        if (x.stop) break;
+        if (x.u.pad) {
+            ask();
+            u = find(answer());
+            continue;
+        }
+        Job job;
+        set_job(p, x, job);
+        auto query = [&](int i) {
+            const Tile &t = job.t[i];
+            if (!t.live) return true;
+            if (!wait_warp(su32(&c.q_empty[i]), (uint32_t)((nq[i] & 1) ^ 1), w)) return false;
+            if (lane == 0)
+                load_rows<D>(smem + C::kOffQ + (uint32_t)i * C::kTile, &p.q_map, p.a.hd, t.head, x.u.begin + t.p0, kRows,
                              su32(&c.q_full[i]));
-                ++nq[i];
-                return true;
-            };
-            for (int b = job.hi - 1; ok && b >= job.lo; --b) {
-                if (b == job.lo) bar_arrive(su32(&c.want));
-                const int sk = nk % C::kStages, row = job.u.begin + kRows * b;
-                ok = wait(su32(&c.k_empty[sk]), (uint32_t)(((nk / C::kStages) & 1) ^ 1), w);
-                if (!ok) break;
+            ++nq[i];
+            return true;
+        };
+        for (int b = job.hi - 1; b >= job.lo; --b) {
+            if (b == job.lo + 1 || job.hi - job.lo == 1) ask();
+            const int sk = nk % C::kStages, row = x.u.begin + kRows * b;
+            ok = wait_warp(su32(&c.k_empty[sk]), (uint32_t)(((nk / C::kStages) & 1) ^ 1), w);
+            if (!ok) break;
+            if (lane == 0)
                 load_rows<D>(smem + C::kOffK + (uint32_t)sk * C::kTile, &p.k_map, p.a.hd, job.g, row, kRows,
                              su32(&c.k_full[sk]));
-                ++nk;
-                ok = b != job.hi - 1 || (query(0) && query(1));
-                if (!ok) break;
-                const int sv = nv % C::kStages;
-                ok = wait(su32(&c.v_empty[sv]), (uint32_t)(((nv / C::kStages) & 1) ^ 1), w);
-                if (!ok) break;
+            ++nk;
+            ok = b != job.hi - 1 || (query(0) && query(1));
+            if (!ok) break;
+            if (b == job.lo) {  // while the place of V is not free
+                u = find(answer());
+                if (u.live && !u.pad && lane < 2) {
+                    const Tile t = tile_of(p, u, (int)(index % pairs), lane);
+                    if (t.live) prefetch_rows<D>(&p.q_map, p.a.hd, t.head, u.begin + t.p0);
+                }
+            }
+            const int sv = nv % C::kStages;
+            ok = wait_warp(su32(&c.v_empty[sv]), (uint32_t)(((nv / C::kStages) & 1) ^ 1), w);
+            if (!ok) break;
+            if (lane == 0)
                 load_rows<D>(smem + C::kOffV + (uint32_t)sv * C::kTile, &p.v_map, p.a.hd, job.g, row, kRows,
                              su32(&c.v_full[sv]));
-                ++nv;
-            }
+            ++nv;
         }
-        ok = __all_sync(0xffffffffu, ok) != 0;
     }
-    if (lane == 0) {  // copies still landing must finish before the block exits
+    // What was asked for is written to this block's memory, and copies still landing must finish before the block exits.
+    if (asked != told) drain(su32(&c.answered), told & 1u, w);
+    if (lane == 0) {
         for (int i = 0; i < 2; ++i)
             if (nq[i]) drain(su32(&c.q_full[i]), (uint32_t)((nq[i] - 1) & 1), w);
         for (int q = nk > C::kStages ? nk - C::kStages : 0; q < nk; ++q)
@@ -349,10 +381,9 @@ __device__ __forceinline__ bool any_of_quad(bool x, int id) {
     return r != 0;
 }
 
-// Rows [r0, r0 + 32) of a tile, columns [c0, c1), row by row over the attended keys, by one warp: where a masked value is
-// not finite.
+// Rows [r0, r0 + 32) of a tile, row by row over the attended keys, by one warp: where a masked value is not finite.
 template <int D, bool F16>
-__device__ __noinline__ void recompute(const Args &a, const Unit &u, const Tile &t, int g, int r0, int c0, int c1) {
+__device__ __noinline__ void recompute(const Args &a, const Unit &u, const Tile &t, int g, int r0) {
     using T = typename std::conditional<F16, __half, __nv_bfloat16>::type;
     constexpr int N = D / 32;
     const int lane = threadIdx.x & 31;
@@ -387,9 +418,9 @@ __device__ __noinline__ void recompute(const Args &a, const Unit &u, const Tile 
 #pragma unroll
         for (int i = 0; i < N; ++i) {
             const int d = lane + 32 * i;
-            if (d >= c0 && d < c1 && d < a.hd) o[d] = from_f<T>(acc[i] / l);
+            if (d < a.hd) o[d] = from_f<T>(acc[i] / l);
         }
-        if (c0 == 0 && lane == 0) {
+        if (lane == 0) {
             float *st = a.lse + (row * a.nh + t.head) * 2;
             st[0] = m, st[1] = logf(l);
         }
@@ -416,12 +447,12 @@ __device__ __forceinline__ void store32(uint16_t *dst, const uint32_t (&o)[32], 
 // The softmax of both tiles, one after the other for each key block, unit after unit.  `xch`: shared floats [2][4][32] of
 // this warp's rows (two turns, four quarters of a row).
 template <int D, bool F16>
-__device__ void role_soft(const FwdArgs &p, Ctl &c, uint32_t tmem, int warp, int lane, float *xch, const Waiter &w) {
-    constexpr int W = D / 2;
+__device__ void role_soft(const FwdArgs &p, Ctl &c, uint32_t tmem, int warp, int lane, float *xch, Sums *sums,
+                          const Waiter &w) {
     const int quad = warp & 3, part = warp >> 2;
     const uint32_t lane_tm = (uint32_t)(32 * quad) << 16;
     const float cs = p.a.scale * 1.4426950408889634f;
-    uint32_t seen[2] = {0, 0}, ended = 0;  // scores and outputs taken, over all units
+    uint32_t seen[2] = {0, 0}, ended[2] = {0, 0};  // scores taken and tiles ended, over all units
     int turn = 0;
     float others[3];
     auto meet = [&](float mine) {  // the other quarters' values of this row
@@ -449,7 +480,7 @@ __device__ void role_soft(const FwdArgs &p, Ctl &c, uint32_t tmem, int warp, int
             continue;
         }
         float used[2] = {-INFINITY, -INFINITY}, top[2] = {-INFINITY, -INFINITY};  // the maximum that scales, this quarter's own
-        float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+        float sum[2] = {0.f, 0.f};
         bool begun[2] = {false, false};
         for (int b = job.hi - 1; b >= job.lo; --b) {
 #pragma unroll
@@ -460,12 +491,15 @@ __device__ void role_soft(const FwdArgs &p, Ctl &c, uint32_t tmem, int warp, int
                 const uint32_t s_tm = tmem + lane_tm + kColS + 128u * i + 32u * part;  // P: 16 columns over this warp's scores
                 const int base = kRows * b + 32 * part;
                 uint32_t v[32];
-                tc_ld_32x32(s_tm, v);
-                tc_wait_ld(v);
-                if (!(base + 31 <= t[i].p0 && (p.a.window == 0 || t[i].p0 + kRows - 1 < base + p.a.window))) {
-                    const int pos = t[i].p0 + 32 * quad + lane;
-                    mask32(v, p.a.window > 0 ? pos - p.a.window + 1 - base : 0, pos - base);
-                }
+                auto scores = [&] {
+                    tc_ld_32x32(s_tm, v);
+                    tc_wait_ld(v);
+                    if (!(base + 31 <= t[i].p0 && (p.a.window == 0 || t[i].p0 + kRows - 1 < base + p.a.window))) {
+                        const int pos = t[i].p0 + 32 * quad + lane;
+                        mask32(v, p.a.window > 0 ? pos - p.a.window + 1 - base : 0, pos - base);
+                    }
+                };
+                scores();
                 const float m = max32(v, -INFINITY);
                 top[i] = fmaxf(top[i], m);
                 uint32_t pk[16];
@@ -488,7 +522,7 @@ __device__ void role_soft(const FwdArgs &p, Ctl &c, uint32_t tmem, int warp, int
                     if (begun[i]) {  // before the first product O holds nothing
                         const float keep = now == -INFINITY ? 1.f : fast_exp2((used[i] - now) * cs);
                         const uint32_t o_tm = tmem + lane_tm + kColO + 128u * i + (uint32_t)(D / 4) * part;
-                        sum[i].x *= keep, sum[i].y *= keep;
+                        sum[i] *= keep;
 #pragma unroll 1
                         for (int k = 0; k < D / 4; k += 16) {  // S of this block is behind PV of the last: O is complete
                             uint32_t o[16];
@@ -499,9 +533,10 @@ __device__ void role_soft(const FwdArgs &p, Ctl &c, uint32_t tmem, int warp, int
                         }
                     }
                     used[i] = now;
+                    scores();  // read again: registers for both scores and P would be too many
                     probs();
                 }
-                sum[i] = __fadd2_rn(sum[i], part_sum);
+                sum[i] += part_sum.x + part_sum.y;
                 tc_st_32x16(s_tm, pk);
                 tc_wait_st();
                 tc_before();
@@ -511,57 +546,79 @@ __device__ void role_soft(const FwdArgs &p, Ctl &c, uint32_t tmem, int warp, int
                 begun[i] = true;
             }
         }
-        float total[2];
+        job_taken(c, k, lane);
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-            meet(top[i]);
-            top[i] = fmaxf(fmaxf(top[i], others[0]), fmaxf(others[1], others[2]));
-            total[i] = sum[i].x + sum[i].y;
-            meet(total[i]);
-            // In the quarters' order, whichever this warp has: the four warps get the same sum.
-            const float a[4] = {total[i], others[0], others[1], others[2]};
-            total[i] = (a[(4 - part) & 3] + a[(5 - part) & 3]) + (a[(6 - part) & 3] + a[(7 - part) & 3]);
-        }
-        read_job(p, c, k, job);  // once more: the loop above has no registers for all of it
-        job_taken(c, k, lane);
-        // Now warps 0-7 finish tile 0 and 8-15 tile 1, D / 2 columns each, a row per thread.
-        const int i = warp >> 3, half = (warp >> 2) & 1;
-        const Tile own = i ? t[1] : t[0];
-        if (!own.live) continue;
-        const float all = i ? total[1] : total[0], was = i ? used[1] : used[0], best = i ? top[1] : top[0];
-        const bool row_live = 32 * quad + lane < own.live;
-        const int64_t row = (int64_t)u.begin + own.p0 + 32 * quad + lane;
-        if (row_live && half == 0) {
-            // The sum is relative to the maximum in use; LSE wants it relative to the true one.
-            const float ln2 = 0.6931471805599453f;
-            const float l = logf(all) - ((best - was) * cs + (F16 ? kShift16 : 0.f)) * ln2;
-            float *st = p.a.lse + (row * p.a.nh + own.head) * 2;
-            st[0] = best * p.a.scale, st[1] = l;
-        }
-        const float inv = 1.0f / all;
-        if (!wait_warp(su32(&c.o_full[i]), ended & 1u, w)) return;
-        ++ended;
-        tc_after();
-        float2 odd = make_float2(0.f, 0.f);  // 0 as long as every value is finite
-        uint16_t *out = static_cast<uint16_t *>(p.a.out) + (row * p.a.nh + own.head) * p.a.hd + W * half;
-        uint32_t o[W / 32][32];
-#pragma unroll
-        for (int x = 0; x < W / 32; ++x) {
-            tc_ld_32x32(tmem + lane_tm + kColO + 128u * i + (uint32_t)(W * half + 32 * x), o[x]);
-            tc_wait_ld(o[x]);
-            scale_pack<F16>(o[x], inv, odd);
-        }
-        tc_before();  // O is read: the next unit's products may overwrite it
-        __syncwarp();
-        if (lane == 0) bar_arrive(su32(&c.o_empty[i]));
-        if (row_live)
-#pragma unroll
-            for (int x = 0; x < W / 32; ++x)
-                store32(out + 32 * x, o[x], p.a.hd - W * half - 32 * x, p.wide != 0);
-        if (__any_sync(0xffffffffu, row_live && !(odd.x + odd.y == 0.f))) {
+            if (!begun[i]) continue;
+            if (!wait_warp(su32(&c.sums_empty[i]), (ended[i] & 1u) ^ 1u, w)) return;
+            Sums &z = sums[i];
+            z.top[part][32 * quad + lane] = top[i];
+            z.sum[part][32 * quad + lane] = sum[i];
+            if (part == 0) z.used[32 * quad + lane] = used[i];
             __syncwarp();
-            recompute<D, F16>(p.a, u, own, job.g, 32 * quad, W * half, W * half + W);
+            if (lane == 0) bar_arrive(su32(&c.sums_full[i]));
+            ++ended[i];
         }
+    }
+}
+
+// O and the statistics of tile 0, then of tile 1, a row per thread, while the softmax warps begin the next unit.
+template <int D, bool F16>
+__device__ void role_out(const FwdArgs &p, Ctl &c, uint32_t tmem, int quad, int lane, const Sums *sums,
+                         const Waiter &w) {
+    const uint32_t o_tm = tmem + ((uint32_t)(32 * quad) << 16) + kColO;
+    const int r = 32 * quad + lane;
+    const float cs = p.a.scale * 1.4426950408889634f;
+    uint32_t ended[2] = {0, 0};
+    Job job;
+    for (uint32_t k = 0; job_there(c, k, w); ++k) {
+        read_job(p, c, k, job);
+        if (!job.u.pad)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const Tile &t = job.t[i];
+                if (!t.live) continue;
+                if (!wait_warp(su32(&c.sums_full[i]), ended[i] & 1u, w)) return;
+                const Sums &z = sums[i];
+                const float all = (z.sum[0][r] + z.sum[1][r]) + (z.sum[2][r] + z.sum[3][r]), inv = 1.0f / all;
+                const float best = fmaxf(fmaxf(z.top[0][r], z.top[1][r]), fmaxf(z.top[2][r], z.top[3][r]));
+                const float used = z.used[r];
+                __syncwarp();
+                if (lane == 0) bar_arrive(su32(&c.sums_empty[i]));
+                if (!wait_warp(su32(&c.o_full[i]), ended[i]++ & 1u, w)) return;
+                tc_after();
+                const int64_t row0 = (int64_t)job.u.begin + t.p0 + 32 * quad;
+                float2 odd = make_float2(0.f, 0.f);  // 0 as long as every value is finite
+                const bool row_live = r < t.live;
+                uint16_t *out = static_cast<uint16_t *>(p.a.out) + ((row0 + lane) * p.a.nh + t.head) * p.a.hd;
+                uint32_t o[2][32];
+                tc_ld_32x32(o_tm + 128u * i, o[0]);
+#pragma unroll
+                for (int x = 0; x < D / 32; ++x) {
+                    tc_wait_ld(o[x & 1]);
+                    if (x + 1 < D / 32) {
+                        tc_ld_32x32(o_tm + 128u * i + 32u * (x + 1), o[(x + 1) & 1]);
+                    } else {  // O is read: the next unit's products may overwrite it
+                        tc_before();
+                        __syncwarp();
+                        if (lane == 0) bar_arrive(su32(&c.o_empty[i]));
+                    }
+                    scale_pack<F16>(o[x & 1], inv, odd);
+                    if (row_live) store32(out + 32 * x, o[x & 1], p.a.hd - 32 * x, p.wide != 0);
+                }
+                if (row_live) {
+                    // The sum is relative to the maximum in use; LSE wants it relative to the true one.
+                    const float ln2 = 0.6931471805599453f;
+                    float *st = p.a.lse + ((row0 + lane) * p.a.nh + t.head) * 2;
+                    st[0] = best * p.a.scale;
+                    st[1] = logf(all) - ((best - used) * cs + (F16 ? kShift16 : 0.f)) * ln2;
+                }
+                if (__any_sync(0xffffffffu, row_live && !(odd.x + odd.y == 0.f))) {
+                    __syncwarp();
+                    recompute<D, F16>(p.a, job.u, t, job.g, 32 * quad);
+                }
+            }
+        job_taken(c, k, lane);
     }
 }
 
@@ -574,7 +631,6 @@ __global__ void __launch_bounds__(kThreads, 1) forward_tc_kernel(const __grid_co
     const int warp = uniform((int)(threadIdx.x >> 5)), lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
         bar_init(su32(&c.answered), 1);
-        bar_init(su32(&c.want), 1);
         c.abort_flag = 0;
     } else if (warp == 0) {
         if (lane <= 4) {
@@ -590,11 +646,13 @@ __global__ void __launch_bounds__(kThreads, 1) forward_tc_kernel(const __grid_co
             bar_init(su32(&c.s_full[i]), 1);
             bar_init(su32(&c.p_ready[i]), kSoftWarps);
             bar_init(su32(&c.o_full[i]), 1);
-            bar_init(su32(&c.o_empty[i]), kSoftWarps / 2);
+            bar_init(su32(&c.o_empty[i]), kOutWarps);
             bar_init(su32(&c.turn[i]), 1);
             bar_init(su32(&c.mma_done[i]), 1);
             bar_init(su32(&c.work_full[i]), 1);
-            bar_init(su32(&c.work_empty[i]), kWalkers);
+            bar_init(su32(&c.work_empty[i]), kTakers);
+            bar_init(su32(&c.sums_full[i]), kSoftWarps);
+            bar_init(su32(&c.sums_empty[i]), kOutWarps);
         }
     } else if (threadIdx.x < 35) {
         const CUtensorMap *m = lane == 0 ? &p.q_map : lane == 1 ? &p.k_map : &p.v_map;
@@ -608,11 +666,11 @@ __global__ void __launch_bounds__(kThreads, 1) forward_tc_kernel(const __grid_co
     const uint32_t tmem = c.tmem_base;
     grid_begin();
 
-    // A warp that recomputes its rows keeps the others waiting, for a time that grows with the sequence.
-    const Waiter w{&c.abort_flag, &g_fwd_error_word, kWaitLimitNs + (uint64_t)p.a.tokens * 20000u};
+    Sums *sums = reinterpret_cast<Sums *>(reinterpret_cast<uint8_t *>(&c) + C::kOffSums);
+    const Waiter w{&c.abort_flag, &g_fwd_error_word, p.a.tokens};
     if (warp < kSoftWarps) {
-        float *xch = reinterpret_cast<float *>(reinterpret_cast<uint8_t *>(&c) + 1024) + 256 * (warp & 3);
-        role_soft<D, F16>(p, c, tmem, warp, lane, xch, w);
+        float *xch = reinterpret_cast<float *>(reinterpret_cast<uint8_t *>(&c) + C::kOffX) + 256 * (warp & 3);
+        role_soft<D, F16>(p, c, tmem, warp, lane, xch, sums, w);
     } else if (warp < kLoadWarp) {
         const int i = warp - kMmaWarp;
         issue_products<D>(p, c, uniform(smem), uniform(tmem), i, lane, w);
@@ -622,7 +680,7 @@ __global__ void __launch_bounds__(kThreads, 1) forward_tc_kernel(const __grid_co
     } else if (warp == kLoadWarp) {
         role_load<D>(p, c, smem, lane, w);
     } else {
-        role_walk(p, c, lane, w);
+        role_out<D, F16>(p, c, tmem, warp & 3, lane, sums, w);
     }
     tc_before();
     __syncthreads();

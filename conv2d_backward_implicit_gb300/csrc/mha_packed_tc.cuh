@@ -21,15 +21,15 @@ constexpr uint64_t kWaitLimitNs = 2000000000ull;  // 2 s: far beyond any step of
 struct Waiter {
     volatile int *abort_flag;
     unsigned *error;
-    uint64_t limit_ns = kWaitLimitNs;
+    int rows = 0;  // of a sequence that one warp may go through row by row while others wait, 20 us each
 };
 __device__ __noinline__ bool wait_long(uint32_t bar, uint32_t parity, Waiter w, bool honour_abort) {
     const uint64_t t0 = now_ns();
-    const uint64_t max_spins = w.limit_ns / 16 + (1u << 20);
+    const uint64_t limit_ns = kWaitLimitNs + (uint64_t)w.rows * 20000u, max_spins = limit_ns / 16 + (1u << 20);
     for (uint64_t spin = 1;; ++spin) {
         if (bar_try(bar, parity)) return true;
         if (honour_abort && *w.abort_flag) return false;
-        if (((spin & 31u) == 0 && now_ns() - t0 > w.limit_ns) || spin > max_spins) {
+        if (((spin & 31u) == 0 && now_ns() - t0 > limit_ns) || spin > max_spins) {
             *w.abort_flag = 1;
             atomicOr(w.error, kErrTimeout);
             return false;
@@ -185,6 +185,13 @@ __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap *map
         : "memory");
 }
 
+__device__ __forceinline__ void tma_prefetch_4d(const CUtensorMap *map, int x, int y, int z, int w) {
+    asm volatile("cp.async.bulk.prefetch.tensor.4d.L2.global.tile [%0, {%1, %2, %3, %4}];" ::"l"(
+                     reinterpret_cast<uint64_t>(map)),
+                 "r"(x), "r"(y), "r"(z), "r"(w)
+                 : "memory");
+}
+
 // One tile of D / 64 halves of `rows` rows through a map of encode_rows: one thread; `bar` counts its arrival and bytes.
 template <int D>
 __device__ __forceinline__ void load_rows(uint32_t dst, const CUtensorMap *map, int hd, int head, int token, int rows,
@@ -196,6 +203,13 @@ __device__ __forceinline__ void load_rows(uint32_t dst, const CUtensorMap *map, 
 #pragma unroll
         for (int h = 0; h < D / 64; ++h) tma_load_4d(dst + (uint32_t)(h * rows) * 128u, map, 64 * h, head, token, 0, bar);
     }
+}
+
+// The same tile to L2.
+template <int D>
+__device__ __forceinline__ void prefetch_rows(const CUtensorMap *map, int hd, int head, int token) {
+#pragma unroll
+    for (int h = 0; h < (D == 64 || hd == D ? 1 : D / 64); ++h) tma_prefetch_4d(map, D == 64 || hd == D ? 0 : 64 * h, head, token, 0);
 }
 
 // The same tensor for stores: boxes of 32 tokens x W elements of one head from rows of 2 W bytes, W = 64 (128-byte
