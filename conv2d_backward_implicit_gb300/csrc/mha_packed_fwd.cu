@@ -149,8 +149,10 @@ __device__ __forceinline__ void read_job(const FwdArgs &p, const Ctl &c, uint32_
     set_job(p, c.work[k & 1u], job);
 }
 // The k-th unit of this block is there: false when there is none (or when aborting).
+template <bool TOGETHER = false>
 __device__ __forceinline__ bool job_there(Ctl &c, uint32_t k, const Waiter &w) {
-    return wait_warp(su32(&c.work_full[k & 1u]), (k >> 1) & 1u, w) && !c.work[k & 1u].stop;
+    const uint32_t bar = su32(&c.work_full[k & 1u]), parity = (k >> 1) & 1u;
+    return (TOGETHER ? wait_together(bar, parity, w) : wait_warp(bar, parity, w)) && !c.work[k & 1u].stop;
 }
 __device__ __forceinline__ void job_taken(Ctl &c, uint32_t k, int lane) {
     __syncwarp();
@@ -464,7 +466,7 @@ __device__ void role_soft(const FwdArgs &p, Ctl &c, uint32_t tmem, int warp, int
         for (int z = 0; z < 3; ++z) others[z] = x[32 * ((part + 1 + z) & 3) + lane];
     };
     Job job;
-    for (uint32_t k = 0; job_there(c, k, w); ++k) {
+    for (uint32_t k = 0; job_there<true>(c, k, w); ++k) {
         read_job(p, c, k, job);
         const Unit &u = job.u;
         const Tile (&t)[2] = job.t;
@@ -486,7 +488,7 @@ __device__ void role_soft(const FwdArgs &p, Ctl &c, uint32_t tmem, int warp, int
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 if (b < t[i].lo || b >= t[i].hi) continue;
-                if (!wait_warp(su32(&c.s_full[i]), seen[i] & 1u, w)) return;
+                if (!wait_together(su32(&c.s_full[i]), seen[i] & 1u, w)) return;
                 tc_after();
                 const uint32_t s_tm = tmem + lane_tm + kColS + 128u * i + 32u * part;  // P: 16 columns over this warp's scores
                 const int base = kRows * b + 32 * part;
@@ -550,7 +552,7 @@ __device__ void role_soft(const FwdArgs &p, Ctl &c, uint32_t tmem, int warp, int
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             if (!begun[i]) continue;
-            if (!wait_warp(su32(&c.sums_empty[i]), (ended[i] & 1u) ^ 1u, w)) return;
+            if (!wait_together(su32(&c.sums_empty[i]), (ended[i] & 1u) ^ 1u, w)) return;
             Sums &z = sums[i];
             z.top[part][32 * quad + lane] = top[i];
             z.sum[part][32 * quad + lane] = sum[i];
